@@ -99,7 +99,12 @@ typedef enum {
    * q in 0..15, one (scale, min) pair of bf16 per 64 consecutive input-dim
    * elements, two codes per byte, the even element in the low nibble.
    * Bank layout: codes uint8 [E][N][K/2], scale and min bf16 [E][N][K/64]. */
-  MOE_Q4_AFFINE_G64 = 2
+  MOE_Q4_AFFINE_G64 = 2,
+  /* 8-bit floating point (e4m3) with one f32 scale per 128 x 128 block:
+   * w = scale * code, scales [E][ceil(N/128)][ceil(K/128)], codes uint8
+   * [E][N][K]. Banks of the moe_fp8_* calls only; the other calls answer it
+   * with MOE_ERR_INVALID_ARG. */
+  MOE_F8_E4M3_B128 = 3
 } moe_dtype_t;
 
 /* Expert-path selection for moe_layer_forward / moe_experts_forward. */
@@ -176,7 +181,13 @@ typedef enum {
   MOE_KERNEL_TC_DOWN = 9,       /* tensor-core grouped down x alpha */
   MOE_KERNEL_GATHER = 10,       /* packed-row gather of x (tensor-core path) */
   MOE_KERNEL_TC_ROUTER = 11,    /* tensor-core router contraction (T >= 128, bf16) */
-  MOE_KERNEL_DECODE = 12        /* single-launch decode kernel (MOE_PATH_FUSED) */
+  MOE_KERNEL_DECODE = 12,       /* single-launch decode kernel (MOE_PATH_FUSED) */
+  MOE_KERNEL_F8_QUANT = 13,     /* fp8 quantiser, also of packed rows */
+  MOE_KERNEL_F8_FEW_GATEUP = 14, /* fp8 gate/up + SwiGLU for a few tokens */
+  MOE_KERNEL_F8_FEW_DOWN = 15,  /* fp8 down + combine for a few tokens */
+  MOE_KERNEL_F8_TC_GATEUP = 16, /* fp8 grouped gate/up + SwiGLU on tcgen05 */
+  MOE_KERNEL_F8_TC_DOWN = 17,   /* fp8 grouped down on tcgen05 */
+  MOE_KERNEL_F8_MATMUL = 18     /* fp8 product (few rows, or tcgen05) */
 } moe_kernel_t;
 
 /* Returns the ABI version (MOE_ROUTE_ABI_VERSION). */
@@ -205,7 +216,9 @@ MOE_API moe_status_t moe_trace_kernel(int kernel, void* const* starts, void* con
                                       int n, int* count);
 
 /* Failure-detection self-test: the next launch of kernel family `kernel`
- * (MOE_KERNEL_TC_GATEUP, MOE_KERNEL_TC_DOWN or MOE_KERNEL_DECODE) waits on a
+ * (MOE_KERNEL_TC_GATEUP, MOE_KERNEL_TC_DOWN, MOE_KERNEL_DECODE,
+ * MOE_KERNEL_F8_TC_GATEUP, MOE_KERNEL_F8_TC_DOWN or MOE_KERNEL_F8_MATMUL; the
+ * last takes it on products of more than 16 rows) waits on a
  * flag that nothing sets, and every bounded wait of that launch gives up
  * after wait_us microseconds instead of about one second. The launch then
  * records MOE_ERR_DEVICE_TIMEOUT in its workspace's status word, lets its
@@ -310,6 +323,83 @@ MOE_API moe_status_t moe_layer_forward(const void* x, const float* r_attn,
                                const void* w_shared, const moe_cfg_t* cfg,
                                float* out, int32_t* topk_ids, float* weights,
                                void* stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit floating point: quantiser, product, and the layer with 8-bit banks.
+ *
+ * A matrix in 8 bits is codes (e4m3: 4 exponent and 3 fraction bits, largest
+ * number 448, no infinity) and f32 scales, one per block of 128 columns and
+ * of 1 row (activations) or 128 rows (weights); blocks at the ends are cut.
+ * It stands for code * scale. Any f32 scales are taken as inputs.
+ * ------------------------------------------------------------------------ */
+
+/* Quantises x [count][rows][ldx] (F32 or BF16, the first `cols` of every ldx
+ * values) into codes [count][rows][ldq] and scales
+ * [count][ceil(rows/block_rows)][ceil(cols/128)], block_rows 1 or 128.
+ * A block's scale is the smallest power of two, 2^-126 at least, with
+ * amax / scale <= 448; code = e4m3(x / scale), to nearest even (the division
+ * is exact). A block with a value that is not finite gets the scale NaN and
+ * NaN codes. Codes past a row's last column are not written.
+ * x and codes need the alignment of their element; 16-byte aligned rows are
+ * read and written in wide pieces. count * rows <= 2^31 - 1. */
+MOE_API moe_status_t moe_fp8_quantize(const void* x, int32_t x_dtype, int64_t ldx, int32_t count,
+                                      int32_t rows, int32_t cols, int32_t block_rows, void* codes,
+                                      int64_t ldq, float* scales, void* stream);
+
+typedef struct {
+  int32_t M, N, K;       /* >= 0; K >= 1 */
+  int32_t out_dtype;     /* MOE_BF16 or MOE_F32 */
+  int64_t lda, ldb;      /* codes between rows of a and b: >= K, multiples of 16 */
+  int64_t ldo;           /* values between rows of out: >= N */
+  void* workspace;       /* device scratch, >= moe_fp8_matmul_workspace_bytes */
+  size_t workspace_bytes;
+} moe_fp8_matmul_t;
+
+/* out [M][N] = a b^T, a [M][K] with scales [M][ceil(K/128)], b [N][K] with
+ * scales [ceil(N/128)][ceil(K/128)], f32 accumulation, one rounding to
+ * out_dtype. a and b 16-byte aligned, out aligned to its element. Up to 16
+ * rows stream b on mma.sync; more run on tcgen05. M or N of 0 enqueues
+ * nothing. Deterministic. */
+MOE_API moe_status_t moe_fp8_matmul(const void* a, const float* a_scale, const void* b,
+                                    const float* b_scale, const moe_fp8_matmul_t* mm, void* out,
+                                    void* stream);
+/* Workspace bytes of the product (0 if mm is invalid; mm's workspace fields
+ * are ignored). A workspace of the most bytes needed serves several shapes
+ * when it is initialised again, on the stream, before a call of another shape. */
+MOE_API size_t moe_fp8_matmul_workspace_bytes(const moe_fp8_matmul_t* mm);
+/* Zeroes the workspace's control words and counters; enqueued once before the
+ * first use of a fresh workspace, and after a device timeout (which
+ * moe_read_device_status reports for a moe_cfg_t with these workspace
+ * fields). */
+MOE_API moe_status_t moe_fp8_matmul_init(const moe_fp8_matmul_t* mm, void* stream);
+
+/* Workspace of the two calls below for this cfg (0 if invalid), and its
+ * initialisation; status is read with moe_read_device_status. */
+MOE_API size_t moe_fp8_workspace_bytes(const moe_cfg_t* cfg);
+MOE_API moe_status_t moe_fp8_workspace_init(const moe_cfg_t* cfg, void* stream);
+
+/* moe_experts_forward with 8-bit banks: cfg->expert_dtype MOE_F8_E4M3_B128
+ * (bank.w codes, bank.scale f32 scales, bank.minv unused), act_dtype BF16,
+ * d_model, d_ff and d_ff_shared multiples of 16. x is quantised with a scale
+ * per 1 x 128 as moe_fp8_quantize does, and so is h = SiLU(gate) * up (from
+ * f32) before the down product. The shared expert's matrices are banks of one
+ * expert. r_attn may be NULL (no residual); out [T][d] is out_dtype (F32 or
+ * BF16) and may alias r_attn when it is F32. Up to 16 tokens take two kernels
+ * (gate/up; down + combine; MOE_PATH_GEMV asks for them), more take grouped
+ * products on tcgen05 (MOE_PATH_TC); MOE_PATH_FUSED is MOE_ERR_UNSUPPORTED. */
+MOE_API moe_status_t moe_fp8_experts_forward(
+    const void* x, const float* r_attn, const int32_t* topk_ids, const float* weights,
+    const float* s_shared, moe_bank_t W_gate, moe_bank_t W_up, moe_bank_t W_down,
+    moe_bank_t Ws_gate, moe_bank_t Ws_up, moe_bank_t Ws_down, const void* w_shared,
+    const moe_cfg_t* cfg, void* out, int32_t out_dtype, void* stream);
+
+/* moe_layer_forward with 8-bit banks: routing from W_router (BF16) by the
+ * separate routing kernels, then moe_fp8_experts_forward. */
+MOE_API moe_status_t moe_fp8_layer_forward(
+    const void* x, const float* r_attn, const void* W_router, const float* expert_bias,
+    moe_bank_t W_gate, moe_bank_t W_up, moe_bank_t W_down, moe_bank_t Ws_gate, moe_bank_t Ws_up,
+    moe_bank_t Ws_down, const void* w_shared, const moe_cfg_t* cfg, void* out, int32_t out_dtype,
+    int32_t* topk_ids, float* weights, void* stream);
 
 #ifdef __cplusplus
 }

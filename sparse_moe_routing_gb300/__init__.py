@@ -18,14 +18,16 @@ __all__ = [
     "workspace_bytes", "alloc_workspace", "route", "bucket", "experts_forward",
     "layer_forward", "read_device_status", "SOFTMAX_TOPK", "SIGMOID_GROUP_TOPK",
     "F32", "BF16", "Q4_AFFINE_G64", "PATH_AUTO", "PATH_GEMV", "PATH_TC", "PATH_FUSED",
-    "inject_stall",
+    "inject_stall", "F8_E4M3_B128", "fp8_empty", "fp8_quantize", "fp8_matmul",
+    "fp8_matmul_workspace", "fp8_workspace_bytes", "fp8_alloc_workspace", "fp8_experts_forward",
+    "fp8_layer_forward", "Fp8Experts", "Fp8Linear",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_PKG, "libmoe_route.so")
 
 SOFTMAX_TOPK, SIGMOID_GROUP_TOPK = 0, 1
-F32, BF16, Q4_AFFINE_G64 = 0, 1, 2
+F32, BF16, Q4_AFFINE_G64, F8_E4M3_B128 = 0, 1, 2, 3
 PATH_AUTO, PATH_GEMV, PATH_TC, PATH_FUSED = 0, 1, 2, 3
 _STATUS = ["MOE_OK", "MOE_ERR_INVALID_ARG", "MOE_ERR_UNSUPPORTED", "MOE_ERR_WORKSPACE",
            "MOE_ERR_CUDA", "MOE_ERR_DEVICE_TIMEOUT", "MOE_ERR_DEVICE_CHECK"]
@@ -58,6 +60,13 @@ class _Bank(ctypes.Structure):
     _fields_ = [("w", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("minv", ctypes.c_void_p)]
 
 
+class _Fp8Matmul(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("lda", ctypes.c_int64), ("ldb", ctypes.c_int64),
+                ("ldo", ctypes.c_int64), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
 _P = ctypes.c_void_p
 _SIGS = {
     "moe_abi_version": (ctypes.c_int, []),
@@ -77,12 +86,25 @@ _SIGS = {
     "moe_trace_kernel": (ctypes.c_int, [ctypes.c_int, _P, _P, ctypes.c_int,
                                         ctypes.POINTER(ctypes.c_int)]),
     "moe_inject_stall": (ctypes.c_int, [ctypes.c_int, ctypes.c_uint32]),
+    "moe_fp8_quantize": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int64] + [ctypes.c_int32] * 4
+                         + [_P, ctypes.c_int64, _P, _P]),
+    "moe_fp8_matmul": (ctypes.c_int, [_P, _P, _P, _P, ctypes.POINTER(_Fp8Matmul), _P, _P]),
+    "moe_fp8_matmul_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(_Fp8Matmul)]),
+    "moe_fp8_matmul_init": (ctypes.c_int, [ctypes.POINTER(_Fp8Matmul), _P]),
+    "moe_fp8_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(_Cfg)]),
+    "moe_fp8_workspace_init": (ctypes.c_int, [ctypes.POINTER(_Cfg), _P]),
+    "moe_fp8_experts_forward": (ctypes.c_int, [_P] * 5 + [_Bank] * 6 + [
+        _P, ctypes.POINTER(_Cfg), _P, ctypes.c_int32, _P]),
+    "moe_fp8_layer_forward": (ctypes.c_int, [_P] * 4 + [_Bank] * 6 + [
+        _P, ctypes.POINTER(_Cfg), _P, ctypes.c_int32, _P, _P, _P]),
 }
 
 # kernel families (moe_kernel_t)
 KERNELS = {"router_logits": 1, "router_topk": 2, "shared_gate": 3, "bucket": 4,
            "gemv_gateup": 5, "gemv_down": 6, "combine": 7, "tc_gateup": 8, "tc_down": 9,
-           "gather": 10, "tc_router": 11, "decode_fused": 12}
+           "gather": 10, "tc_router": 11, "decode_fused": 12, "f8_quant": 13,
+           "f8_few_gateup": 14, "f8_few_down": 15, "f8_tc_gateup": 16, "f8_tc_down": 17,
+           "f8_matmul": 18}
 
 _lib = None
 
@@ -229,8 +251,9 @@ def layer_forward(cfg, workspace, x, r_attn, W_router, W_gate, W_up, W_down, out
 
 def inject_stall(kernel: str, wait_us: int):
     """Failure self-test (moe_inject_stall): the next launch of `kernel`
-    ("tc_gateup", "tc_down" or "decode_fused") waits on a flag nothing sets
-    and gives up after wait_us; None disarms."""
+    ("tc_gateup", "tc_down", "decode_fused", "f8_tc_gateup", "f8_tc_down" or
+    "f8_matmul") waits on a flag nothing sets and gives up after wait_us; None
+    disarms."""
     _check(lib().moe_inject_stall(0 if kernel is None else KERNELS[kernel], int(wait_us)),
            "moe_inject_stall")
 
@@ -309,6 +332,278 @@ class MoELayer:
                       Ws_up=w.get("Ws_up"), Ws_down=w.get("Ws_down"),
                       w_shared=w.get("w_shared"), stream=stream)
         return out, self.ids, self.weights
+
+    def device_status(self, stream=None):
+        return read_device_status(self.cfg, self.ws, stream)
+
+
+# ---------------------------------------------------------------------------
+# 8-bit floating point: e4m3 codes and one fp32 scale per block of 128
+# ---------------------------------------------------------------------------
+_dt = None
+
+
+def _dtypes():
+    """torch dtype -> moe_dtype_t of the 8-bit calls' values."""
+    global _dt
+    if _dt is None:
+        import torch
+        _dt = {torch.float32: F32, torch.bfloat16: BF16}
+    return _dt
+
+
+def _dtype_of(t):
+    d = _dtypes().get(t.dtype)
+    if d is None:
+        raise ValueError("expected a float32 or bfloat16 tensor, got %s" % t.dtype)
+    return d
+
+
+def _rows_ptr(t, name):
+    """Pointer of a matrix (or a stack of them) with unit column stride."""
+    if not t.is_cuda:
+        raise ValueError("%s must be on a CUDA device" % name)
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("%s must have contiguous rows" % name)
+    return t.data_ptr()
+
+
+def _ld(t):
+    """Values between rows; the row length where there is at most one row."""
+    return t.stride(-2) if t.shape[-2] > 1 else max(t.stride(-2), t.shape[-1])
+
+
+def _codes_dtype(t, name):
+    import torch
+    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise ValueError("%s must be float8_e4m3fn (or its bytes as uint8)" % name)
+
+
+def _shape_is(t, shape, name):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+
+
+def _scales_ok(t, shape, name):
+    import torch
+    if t.dtype != torch.float32:
+        raise ValueError("%s must be float32" % name)
+    _shape_is(t, shape, name)
+
+
+def fp8_empty(rows, cols, block_rows=1, count=None, device=None):
+    """(codes, scales) tensors for a rows x cols matrix (a stack of `count` of
+    them): codes' rows are padded to 16 bytes, as the products take them."""
+    import torch
+    lead = () if count is None else (count,)
+    pitch = -(-cols // 16) * 16
+    codes = torch.empty(lead + (rows, pitch), dtype=torch.float8_e4m3fn, device=device or "cuda")
+    scales = torch.empty(lead + (-(-rows // block_rows), -(-cols // 128)), dtype=torch.float32,
+                         device=device or "cuda")
+    return codes[..., :cols], scales
+
+
+def fp8_quantize(x, codes, scales, block_rows=1, stream=None):
+    """moe_fp8_quantize: x [rows, cols] or [count, rows, cols] (float32 or
+    bfloat16) into codes (float8_e4m3fn, same shape) and scales."""
+    if x.dim() not in (2, 3):
+        raise ValueError("x must have two or three dimensions")
+    _codes_dtype(codes, "codes")
+    _shape_is(codes, x.shape, "codes")
+    rows, cols = x.shape[-2:]
+    count = x.shape[0] if x.dim() == 3 else 1
+    ldx, ldq = _ld(x), _ld(codes)
+    if x.dim() == 3 and count > 1 and (x.stride(0) != rows * ldx or codes.stride(0) != rows * ldq):
+        raise ValueError("stacked matrices must follow one another at rows * row stride")
+    _scales_ok(scales, x.shape[:-2] + (-(-rows // block_rows) if block_rows > 0 else 0, -(-cols // 128)),
+               "scales")
+    _check(lib().moe_fp8_quantize(_rows_ptr(x, "x"), _dtype_of(x), ldx, count, rows, cols, block_rows,
+                                  _rows_ptr(codes, "codes"), ldq, _ptr(scales), _stream(stream)),
+           "moe_fp8_quantize")
+
+
+def _matmul_args(M, N, K, out_dtype=BF16, lda=0, ldb=0, ldo=0, workspace=None):
+    p = -(-max(K, 1) // 16) * 16
+    m = _Fp8Matmul(M, N, K, out_dtype, lda or p, ldb or p, ldo or N, None, 0)
+    if workspace is not None:
+        m.workspace = workspace.data_ptr()
+        m.workspace_bytes = workspace.numel() * workspace.element_size()
+    return m
+
+
+def fp8_matmul_workspace(M, N, K, device=None, stream=None):
+    """Allocates (with torch) and initialises the workspace of an M x N x K
+    product."""
+    import torch
+    n = lib().moe_fp8_matmul_workspace_bytes(ctypes.byref(_matmul_args(M, N, K)))
+    if n == 0:
+        raise MoEError(1, "moe_fp8_matmul_workspace_bytes")
+    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    _check(lib().moe_fp8_matmul_init(ctypes.byref(_matmul_args(M, N, K, workspace=ws)),
+                                     _stream(stream)), "moe_fp8_matmul_init")
+    return ws
+
+
+def fp8_matmul(a, a_scale, b, b_scale, out, workspace, stream=None):
+    """moe_fp8_matmul: out [M, N] = a [M, K] b [N, K]^T, codes with scales per
+    1 x 128 (a) and 128 x 128 (b); out float32 or bfloat16."""
+    M, K = a.shape
+    N = b.shape[0]
+    _codes_dtype(a, "a")
+    _codes_dtype(b, "b")
+    _shape_is(b, (N, K), "b")
+    _shape_is(out, (M, N), "out")
+    kb = -(-K // 128)
+    _scales_ok(a_scale, (M, kb), "a_scale")
+    _scales_ok(b_scale, (-(-N // 128), kb), "b_scale")
+    m = _matmul_args(M, N, K, _dtype_of(out), _ld(a), _ld(b), _ld(out), workspace)
+    _check(lib().moe_fp8_matmul(_rows_ptr(a, "a"), _ptr(a_scale), _rows_ptr(b, "b"), _ptr(b_scale),
+                                ctypes.byref(m), _rows_ptr(out, "out"), _stream(stream)),
+           "moe_fp8_matmul")
+
+
+class Fp8Linear:
+    """y = x W^T with W [N, K] held in 8 bits and x quantised on the way:
+    fp8_quantize, then fp8_matmul, for up to max_rows rows."""
+
+    def __init__(self, weight, max_rows, device=None):
+        N, K = weight.shape
+        self.N, self.K = N, K
+        self.codes, self.scales = fp8_empty(N, K, 128, device=weight.device)
+        fp8_quantize(weight, self.codes, self.scales, block_rows=128)
+        self.x, self.x_scales = fp8_empty(max_rows, K, 1, device=weight.device)
+        self._ws = {}
+
+    def __call__(self, x, out, stream=None):
+        M = x.shape[0]
+        if M not in self._ws:
+            self._ws[M] = fp8_matmul_workspace(M, self.N, self.K, x.device, stream)
+        xq, xs = self.x[:M], self.x_scales[:M]
+        fp8_quantize(x, xq, xs, stream=stream)
+        fp8_matmul(xq, xs, self.codes, self.scales, out, self._ws[M], stream)
+        return out
+
+
+def fp8_workspace_bytes(cfg: MoEConfig) -> int:
+    c = cfg._c()
+    n = lib().moe_fp8_workspace_bytes(ctypes.byref(c))
+    if n == 0:
+        raise MoEError(1, "moe_fp8_workspace_bytes")
+    return n
+
+
+def fp8_alloc_workspace(cfg: MoEConfig, device=None, stream=None):
+    """Allocates (with torch) and initialises a workspace of the 8-bit layer."""
+    import torch
+    ws = torch.empty(fp8_workspace_bytes(cfg), dtype=torch.uint8, device=device or "cuda")
+    _check(lib().moe_fp8_workspace_init(ctypes.byref(cfg._c(ws)), _stream(stream)),
+           "moe_fp8_workspace_init")
+    return ws
+
+
+def _bank8(b, shape):
+    """An 8-bit bank from (codes, scales); None stands for no shared expert."""
+    if b is None:
+        return _Bank(None, None, None)
+    codes, scales = b
+    _codes_dtype(codes, "a bank's codes")
+    if tuple(codes.shape) not in (tuple(shape), tuple(shape)[1:] if shape[0] == 1 else None):
+        raise ValueError("a bank's codes have shape %s, expected %s" % (tuple(codes.shape), tuple(shape)))
+    want = (shape[0], -(-shape[1] // 128), -(-shape[2] // 128))
+    _scales_ok(scales, want if scales.dim() == 3 else want[1:], "a bank's scales")
+    return _Bank(_ptr(codes), _ptr(scales), None)
+
+
+def _banks8(cfg, W_gate, W_up, W_down, Ws_gate, Ws_up, Ws_down):
+    E, d, I, Is = cfg.n_experts, cfg.d_model, cfg.d_ff, cfg.d_ff_shared
+    sh = (lambda b, s: _bank8(b, s)) if Is else (lambda b, s: _Bank(None, None, None))
+    return (_bank8(W_gate, (E, I, d)), _bank8(W_up, (E, I, d)), _bank8(W_down, (E, d, I)),
+            sh(Ws_gate, (1, Is, d)), sh(Ws_up, (1, Is, d)), sh(Ws_down, (1, d, Is)))
+
+
+def fp8_experts_forward(cfg, workspace, x, topk_ids, weights, W_gate, W_up, W_down, out,
+                        s_shared=None, r_attn=None, Ws_gate=None, Ws_up=None, Ws_down=None,
+                        w_shared=None, stream=None):
+    """moe_fp8_experts_forward: banks are (codes, scales) pairs; out float32 or
+    bfloat16 [T, d_model]; r_attn optional."""
+    b = _banks8(cfg, W_gate, W_up, W_down, Ws_gate, Ws_up, Ws_down)
+    _check(lib().moe_fp8_experts_forward(
+        _ptr(x), _ptr(r_attn), _ptr(topk_ids), _ptr(weights), _ptr(s_shared), *b, _ptr(w_shared),
+        ctypes.byref(cfg._c(workspace)), _ptr(out), _dtype_of(out), _stream(stream)),
+        "moe_fp8_experts_forward")
+
+
+def fp8_layer_forward(cfg, workspace, x, W_router, W_gate, W_up, W_down, out, topk_ids, weights,
+                      r_attn=None, expert_bias=None, Ws_gate=None, Ws_up=None, Ws_down=None,
+                      w_shared=None, stream=None):
+    """moe_fp8_layer_forward: the whole layer with 8-bit banks."""
+    b = _banks8(cfg, W_gate, W_up, W_down, Ws_gate, Ws_up, Ws_down)
+    _check(lib().moe_fp8_layer_forward(
+        _ptr(x), _ptr(r_attn), _ptr(W_router), _ptr(expert_bias), *b, _ptr(w_shared),
+        ctypes.byref(cfg._c(workspace)), _ptr(out), _dtype_of(out), _ptr(topk_ids), _ptr(weights),
+        _stream(stream)), "moe_fp8_layer_forward")
+
+
+class Fp8Experts:
+    """One layer's 8-bit banks plus its workspace; `forward` runs the expert
+    half for given routing, `layer` routing and experts.
+
+    weights: dict of (codes, scales) pairs W_gate, W_up, W_down and, with a
+    shared expert, Ws_gate, Ws_up, Ws_down; for `layer` also W_router,
+    expert_bias and w_shared tensors. `from_bf16` quantises a bf16 layer's."""
+
+    def __init__(self, cfg: MoEConfig, weights: dict, device=None):
+        import torch
+        self.cfg = cfg
+        self.w = weights
+        self.device = device or torch.device("cuda", torch.cuda.current_device())
+        self.ws = fp8_alloc_workspace(cfg, self.device)
+        self._banks = _banks8(cfg, weights["W_gate"], weights["W_up"], weights["W_down"],
+                              weights.get("Ws_gate"), weights.get("Ws_up"), weights.get("Ws_down"))
+        self._c = cfg._c(self.ws)
+        self._cp = ctypes.byref(self._c)
+        self._x_shape = (cfg.T, cfg.d_model)
+
+    @staticmethod
+    def from_bf16(cfg: MoEConfig, weights: dict, device=None):
+        """Quantises the banks of a layer's weight dict (128 x 128 blocks)."""
+        w = dict(weights)
+        for name in ("W_gate", "W_up", "W_down", "Ws_gate", "Ws_up", "Ws_down"):
+            m = weights.get(name)
+            if m is None:
+                continue
+            codes, scales = fp8_empty(m.shape[-2], m.shape[-1], 128,
+                                      m.shape[0] if m.dim() == 3 else None, m.device)
+            fp8_quantize(m, codes, scales, block_rows=128)
+            w[name] = (codes, scales)
+        return Fp8Experts(cfg, w, device)
+
+    def _rows(self, x, out, r_attn):
+        if x.shape != self._x_shape or out.shape != self._x_shape or \
+                (r_attn is not None and r_attn.shape != self._x_shape):
+            raise ValueError("x, out and r_attn must be [%d, %d]" % self._x_shape)
+
+    def forward(self, x, topk_ids, weights, s_shared=None, r_attn=None, out=None, stream=None):
+        import torch
+        if out is None:
+            out = torch.empty(self._x_shape, dtype=torch.bfloat16, device=self.device)
+        self._rows(x, out, r_attn)
+        _check(lib().moe_fp8_experts_forward(
+            _ptr(x), _ptr(r_attn), _ptr(topk_ids), _ptr(weights), _ptr(s_shared), *self._banks,
+            _ptr(self.w.get("w_shared")), self._cp, _ptr(out), _dtype_of(out), _stream(stream)),
+            "moe_fp8_experts_forward")
+        return out
+
+    def layer(self, x, topk_ids, weights, r_attn=None, out=None, stream=None):
+        import torch
+        if out is None:
+            out = torch.empty(self._x_shape, dtype=torch.bfloat16, device=self.device)
+        self._rows(x, out, r_attn)
+        _check(lib().moe_fp8_layer_forward(
+            _ptr(x), _ptr(r_attn), _ptr(self.w["W_router"]), _ptr(self.w.get("expert_bias")),
+            *self._banks, _ptr(self.w.get("w_shared")), self._cp, _ptr(out), _dtype_of(out),
+            _ptr(topk_ids), _ptr(weights), _stream(stream)), "moe_fp8_layer_forward")
+        return out
 
     def device_status(self, stream=None):
         return read_device_status(self.cfg, self.ws, stream)

@@ -286,6 +286,12 @@ const char* kernel_name(int kid) {
     case MOE_KERNEL_GATHER: return "moe:gather";
     case MOE_KERNEL_TC_ROUTER: return "moe:tc_router";
     case MOE_KERNEL_DECODE: return "moe:decode_fused";
+    case MOE_KERNEL_F8_QUANT: return "moe:f8_quant";
+    case MOE_KERNEL_F8_FEW_GATEUP: return "moe:f8_few_gateup";
+    case MOE_KERNEL_F8_FEW_DOWN: return "moe:f8_few_down";
+    case MOE_KERNEL_F8_TC_GATEUP: return "moe:f8_tc_gateup";
+    case MOE_KERNEL_F8_TC_DOWN: return "moe:f8_tc_down";
+    case MOE_KERNEL_F8_MATMUL: return "moe:f8_matmul";
   }
   return "moe:kernel";
 }
@@ -705,6 +711,25 @@ moe_status_t enqueue_fused(const void* x, const float* r_attn, const void* W_rou
 }
 
 }  // namespace
+
+cudaError_t run_launch(int kid, cudaStream_t st, cudaError_t (*fn)(void*), void* ctx) {
+  return run(kid, st, [&] { return fn(ctx); });
+}
+
+uint64_t launch_wait_limit(int kid, int* stall) { return take_stall(kid, stall); }
+
+RoutePlan route_plan(const moe_cfg_t& c) {
+  const Plan p = make_plan(c);
+  return RoutePlan{p.s_shared, p.counts, p.offsets, p.active, p.perm, p.pos, p.rowblocks, p.cta_hist,
+                   p.H};
+}
+
+moe_status_t route_chain(const void* x, const void* W_router, const float* bias,
+                         const void* w_shared, const moe_cfg_t* c, int32_t* ids, float* w,
+                         float* s_shared, cudaStream_t st) {
+  return enqueue_route(x, W_router, bias, w_shared, c, ids, w, s_shared, st);
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -736,7 +761,7 @@ moe_status_t moe_trace_kernel(int kernel, void* const* starts, void* const* stop
     g_trace = TraceState{};
     return MOE_OK;
   }
-  if (kernel < MOE_KERNEL_ROUTER_LOGITS || kernel > MOE_KERNEL_DECODE || n <= 0 || !starts ||
+  if (kernel < MOE_KERNEL_ROUTER_LOGITS || kernel > MOE_KERNEL_F8_MATMUL || n <= 0 || !starts ||
       !stops || !count)
     return MOE_ERR_INVALID_ARG;
   g_trace.kernel = kernel;
@@ -753,7 +778,9 @@ moe_status_t moe_inject_stall(int kernel, uint32_t wait_us) {
     g_stall_kernel.store(0);
     return MOE_OK;
   }
-  if (kernel != MOE_KERNEL_TC_GATEUP && kernel != MOE_KERNEL_TC_DOWN && kernel != MOE_KERNEL_DECODE)
+  if (kernel != MOE_KERNEL_TC_GATEUP && kernel != MOE_KERNEL_TC_DOWN &&
+      kernel != MOE_KERNEL_DECODE && kernel != MOE_KERNEL_F8_TC_GATEUP &&
+      kernel != MOE_KERNEL_F8_TC_DOWN && kernel != MOE_KERNEL_F8_MATMUL)
     return MOE_ERR_INVALID_ARG;
   g_stall_wait_ns.store((uint64_t)(wait_us ? wait_us : 1) * 1000ull);
   g_stall_kernel.store(kernel);

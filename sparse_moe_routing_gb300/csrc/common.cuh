@@ -27,6 +27,8 @@ enum : uint32_t {
   kSiteTcRouter = 7,
   kSiteRouter = 8,
   kSiteDecode = 9,
+  kSiteFewFp8 = 10,
+  kSiteTcFp8 = 11,
 };
 
 struct Ctrl {

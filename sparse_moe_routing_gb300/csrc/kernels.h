@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -198,6 +199,105 @@ cudaError_t launch_tc_gemm(int mode, const TcMaps& maps, const TcArgs& a, int ma
 cudaError_t launch_gather_rows(const void* x, const int32_t* perm, int k, int d, void* out, int P,
                                cudaStream_t st);
 int tc_sm_count();
+// cuTensorMapEncodeTiled, or null.
+PFN_cuTensorMapEncodeTiled_v12000 tc_encode_fn();
+
+// ---------------------------------------------------------------------------
+// 8-bit floating point (e4m3, a scale per block of 128; format in
+// fp8_common.cuh)
+// ---------------------------------------------------------------------------
+struct F8QuantArgs {
+  const void* x;       // [count][rows][ldx] bf16 or f32
+  uint8_t* codes;      // [count][rows][ldq]
+  float* scales;       // [count][row blocks][column blocks]
+  int rows, cols, count;
+  long long ldx, ldq;  // elements
+};
+cudaError_t launch_f8_quant(const F8QuantArgs& a, bool bf16, bool tiles, cudaStream_t st);
+
+// The tokens' codes in packed row order: row pos[t*k+s] for every routed pair
+// and, when own_rows is 1, row T*k + t.
+struct F8PackArgs {
+  const __nv_bfloat16* x;  // [T][d]
+  const int32_t* pos;      // [T*k]
+  uint8_t* codes;          // [T*k + T][d]
+  float* scales;           // [T*k + T][d / 128]
+  int T, d, k, own_rows;
+};
+cudaError_t launch_f8_pack(const F8PackArgs& a, cudaStream_t st);
+
+// The layer for a few tokens (fp8_few.cu). Rows of the intermediates are
+// positions of the pairs in (expert, pair) order, then the tokens.
+struct F8ExpertsArgs {
+  const __nv_bfloat16* x;  // [T][d]
+  const int32_t* ids;      // [T][k]
+  const float* alpha;      // [T][k]
+  const float* s_shared;   // [T] or null
+  const float* r_attn;     // [T][d] or null
+  const uint8_t *Wg, *Wu, *Wd, *Wsg, *Wsu, *Wsd;
+  const float *Sg, *Su, *Sd, *Ssg, *Ssu, *Ssd;
+  float* Hf;               // [T*k + T][ldh]
+  uint8_t* Hq;             // [T*k + T][ldh]
+  float* Hs;               // [T*k + T][hblocks]
+  unsigned* counters;      // [chunks][hblocks], zero between launches
+  void* out;               // [T][d]
+  Ctrl* ctrl;
+  int T, d, E, k, I, Is, ldh, hblocks, out_bf16;
+};
+constexpr int kF8FewTokens = 16;
+constexpr size_t few_lists_bytes() { return 13056; }
+bool f8_few_ok(int T, int d, int k);
+cudaError_t launch_f8_few_gateup(const F8ExpertsArgs& a, cudaStream_t st);
+cudaError_t launch_f8_few_down(const F8ExpertsArgs& a, cudaStream_t st);
+
+// out = A B^T for at most kF8FewTokens rows (fp8_few.cu).
+struct F8MatmulArgs {
+  const uint8_t* a;       // [M][lda]
+  const float* a_scale;   // [M][K blocks]
+  const uint8_t* b;       // [N][ldb]
+  const float* b_scale;   // [N blocks][K blocks]
+  void* out;              // [M][ldo]
+  int M, N, K, out_bf16;
+  long long lda, ldb, ldo;
+};
+cudaError_t launch_f8_few_matmul(const F8MatmulArgs& a, cudaStream_t st);
+
+// Tensor-core products (fp8_tc.cu).
+enum F8Mode { kF8GateUp = 0, kF8Down = 1, kF8Dense = 2 };
+struct F8TcArgs {
+  const int2* rowblocks;       // grouped: (group, row block) list
+  const int32_t* n_rowblocks;
+  const int32_t* offsets;
+  const int32_t* perm;
+  const float* alpha;          // down: [P]
+  const float* s_shared;       // down: [T]
+  const float* a_scale;        // [rows of A][a_blocks]
+  const float *b_scale0, *b_scale1;  // routed (gate, up | down) or dense B
+  const float *b_scale2, *b_scale3;  // shared expert
+  void* out;                   // codes | bf16 rows | dense out
+  float* out_scale;            // gate/up: [rows][out_blocks]
+  float4* partial;             // dense, ksplit > 1
+  unsigned* counters;          // dense, ksplit > 1: [tiles][8], zero between launches
+  Ctrl* ctrl;
+  int E, T, P, K;
+  int rows;                    // dense: rows of A
+  int n_cols, n_tiles;         // columns of a group's output, N tiles
+  int brows, b_blocks;         // rows of one expert in B's view, scale rows of it
+  int a_blocks, out_blocks;    // scales per row of a_scale and of out_scale
+  long long ldo;
+  int shared_only, arows;      // arows: box height of A's map
+  int ksplit, out_bf16, out_vec;
+  uint64_t wait_ns;
+  int stall;
+};
+struct F8TcMaps {
+  CUtensorMap A, B0, B1, B2, B3;
+};
+// 2D map of codes [rows][cols], rows `pitch` bytes apart, box 128 x box_rows.
+bool f8_make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t pitch,
+                 uint32_t box_rows);
+cudaError_t launch_f8_tc(int mode, const F8TcMaps& m, const F8TcArgs& a, int max_items,
+                         cudaStream_t st);
 
 // Raises `kernel`'s dynamic shared-memory opt-in limit to at least `bytes`
 // on the current device; `limits` holds the value set so far per device
@@ -242,6 +342,28 @@ moe_status_t validate_route_cfg(const moe_cfg_t* c);
 // Records the CUDA error behind a MOE_ERR_CUDA for moe_last_cuda_error.
 void set_last_cuda_error(cudaError_t e);
 
+// Shared by the entry points of api.cu and fp8_api.cu.
+// Runs one launcher of kernel family `kid`: counted, traced, in an NVTX range.
+cudaError_t run_launch(int kid, cudaStream_t st, cudaError_t (*fn)(void*), void* ctx);
+template <typename F>
+cudaError_t run_kernel(int kid, cudaStream_t st, F f) {
+  return run_launch(kid, st, [](void* p) { return (*static_cast<F*>(p))(); }, &f);
+}
+// The one-shot failure self-test of family `kid`, if armed: wait limit and
+// stall flag of the launch.
+uint64_t launch_wait_limit(int kid, int* stall);
+// Workspace offsets that every layer workspace starts with (routing and
+// bucketing), and their end.
+struct RoutePlan {
+  size_t s_shared, counts, offsets, active, perm, pos, rowblocks, cta_hist, end;
+};
+RoutePlan route_plan(const moe_cfg_t& c);
+// Routing into ids, weights and s_shared (or null) with the separate routing
+// kernels, whatever cfg's path.
+moe_status_t route_chain(const void* x, const void* W_router, const float* bias,
+                         const void* w_shared, const moe_cfg_t* c, int32_t* ids, float* w,
+                         float* s_shared, cudaStream_t st);
+
 // One launcher per kernel; each returns the launch's cudaError_t.
 cudaError_t launch_router_logits(const RouterArgs& ra, bool bf16, cudaStream_t st);
 cudaError_t launch_router_topk(const TopkArgs& ta, cudaStream_t st);
@@ -264,5 +386,14 @@ cudaError_t launch_gemv_small(const GemvArgs& a, int act, int wdt, bool down, cu
 // True when the GEMV kernels can stage at least one token of width d and kmax.
 bool gemv_supported(int d, int kmax);
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t st);
+// out[t] = [r_attn[t] +] the sum over slots of Y[pos[t*k+s]] [+ Y[T*k+t]], bf16 rows in.
+struct CombineRowsArgs {
+  const float* r_attn;       // [T][d] or null
+  const __nv_bfloat16* Y;    // [T*k + T][d]
+  const int32_t* pos;        // [T*k]
+  void* out;                 // [T][d] f32, or bf16 when out_bf16
+  int T, d, k, own_rows, out_bf16;
+};
+cudaError_t launch_combine_rows(const CombineRowsArgs& a, cudaStream_t st);
 
 }  // namespace moe

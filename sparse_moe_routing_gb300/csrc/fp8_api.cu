@@ -61,7 +61,7 @@ MmPlan mm_plan(const moe_fp8_matmul_t& m) {
     if (s > 1) p.ksplit = s;
   }
   if (p.ksplit > 1) {
-    p.partial = p.counters + align256((size_t)p.tiles * 8 * sizeof(unsigned));
+    p.partial = p.counters + align256((size_t)p.tiles * kF8TileCounters * sizeof(unsigned));
     p.total = p.partial + (size_t)p.ksplit * p.tiles * kBm * kBn * 4;
   }
   return p;

@@ -6,14 +6,14 @@
 // step (128-byte swizzle, 4 stages of 48 KB); one thread issues the four
 // tcgen05.mma (e4m3, fp32, K = 32) of a step into one of two 256-column TMEM
 // buffers. The scales change with every block of 128 k, so a buffer holds one
-// step's products only: eight epilogue warps read it back, multiply by the two
-// scales and add into fp32 sums that stay in their registers (128 a thread),
+// step's products only: sixteen epilogue warps read it back, multiply by the two
+// scales and add into fp32 sums that stay in their registers (64 a thread),
 // while the tensor core fills the other buffer.
 //
 // Three uses:
 //  * gate/up: B = 128 gate and 128 up rows; the epilogue applies SwiGLU and
-//    quantises h: a thread holds half of a row's 128 columns, the other half's
-//    maximum comes through shared memory, and codes and scale go out in the
+//    quantises h: a thread holds 32 of a row's 128 columns, the others'
+//    maxima come through shared memory, and codes and scale go out in the
 //    form that the down product reads;
 //  * down: the routing weight (or the shared gate) applied, rows out in bf16;
 //  * dense: one product, bf16 or fp32 out, k split over CTAs when there are
@@ -35,20 +35,29 @@ constexpr int BM = 128, BN = 256, BK = 128;
 constexpr int kStages = 4;
 constexpr int kStageA = BM * BK, kStageB = BN * BK;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kEpiWarps = 8;
-// Three warpgroups: warp 0 the producer, warp 1 the MMA issuer (2 and 3 idle),
-// warps 4-11 the epilogue. Launched with 168 registers a thread (64,512 in
-// all); the first group hands registers to the epilogue, whose 128 fp32 sums
-// and 32 values in flight do not fit 168: 128 x 64 + 256 x 216 = 63,488.
+constexpr int kEpiWarps = 16;
+constexpr int kParts = kEpiWarps / 4;     // column parts of a tile, one per warp of a lane quarter
+constexpr int kPartCols = BN / kParts;    // 64
+// Warp 0 is the producer, warps 1 and 2 issue the MMAs, warp 3 brings the
+// scales, warps 4-19 are the epilogue: four a scheduler, so that one warp's
+// wait for TMEM is covered by the others' arithmetic. Launched with 96
+// registers a thread (61,440 in all); the first warpgroup hands some to the
+// epilogue, which holds 64 fp32 sums and 16 values in flight a thread:
+// 128 x 64 + 512 x 104 = 61,440.
 constexpr int kEpiWarp0 = 4;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
+
+// Scales, kChunk steps at a time: A's [kChunks][kChunk][128 rows], then B's
+// [kChunks][kChunk][2: gate, up | left, right half of the columns].
+constexpr int kChunk = 4, kChunks = 8;
 
 struct Smem {
   static constexpr size_t kA = 0;
   static constexpr size_t kB = kA + (size_t)kStages * kStageA;
-  static constexpr size_t kMax = kB + (size_t)kStages * kStageB;  // [2][2][BM] row maxima
-  static constexpr size_t kBars = kMax + 4 * BM * 4;
-  static constexpr size_t kBytes = 1024 + kBars + (2 * kStages + 5) * 8 + 16;
+  static constexpr size_t kMax = kB + (size_t)kStages * kStageB;  // [2][kParts][BM] row maxima
+  static constexpr size_t kScale = kMax + 2 * kParts * BM * 4;
+  static constexpr size_t kBars = kScale + kChunks * kChunk * (BM + 2) * 4;
+  static constexpr size_t kBytes = 1024 + kBars + (2 * kStages + 2 * kChunks + 5) * 8 + 16;
 };
 static_assert(Smem::kBytes <= 227 * 1024, "shared memory plan exceeds 227 KB");
 
@@ -63,18 +72,16 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_
       "l"(a_desc), "l"(b_desc), "r"(kIdesc), "r"(accumulate));
 }
 
-// Two fp32 sums in one 64-bit register: sum += v * s.
-__device__ __forceinline__ void fma2(uint64_t& sum, uint32_t v0, uint32_t v1, uint64_t s) {
-  asm("{\n .reg .b64 v;\n mov.b64 v, {%1, %2};\n fma.rn.f32x2 %0, v, %3, %0;\n}"
-      : "+l"(sum)
-      : "r"(v0), "r"(v1), "l"(s));
+// Asynchronous copy of one fp32 value to shared memory, or of zero.
+__device__ __forceinline__ void copy4_async(float* dst, const float* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(valid ? 4 : 0)
+               : "memory");
 }
-__device__ __forceinline__ uint64_t both(float s) {
-  const uint32_t b = __float_as_uint(s);
-  return (uint64_t)b << 32 | b;
+// Arrives on `bar` once this thread's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ float lo(uint64_t v) { return __uint_as_float((uint32_t)v); }
-__device__ __forceinline__ float hi(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
 struct Item {
   int g, m, nt;     // group, row block in it, N tile
@@ -135,6 +142,32 @@ __device__ __forceinline__ void give_up(const F8TcArgs& a, volatile int* abort_f
   report(a.ctrl, kDevTimeout, kSiteTcFp8);
 }
 
+// One thread waits for a phase of `bar`; false when the wait ran out of its
+// limit or another warp gave up.
+__device__ __forceinline__ bool lane_wait(uint64_t* bar, uint32_t parity, const F8TcArgs& a,
+                                          volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = 0;
+  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+    if ((n & 63u) == 0) {
+      if (*abort_flag) return false;
+      if (t0 == 0) t0 = globaltimer();
+      if (globaltimer() - t0 > a.wait_ns) return false;
+    }
+  }
+  return true;
+}
+// The whole warp waits. Every lane polls: one lane's poll with its outcome
+// shuffled to the others took 1390 cycles for a round trip between one warp
+// and sixteen, this 260 (measured alone), and there are two such round trips a
+// step.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const F8TcArgs& a,
+                                          volatile int* abort_flag) {
+  const bool ok = __all_sync(0xffffffffu, lane_wait(bar, parity, a, abort_flag));
+  if (!ok && (threadIdx.x & 31) == 0) give_up(a, abort_flag);
+  return ok;
+}
+
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     f8_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
@@ -146,11 +179,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sA = smem + Smem::kA;
   uint8_t* sB = smem + Smem::kB;
   uint32_t* sMax = reinterpret_cast<uint32_t*>(smem + Smem::kMax);
+  float* sScale = reinterpret_cast<float*>(smem + Smem::kScale);
+  float* sScaleB = sScale + kChunks * kChunk * BM;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Smem::kBars);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 2;
-  uint64_t* xbar = tempty + 2;
+  uint64_t* cfull = tempty + 2;
+  uint64_t* cempty = cfull + kChunks;
+  uint64_t* xbar = cempty + kChunks;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(xbar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -162,6 +199,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], kEpiWarps);
+    }
+    for (int b = 0; b < kChunks; ++b) {
+      mbar_init(&cfull[b], 32);
+      mbar_init(&cempty[b], kEpiWarps);
     }
     mbar_init(xbar, kEpiWarps);
     *abort_flag = 0;
@@ -177,7 +218,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const uint64_t lim = a.wait_ns;
   pdl_wait();
   pdl_trigger();
 
@@ -187,226 +227,260 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int KB = (a.K + BK - 1) / BK;
 
   // Every role loop is run by its whole warp, so that each warp reaches the
-  // closing CTA barrier converged; a wait's outcome is lane 0's.
+  // closing CTA barrier converged.
   if (warp < kEpiWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    // The producer's and the issuer's loops are lane 0's alone: an issue waits
+    // for room in the tensor core's short queue, and every cycle between two
+    // issues leaves it idle (votes and shuffles there cost 400 a step).
     if (warp == 0) {
       // -------------------------------------------------------------- producer
-      const uint32_t bytes = (uint32_t)a.arows * BK + kStageB;
-      int stage = 0;
-      uint32_t ph = 0;
-      bool alive = true;
-      for (int t = blockIdx.x; t < total && alive; t += gridDim.x) {
-        const Item it = item_at<MODE>(a, t, n_rb, KB);
-        const CUtensorMap* b0 = it.shared ? &tmB2 : &tmB0;
-        const CUtensorMap* b1 = it.shared ? &tmB3 : &tmB1;
-        const int arow = it.row0 + it.m * BM;
-        const int brow = (MODE == kF8Dense || it.shared ? 0 : it.g * a.brows) +
-                         it.nt * (MODE == kF8GateUp ? BN / 2 : BN);
-        for (int kb = it.kb0; kb < it.kb1; ++kb) {
-          bool ok = lane == 0 ? mbar_wait(&empty[stage], ph ^ 1u, lim) : true;
-          ok = __shfl_sync(0xffffffffu, ok, 0) && !*abort_flag;
-          if (!ok) {
-            if (lane == 0) give_up(a, abort_flag);
-            alive = false;
-            break;
-          }
-          if (lane == 0) {
+      if (lane == 0) {
+        const uint32_t bytes = (uint32_t)a.arows * BK + kStageB;
+        int stage = 0;
+        uint32_t ph = 0;
+        bool alive = true;
+        for (int t = blockIdx.x; t < total && alive; t += gridDim.x) {
+          const Item it = item_at<MODE>(a, t, n_rb, KB);
+          const CUtensorMap* b0 = it.shared ? &tmB2 : &tmB0;
+          const CUtensorMap* b1 = it.shared ? &tmB3 : &tmB1;
+          const int arow = it.row0 + it.m * BM;
+          const int brow = (MODE == kF8Dense || it.shared ? 0 : it.g * a.brows) +
+                           it.nt * (MODE == kF8GateUp ? BN / 2 : BN);
+          for (int kb = it.kb0; kb < it.kb1; ++kb) {
+            if (!lane_wait(&empty[stage], ph ^ 1u, a, abort_flag)) {
+              give_up(a, abort_flag);
+              alive = false;
+              break;
+            }
             uint64_t* bar = &full[stage];
             mbar_expect_tx(bar, bytes);
             tma_load_2d(sA + stage * kStageA, &tmA, bar, kb * BK, arow);
             tma_load_2d(sB + stage * kStageB, b0, bar, kb * BK, brow);
             if (MODE == kF8GateUp)
               tma_load_2d(sB + stage * kStageB + kStageB / 2, b1, bar, kb * BK, brow);
-          }
-          __syncwarp();
-          if (++stage == kStages) {
-            stage = 0;
-            ph ^= 1u;
+            if (++stage == kStages) {
+              stage = 0;
+              ph ^= 1u;
+            }
           }
         }
       }
-    } else if (warp == 1) {
-      // ------------------------------------------------------------ MMA issuer
-      int stage = 0, acc = 0;
-      uint32_t ph = 0, aph = 0;
-      bool alive = true;
-      if (a.stall) {
+      __syncwarp();
+    } else if (warp <= 2) {
+      // ----------------------------------------------------------- MMA issuers
+      // Two, each with every second step and its TMEM buffer: issuing a step
+      // takes its MMAs' 512 cycles, and the commits and the next step's waits
+      // some 600 more, which one issuer would leave the tensor core idle.
+      if (lane == 0) {
+        const uint32_t me = warp - 1;
         // failure self-test: wait on a barrier that only this warp completes
-        bool ok = lane == 0 ? mbar_wait(&tfull[0], 0u, lim) : true;
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) {
-          if (lane == 0) give_up(a, abort_flag);
-          alive = false;
+        bool alive = !a.stall || lane_wait(&tfull[me], 0u, a, abort_flag);
+        if (!alive) give_up(a, abort_flag);
+        const uint32_t d = tmem_base + me * BN;
+        uint32_t n = 0;  // steps so far
+        for (int t = blockIdx.x; t < total && alive; t += gridDim.x) {
+          const Item it = item_at<MODE>(a, t, n_rb, KB);
+          for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
+            if ((n & 1u) != me) continue;
+            const uint32_t stage = n % kStages;
+            if (!lane_wait(&full[stage], n / kStages & 1u, a, abort_flag) ||
+                !lane_wait(&tempty[me], (n >> 1 & 1u) ^ 1u, a, abort_flag)) {
+              give_up(a, abort_flag);
+              alive = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t a_desc = sw128_desc(smem_u32(sA + stage * kStageA));
+            const uint64_t b_desc = sw128_desc(smem_u32(sB + stage * kStageB));
+#pragma unroll
+            for (int k = 0; k < BK / 32; ++k)  // 32 bytes on: 2 in the descriptor
+              mma_f8(d, a_desc + 2 * k, b_desc + 2 * k, k != 0 ? 1u : 0u);
+            mma_commit(&tfull[me]);
+            mma_commit(&empty[stage]);
+          }
         }
       }
+      __syncwarp();
+    } else {
+      // ---------------------------------------------------------------- scales
+      // Four rows a lane, copied asynchronously up to kChunks chunks ahead of
+      // the epilogue (loading a step's scales in the epilogue, one step ahead,
+      // waited out the latency of L2 there: 2432 x 4096 x 4096 100 us against
+      // 63 with constant scales).
+      const int r0 = lane;
+      int cb = 0;
+      uint32_t cph = 0;
+      bool alive = true;
       for (int t = blockIdx.x; t < total && alive; t += gridDim.x) {
         const Item it = item_at<MODE>(a, t, n_rb, KB);
-        for (int kb = it.kb0; kb < it.kb1; ++kb) {
-          bool ok = true;
-          if (lane == 0) ok = mbar_wait(&tempty[acc], aph ^ 1u, lim) && mbar_wait(&full[stage], ph, lim);
-          ok = __shfl_sync(0xffffffffu, ok, 0) && !*abort_flag;
-          if (!ok) {
-            if (lane == 0) give_up(a, abort_flag);
+        const float* sa[4];
+        bool valid[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const int i = it.m * BM + r0 + 32 * h;  // rows past the group's end take zeros
+          valid[h] = i < it.rows;
+          sa[h] = a.a_scale + (size_t)(it.row0 + (valid[h] ? i : 0)) * a.a_blocks;
+        }
+        // the scale rows of B: gate and up of N tile nt, or two blocks of 128 columns
+        const size_t g0 = MODE == kF8Dense || it.shared ? 0 : (size_t)it.g * a.b_blocks;
+        const float* sb0 = (it.shared ? a.b_scale2 : a.b_scale0) +
+                           (g0 + (MODE == kF8GateUp ? it.nt : 2 * it.nt)) * KB;
+        const float* sb1 = MODE == kF8GateUp
+                               ? (it.shared ? a.b_scale3 : a.b_scale1) + (g0 + it.nt) * KB
+                               : (it.shared ? a.b_scale2 : a.b_scale0) +
+                                     (g0 + min(2 * it.nt + 1, a.b_blocks - 1)) * KB;
+        for (int k0 = it.kb0; k0 < it.kb1; k0 += kChunk) {
+          if (!warp_wait(&cempty[cb], cph ^ 1u, a, abort_flag)) {
             alive = false;
             break;
           }
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t d = tmem_base + (uint32_t)(acc * BN);
-            const uint32_t a_base = smem_u32(sA + stage * kStageA), b_base = smem_u32(sB + stage * kStageB);
-  #pragma unroll
-            for (int k = 0; k < BK / 32; ++k)
-              mma_f8(d, sw128_desc(a_base + k * 32), sw128_desc(b_base + k * 32), k != 0 ? 1u : 0u);
-            mma_commit(&empty[stage]);
-            mma_commit(&tfull[acc]);
+          const int n = min(kChunk, it.kb1 - k0);
+#pragma unroll
+          for (int j = 0; j < kChunk; ++j)
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+              if (j < n)
+                copy4_async(sScale + (cb * kChunk + j) * BM + r0 + 32 * h, sa[h] + k0 + j, valid[h]);
+          if (r0 < 2 * n)
+            copy4_async(sScaleB + cb * kChunk * 2 + r0, ((r0 & 1) ? sb1 : sb0) + k0 + (r0 >> 1), true);
+          copies_arrive(&cfull[cb]);
+          if (++cb == kChunks) {
+            cb = 0;
+            cph ^= 1u;
           }
-          __syncwarp();
-          if (++stage == kStages) {
-            stage = 0;
-            ph ^= 1u;
-          }
-          acc ^= 1;
-          if (acc == 0) aph ^= 1u;
         }
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     // -------------------------------------------------------------- epilogue
     const int q = warp & 3;             // TMEM lane quarter this warp may access
-    const int half = (warp - kEpiWarp0) >> 2;  // half of the tile's columns
+    const int part = (warp - kEpiWarp0) >> 2;  // this warp's columns of the tile
     const int r = q * 32 + lane;
     const uint32_t tq = tmem_base + ((uint32_t)(q * 32) << 16);
-    int acc = 0;
-    uint32_t aph = 0, xph = 0;
+    int acc = 0, cb = 0;
+    uint32_t aph = 0, cph = 0, xph = 0;
     bool alive = true;
+    Item next = item_at<MODE>(a, min((int)blockIdx.x, total - 1), n_rb, KB);
     for (int t = blockIdx.x; t < total && alive; t += gridDim.x) {
-      const Item it = item_at<MODE>(a, t, n_rb, KB);
+      const Item it = next;
+      if (t + (int)gridDim.x < total) next = item_at<MODE>(a, t + gridDim.x, n_rb, KB);
       const int i = it.m * BM + r;  // row inside the group
       const bool valid = i < it.rows;
-      // rows past the group's end take the scale zero: their sums are never
-      // stored
-      const float* sap = a.a_scale + (size_t)(it.row0 + (valid ? i : 0)) * a.a_blocks;
-      // the scale rows of B: gate and up of N tile nt, or this half's 128 columns
-      const int sb_row = MODE == kF8GateUp ? it.nt : min(2 * it.nt + half, a.b_blocks - 1);
-      const size_t sb_at =
-          ((MODE == kF8Dense || it.shared ? 0 : (size_t)it.g * a.b_blocks) + sb_row) * KB;
-      const float* sb0 = (it.shared ? a.b_scale2 : a.b_scale0) + sb_at;
-      const float* sb1 = (it.shared ? a.b_scale3 : a.b_scale1) + sb_at;
-      uint64_t sum[64];
+      float al = 0.f;  // down: the row's weight, in flight during the steps
+      if (MODE == kF8Down && valid) al = it.shared ? a.s_shared[i] : a.alpha[a.perm[it.row0 + i]];
+      float sum[kPartCols];
 #pragma unroll
-      for (int j = 0; j < 64; ++j) sum[j] = 0;
-      float sa = valid ? sap[it.kb0] : 0.f, s0 = __ldg(sb0 + it.kb0);
-      float s1 = MODE == kF8GateUp ? __ldg(sb1 + it.kb0) : 0.f;
+      for (int j = 0; j < kPartCols; ++j) sum[j] = 0.f;
       for (int kb = it.kb0; kb < it.kb1; ++kb) {
-        const uint64_t c0 = both(sa * s0), c1 = both(sa * s1);
-        if (kb + 1 < it.kb1) {
-          sa = valid ? sap[kb + 1] : 0.f;
-          s0 = __ldg(sb0 + kb + 1);
-          if (MODE == kF8GateUp) s1 = __ldg(sb1 + kb + 1);
+        const int step = (kb - it.kb0) & (kChunk - 1);
+        if (step == 0) {
+          if (!warp_wait(&cfull[cb], cph, a, abort_flag)) {
+            alive = false;
+            break;
+          }
         }
-        bool ok = lane == 0 ? mbar_wait(&tfull[acc], aph, lim) : true;
-        ok = __shfl_sync(0xffffffffu, ok, 0) && !*abort_flag;
-        if (!ok) {
-          if (lane == 0) give_up(a, abort_flag);
+        const float sa = sScale[(cb * kChunk + step) * BM + r];
+        const float* sb = sScaleB + (cb * kChunk + step) * 2;
+        const float c0 = sa * sb[MODE == kF8GateUp ? 0 : part >> 1];
+        const float c1 = MODE == kF8GateUp ? sa * sb[1] : c0;
+        if (!warp_wait(&tfull[acc], aph, a, abort_flag)) {
           alive = false;
           break;
         }
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const int col = MODE == kF8GateUp ? (c >> 1) * 128 + half * 64 + (c & 1) * 32
-                                            : half * 128 + c * 32;
-          uint32_t v[32];
-          tmem_ld32(tq + (uint32_t)(acc * BN + col), v);
+          // gate/up: 32 gate columns and the same 32 of up
+          const int col = MODE == kF8GateUp ? (c >> 1) * 128 + part * 32 + (c & 1) * 16
+                                            : part * kPartCols + c * 16;
+          uint32_t v[16];
+          tmem_ld16(tq + (uint32_t)(acc * BN + col), v);
           tmem_ld_wait();
-          const uint64_t s = MODE == kF8GateUp && c >= 2 ? c1 : c0;
+          const float s = c >= 2 ? c1 : c0;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) fma2(sum[c * 16 + j], v[2 * j], v[2 * j + 1], s);
+          for (int j = 0; j < 16; ++j) sum[c * 16 + j] = fmaf(__uint_as_float(v[j]), s, sum[c * 16 + j]);
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&tempty[acc]);
         acc ^= 1;
         if (acc == 0) aph ^= 1u;
+        if (step == kChunk - 1 || kb == it.kb1 - 1) {
+          if (lane == 0) mbar_arrive(&cempty[cb]);
+          if (++cb == kChunks) {
+            cb = 0;
+            cph ^= 1u;
+          }
+        }
       }
       if (!alive) break;
       if (MODE == kF8GateUp) {
-        // h = silu(gate) * up for this half's 64 columns, in place
-        const int left = a.n_cols - it.nt * 128 - half * 64;  // valid columns (16s)
+        // h = silu(gate) * up for this warp's 32 columns, in place
+        const int left = a.n_cols - it.nt * 128 - part * 32;  // valid columns (16s)
         uint32_t m = 0;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          const float h0 = siluf_(lo(sum[j])) * lo(sum[32 + j]);
-          const float h1 = siluf_(hi(sum[j])) * hi(sum[32 + j]);
-          sum[j] = (uint64_t)__float_as_uint(h1) << 32 | __float_as_uint(h0);
-          if (2 * j < left) m = max(m, max(f8_mag(h0), f8_mag(h1)));
+          sum[j] = siluf_(sum[j]) * sum[32 + j];
+          if (j < left) m = max(m, f8_mag(sum[j]));
         }
-        uint32_t* mx = sMax + xph * 2 * BM;
-        mx[half * BM + r] = m;
+        uint32_t* mx = sMax + xph * kParts * BM + r;
+        mx[part * BM] = m;
         __syncwarp();
-        bool ok = true;
-        if (lane == 0) {
-          mbar_arrive(xbar);
-          ok = mbar_wait(xbar, xph, lim);
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) {
-          if (lane == 0) give_up(a, abort_flag);
-          break;
-        }
-        __syncwarp();
-        const uint32_t sbits = f8_scale_bits(max(m, mx[(half ^ 1) * BM + r]));
+        if (lane == 0) mbar_arrive(xbar);
+        if (!warp_wait(xbar, xph, a, abort_flag)) break;
+#pragma unroll
+        for (int z = 0; z < kParts; ++z) m = max(m, mx[z * BM]);
+        const uint32_t sbits = f8_scale_bits(m);
         const float inv = f8_inverse(sbits);
         xph ^= 1u;
         if (valid) {
           const size_t row = (size_t)it.row0 + i;
-          uint8_t* dst = static_cast<uint8_t*>(a.out) + row * a.ldo + it.nt * 128 + half * 64;
+          uint8_t* dst = static_cast<uint8_t*>(a.out) + row * a.ldo + it.nt * 128 + part * 32;
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
+          for (int v = 0; v < 2; ++v) {
             if (16 * v < left) {
               uint32_t w[4];
 #pragma unroll
               for (int z = 0; z < 4; ++z) {
-                const uint64_t p = sum[8 * v + 2 * z], p2 = sum[8 * v + 2 * z + 1];
-                w[z] = f8_pack4(lo(p) * inv, hi(p) * inv, lo(p2) * inv, hi(p2) * inv);
+                const float* h = sum + 16 * v + 4 * z;
+                w[z] = f8_pack4(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
               }
               st_global_v4(dst + 16 * v, w[0], w[1], w[2], w[3]);
             }
           }
-          if (half == 0) a.out_scale[row * a.out_blocks + it.nt] = __uint_as_float(sbits);
+          if (part == 0) a.out_scale[row * a.out_blocks + it.nt] = __uint_as_float(sbits);
         }
       } else if (MODE == kF8Down) {
         if (valid) {
-          const float al = it.shared ? a.s_shared[i] : a.alpha[a.perm[it.row0 + i]];
-          const int col = it.nt * BN + half * 128;
+          const int col = it.nt * BN + part * kPartCols;
           __nv_bfloat16* dst =
               static_cast<__nv_bfloat16*>(a.out) + ((size_t)it.row0 + i) * a.ldo + col;
 #pragma unroll
-          for (int v = 0; v < 16; ++v) {
+          for (int v = 0; v < kPartCols / 8; ++v) {
             if (col + 8 * v < a.n_cols) {
               uint32_t w[4];
 #pragma unroll
               for (int z = 0; z < 4; ++z)
-                w[z] = pack_bf16x2(al * lo(sum[4 * v + z]), al * hi(sum[4 * v + z]));
+                w[z] = pack_bf16x2(al * sum[8 * v + 2 * z], al * sum[8 * v + 2 * z + 1]);
               st_global_v4(dst + 8 * v, w[0], w[1], w[2], w[3]);
             }
           }
         }
       } else {
-        const int col = it.nt * BN + half * 128;
+        const int col = it.nt * BN + part * kPartCols;
         bool write = true;
         if (a.ksplit > 1) {
-          // this warp's 32 rows x 128 columns of the tile, fp32, columns in
+          // this warp's 32 rows x 64 columns of the tile, fp32, columns in
           // fours: [split][tile][64 column groups][128 rows]
           const int tiles = n_rb * a.n_tiles;
-          float4* mine = a.partial + (((size_t)it.split * tiles + it.tile) * 64 + half * 32) * BM + r;
+          float4* mine = a.partial + (((size_t)it.split * tiles + it.tile) * 64 + part * 16) * BM + r;
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
+          for (int j = 0; j < kPartCols / 4; ++j)
             if (valid)
-              __stcg(mine + (size_t)j * BM, make_float4(lo(sum[2 * j]), hi(sum[2 * j]),
-                                                        lo(sum[2 * j + 1]), hi(sum[2 * j + 1])));
+              __stcg(mine + (size_t)j * BM, make_float4(sum[4 * j], sum[4 * j + 1], sum[4 * j + 2],
+                                                        sum[4 * j + 3]));
           __threadfence();
           __syncwarp();
           unsigned prev = 0;
@@ -418,15 +492,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) *ctr = 0u;
             __threadfence();
 #pragma unroll
-            for (int j = 0; j < 64; ++j) sum[j] = 0;
+            for (int j = 0; j < kPartCols; ++j) sum[j] = 0.f;
             for (int s = 0; s < a.ksplit; ++s) {
-              const float4* o = a.partial + (((size_t)s * tiles + it.tile) * 64 + half * 32) * BM + r;
+              const float4* o = a.partial + (((size_t)s * tiles + it.tile) * 64 + part * 16) * BM + r;
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
+              for (int j = 0; j < kPartCols / 4; ++j) {
                 const float4 p = valid ? __ldcg(o + (size_t)j * BM) : make_float4(0.f, 0.f, 0.f, 0.f);
-                const uint64_t one = both(1.f);
-                fma2(sum[2 * j], __float_as_uint(p.x), __float_as_uint(p.y), one);
-                fma2(sum[2 * j + 1], __float_as_uint(p.z), __float_as_uint(p.w), one);
+                sum[4 * j] += p.x;
+                sum[4 * j + 1] += p.y;
+                sum[4 * j + 2] += p.z;
+                sum[4 * j + 3] += p.w;
               }
             }
           }
@@ -435,35 +510,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (a.out_bf16) {
             __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (size_t)i * a.ldo + col;
 #pragma unroll
-            for (int v = 0; v < 16; ++v) {
+            for (int v = 0; v < kPartCols / 8; ++v) {
               if (a.out_vec && col + 8 * v + 8 <= a.n_cols) {
                 uint32_t w[4];
 #pragma unroll
-                for (int z = 0; z < 4; ++z) w[z] = pack_bf16x2(lo(sum[4 * v + z]), hi(sum[4 * v + z]));
+                for (int z = 0; z < 4; ++z) w[z] = pack_bf16x2(sum[8 * v + 2 * z], sum[8 * v + 2 * z + 1]);
                 st_global_v4(dst + 8 * v, w[0], w[1], w[2], w[3]);
               } else {
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                  const int c = 8 * v + 2 * z;
-                  if (col + c < a.n_cols) dst[c] = __float2bfloat16_rn(lo(sum[4 * v + z]));
-                  if (col + c + 1 < a.n_cols) dst[c + 1] = __float2bfloat16_rn(hi(sum[4 * v + z]));
-                }
+                for (int z = 0; z < 8; ++z)
+                  if (col + 8 * v + z < a.n_cols) dst[8 * v + z] = __float2bfloat16_rn(sum[8 * v + z]);
               }
             }
           } else {
             float* dst = static_cast<float*>(a.out) + (size_t)i * a.ldo + col;
 #pragma unroll
-            for (int v = 0; v < 32; ++v) {
+            for (int v = 0; v < kPartCols / 4; ++v) {
               if (a.out_vec && col + 4 * v + 4 <= a.n_cols) {
-                st_global_v4(dst + 4 * v, (uint32_t)sum[2 * v], (uint32_t)(sum[2 * v] >> 32),
-                             (uint32_t)sum[2 * v + 1], (uint32_t)(sum[2 * v + 1] >> 32));
+                *reinterpret_cast<float4*>(dst + 4 * v) =
+                    make_float4(sum[4 * v], sum[4 * v + 1], sum[4 * v + 2], sum[4 * v + 3]);
               } else {
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                  const int c = 4 * v + 2 * z;
-                  if (col + c < a.n_cols) dst[c] = lo(sum[2 * v + z]);
-                  if (col + c + 1 < a.n_cols) dst[c + 1] = hi(sum[2 * v + z]);
-                }
+                for (int z = 0; z < 4; ++z)
+                  if (col + 4 * v + z < a.n_cols) dst[4 * v + z] = sum[4 * v + z];
               }
             }
           }
@@ -472,6 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  asm volatile("cp.async.wait_all;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   if (*abort_flag && threadIdx.x == 0) {

@@ -264,6 +264,7 @@ cudaError_t launch_f8_few_matmul(const F8MatmulArgs& a, cudaStream_t st);
 
 // Tensor-core products (fp8_tc.cu).
 enum F8Mode { kF8GateUp = 0, kF8Down = 1, kF8Dense = 2 };
+constexpr int kF8TileCounters = 16;  // one per epilogue warp
 struct F8TcArgs {
   const int2* rowblocks;       // grouped: (group, row block) list
   const int32_t* n_rowblocks;
@@ -277,7 +278,7 @@ struct F8TcArgs {
   void* out;                   // codes | bf16 rows | dense out
   float* out_scale;            // gate/up: [rows][out_blocks]
   float4* partial;             // dense, ksplit > 1
-  unsigned* counters;          // dense, ksplit > 1: [tiles][8], zero between launches
+  unsigned* counters;          // dense, ksplit > 1: [tiles][kF8TileCounters], zero between launches
   Ctrl* ctrl;
   int E, T, P, K;
   int rows;                    // dense: rows of A

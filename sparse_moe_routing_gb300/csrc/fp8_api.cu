@@ -191,9 +191,24 @@ moe_status_t enqueue_few(const void* x, const float* r_attn, const int32_t* ids,
   a.hblocks = p.hblocks;
   a.ldh = p.hblocks * kF8Block;
   a.out_bf16 = out_dtype == MOE_BF16;
-  cudaError_t e = run_kernel(MOE_KERNEL_F8_FEW_GATEUP, st, [&] { return launch_f8_few_gateup(a, st); });
+  const uint64_t E = a.E, d = a.d, I = a.I, Is = a.Is, rows = (uint64_t)a.T * a.k + a.T;
+  F8FewMaps m;
+  bool ok = f8_make_map(&m.g, a.Wg, E * I, d, d, 16) && f8_make_map(&m.u, a.Wu, E * I, d, d, 16) &&
+            f8_make_map(&m.w, a.Wd, E * d, I, I, 16) && f8_make_map(&m.x, a.Hq, rows, a.ldh, a.ldh, 8);
+  if (ok && Is)
+    ok = f8_make_map(&m.sg, a.Wsg, Is, d, d, 16) && f8_make_map(&m.su, a.Wsu, Is, d, d, 16) &&
+         f8_make_map(&m.sw, a.Wsd, d, Is, Is, 16);
+  if (!ok) return MOE_ERR_CUDA;
+  if (!Is) {
+    m.sg = m.g;
+    m.su = m.u;
+    m.sw = m.w;
+  }
+  m.sx = m.x;
+  cudaError_t e =
+      run_kernel(MOE_KERNEL_F8_FEW_GATEUP, st, [&] { return launch_f8_few_gateup(m, a, st); });
   if (e != cudaSuccess) return MOE_ERR_CUDA;
-  return cuda_status(run_kernel(MOE_KERNEL_F8_FEW_DOWN, st, [&] { return launch_f8_few_down(a, st); }));
+  return cuda_status(run_kernel(MOE_KERNEL_F8_FEW_DOWN, st, [&] { return launch_f8_few_down(m, a, st); }));
 }
 
 moe_status_t enqueue_bucket(const int32_t* ids, const moe_cfg_t* c, const RoutePlan& r,
@@ -405,7 +420,8 @@ moe_status_t moe_fp8_matmul(const void* a, const float* a_scale, const void* b, 
   cudaStream_t st = (cudaStream_t)stream;
   if (mm->M <= kF8FewTokens) {
     const F8MatmulArgs f{static_cast<const uint8_t*>(a), a_scale, static_cast<const uint8_t*>(b),
-                         b_scale, out, mm->M, mm->N, mm->K, bf16 ? 1 : 0, mm->lda, mm->ldb, mm->ldo};
+                         b_scale, out, static_cast<Ctrl*>(mm->workspace), mm->M, mm->N, mm->K, bf16 ? 1 : 0,
+                         mm->lda, mm->ldb, mm->ldo};
     return cuda_status(run_kernel(MOE_KERNEL_F8_MATMUL, st, [&] { return launch_f8_few_matmul(f, st); }));
   }
   F8TcMaps m{};

@@ -5,9 +5,13 @@
 // HBM and, for one token, by latency. mma.sync m16n8k32 takes 16 weight rows
 // as its m side and up to 8 tokens as its n side. A contraction does not care
 // in which order k is visited as long as both operands agree, so a lane's
-// fragment registers are simply the 16-byte pieces that it loads from memory:
-// no shared-memory staging, no conversion, no shuffles. A warp keeps
-// kAhead blocks of 16 rows x 128 k in flight in registers.
+// fragment registers are simply 16-byte pieces of the rows: no conversion, no
+// shuffles. Every warp owns a ring of slots that its lane 0 fills by TMA
+// (128-byte swizzle). What such a stream can lose to is instruction issue: an
+// SM has some 350 issue slots for every 2 KB that HBM brings it. So a slot holds
+// two blocks of k, and a gate/up item two m16 tiles (with single blocks and
+// tiles, whether loaded into registers, by cp.async or by TMA, 280 instructions
+// per 2 KB kept 8 tokens of the 256-expert shape at 3 TB/s).
 //
 // The products of one 128-wide block are summed by the tensor core and then
 // scaled by the block's two scales into fp32 sums held in registers.
@@ -15,8 +19,8 @@
 // The layer takes two kernels:
 //  1. f8_few_gateup: every CTA groups the (token, slot) pairs by expert into
 //     chunks of at most 8 (ranking by counting), quantises the tokens into
-//     shared memory, then takes items of 8 gate and 8 up rows of a chunk's
-//     expert (one m16 tile, so a lane holds a row's gate and up sums). The
+//     shared memory, then takes items of 16 gate and 16 up rows of a chunk's
+//     expert (eight and eight make an m16 tile, so a lane holds a row's gate and up sums). The
 //     warps split k; their sums meet in shared memory and are added in warp
 //     order. h needs one scale per 128 columns, which 16 items share: the item
 //     that finishes a block last (a counter that it also resets) quantises it.
@@ -24,6 +28,7 @@
 //     slots, the shared expert and the residual in a fixed order.
 #include "fp8_common.cuh"
 #include "kernels.h"
+#include "tc_ptx.cuh"
 
 namespace moe {
 namespace {
@@ -39,19 +44,24 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma_e4m3_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                               uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // One block of 128 k: rows g and g + 8 of the m16 tile, two 16-byte pieces
 // each (k 16 t.. and k 64 + 16 t.. for t = lane % 4).
 struct WeightBlock {
   uint4 lo[2], hi[2];
 };
-struct ActBlock {
-  uint4 v[2];
-};
 
 __device__ __forceinline__ void block_mma(float (&d)[4], const WeightBlock& w, const uint4& b0,
                                           const uint4& b1) {
-  d[0] = d[1] = d[2] = d[3] = 0.f;
-  mma_e4m3(d, w.lo[0].x, w.hi[0].x, w.lo[0].y, w.hi[0].y, b0.x, b0.y);
+  mma_e4m3_first(d, w.lo[0].x, w.hi[0].x, w.lo[0].y, w.hi[0].y, b0.x, b0.y);
   mma_e4m3(d, w.lo[0].z, w.hi[0].z, w.lo[0].w, w.hi[0].w, b0.z, b0.w);
   mma_e4m3(d, w.lo[1].x, w.hi[1].x, w.lo[1].y, w.hi[1].y, b1.x, b1.y);
   mma_e4m3(d, w.lo[1].z, w.hi[1].z, w.lo[1].w, w.hi[1].w, b1.z, b1.w);
@@ -59,57 +69,106 @@ __device__ __forceinline__ void block_mma(float (&d)[4], const WeightBlock& w, c
 
 __device__ __forceinline__ uint4 zero4() { return make_uint4(0u, 0u, 0u, 0u); }
 
-// Bytes of a 16-byte piece past the first n zeroed (n <= 0: all of them). A
-// code past the end of a row may be NaN, and NaN times zero is NaN, so both
-// operands are cut.
-__device__ __forceinline__ uint4 keep_bytes(uint4 v, int n) {
-  if (n >= 16) return v;
-  auto cut = [](uint32_t w, int m) { return m >= 4 ? w : (m <= 0 ? 0u : w & ((1u << (8 * m)) - 1u)); };
-  return make_uint4(cut(v.x, n), cut(v.y, n - 4), cut(v.z, n - 8), cut(v.w, n - 12));
+// Scales come by 4-byte asynchronous copies; each copying lane arrives on the
+// slot's barrier once its copy has landed.
+__device__ __forceinline__ void copy4(float* dst, const float* src, uint64_t* bar) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
+}
+template <int OFF>
+__device__ __forceinline__ uint4 lds16(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4 + %5];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(src), "n"(OFF)
+               : "memory");
+  return v;
+}
+template <int OFF>
+__device__ __forceinline__ float lds4(uint32_t src) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1 + %2];" : "=f"(v) : "r"(src), "n"(OFF) : "memory");
+  return v;
+}
+// The generic reads of a slot come before the copies that refill it.
+__device__ __forceinline__ void reads_before_refill() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// A box of rows of 128 bytes, 1024-byte aligned; TMA puts piece p (16 bytes) of
+// row r at p ^ (r % 8).
+constexpr int kBox8 = 1024, kBox16 = 2048;
+// A lane's pieces t and t + 4 of row g lie at get and get ^ 64.
+__device__ __forceinline__ uint32_t get_at(int g, int t) { return (uint32_t)(g * 128 + ((t ^ g) << 4)); }
+
+// The m16 tile of eight rows at `lo` and eight at `hi` (box rows, shared memory).
+__device__ __forceinline__ WeightBlock weights_of(uint32_t lo, uint32_t hi, uint32_t get) {
+  WeightBlock w;
+  w.lo[0] = lds16<0>(lo + get);
+  w.lo[1] = lds16<0>(lo + (get ^ 64u));
+  w.hi[0] = lds16<0>(hi + get);
+  w.hi[1] = lds16<0>(hi + (get ^ 64u));
+  return w;
+}
+
+__device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~static_cast<uintptr_t>(1023));
 }
 
 // ---------------------------------------------------------------------------
 // chunks of at most 8 pairs of one expert, then of 8 tokens for the shared one
 // ---------------------------------------------------------------------------
 struct FewLists {
-  alignas(16) int ids[kFewMaxPairs + 4];
+  alignas(16) short ids[kFewMaxPairs];
+  short sorted[kFewMaxPairs];          // position -> pair
+  short pos[kFewMaxPairs];             // pair -> position
+  short token[kFewMaxPairs];           // position -> token
+  short start[kFewMaxPairs + 8];       // chunk -> first position (shared: first token)
+  short expert[kFewMaxPairs + 8];      // chunk -> expert (E: shared)
+  short count[kFewMaxPairs + 8];       // chunk -> pairs in it
+  unsigned char first[kFewMaxPairs];   // position starts a chunk
   int n_routed, n_chunks;
-  int sorted[kFewMaxPairs];          // position -> pair
-  int pos[kFewMaxPairs];             // pair -> position
-  int start[kFewMaxPairs + 8];       // chunk -> first position (shared: first token)
-  int expert[kFewMaxPairs + 8];      // chunk -> expert (E: shared)
-  int count[kFewMaxPairs + 8];       // chunk -> pairs in it
-  unsigned char first[kFewMaxPairs]; // position starts a chunk
 };
 
-// Positions order the pairs by (expert, pair). All threads of the CTA call it.
+// Positions order the pairs by (expert, pair). The first N threads of the CTA
+// call it; it ends with a barrier of them.
+template <int N>
+__device__ __forceinline__ void lists_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+}
+template <int N>
 __device__ __forceinline__ void build_lists(const F8ExpertsArgs& a, FewLists& L) {
   const int P = a.T * a.k, tid = threadIdx.x, lane = tid & 31;
   bool bad = false;
-  for (int i = tid; i < ((P + 3) & ~3); i += blockDim.x) {
-    int e = i < P ? __ldcg(a.ids + i) : 0x7FFFFFFF;
+  for (int i = tid; i < ((P + 7) & ~7); i += N) {
+    int e = i < P ? __ldcg(a.ids + i) : 0x7FFF;
     if (i < P && (e < 0 || e >= a.E)) {
       bad = true;
       e = a.E - 1;
     }
-    L.ids[i] = e;
+    L.ids[i] = (short)e;
   }
   if (__any_sync(0xffffffffu, bad) && lane == 0) report(a.ctrl, kDevBadId, kSiteFewFp8);
-  __syncthreads();
-  for (int i = tid; i < P; i += blockDim.x) {
+  lists_sync<N>();
+  for (int i = tid; i < P; i += N) {
     const int e = L.ids[i];
     int below = 0, same = 0;
-    for (int j = 0; j < P; j += 4) {
-      const int4 o = *reinterpret_cast<const int4*>(L.ids + j);
-      below += (o.x < e) + (o.y < e) + (o.z < e) + (o.w < e);
-      same += (o.x == e && j < i) + (o.y == e && j + 1 < i) + (o.z == e && j + 2 < i) +
-              (o.w == e && j + 3 < i);
+    for (int j = 0; j < P; j += 8) {
+      const uint4 o = *reinterpret_cast<const uint4*>(L.ids + j);
+      const uint32_t v[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int id = (int)((v[q >> 1] >> (16 * (q & 1))) & 0xFFFFu);
+        below += id < e;
+        same += id == e && j + q < i;
+      }
     }
-    L.sorted[below + same] = i;
-    L.pos[i] = below + same;
+    L.sorted[below + same] = (short)i;
+    L.pos[i] = (short)(below + same);
+    L.token[below + same] = (short)(i / a.k);
     L.first[below + same] = (same & 7) == 0;
   }
-  __syncthreads();
+  lists_sync<N>();
   if (tid < 32) {
     int n = 0;
     for (int r0 = 0; r0 < P; r0 += 32) {
@@ -117,204 +176,329 @@ __device__ __forceinline__ void build_lists(const F8ExpertsArgs& a, FewLists& L)
       const unsigned m = __ballot_sync(0xffffffffu, f);
       if (f) {
         const int c = n + __popc(m & ((1u << lane) - 1u));
-        L.start[c] = r0 + lane;
+        L.start[c] = (short)(r0 + lane);
         L.expert[c] = L.ids[L.sorted[r0 + lane]];
       }
       n += __popc(m);
     }
     __syncwarp();
-    for (int c = lane; c < n; c += 32) L.count[c] = (c + 1 < n ? L.start[c + 1] : P) - L.start[c];
+    for (int c = lane; c < n; c += 32) L.count[c] = (short)((c + 1 < n ? L.start[c + 1] : P) - L.start[c]);
     const int ns = a.Is > 0 ? (a.T + 7) / 8 : 0;
     if (lane < ns) {
-      L.start[n + lane] = 8 * lane;
-      L.expert[n + lane] = a.E;
-      L.count[n + lane] = min(8, a.T - 8 * lane);
+      L.start[n + lane] = (short)(8 * lane);
+      L.expert[n + lane] = (short)a.E;
+      L.count[n + lane] = (short)min(8, a.T - 8 * lane);
     }
     if (lane == 0) {
       L.n_routed = n;
       L.n_chunks = n + ns;
     }
   }
-  __syncthreads();
+  lists_sync<N>();
 }
 
 // ---------------------------------------------------------------------------
 // 1. gate/up
 // ---------------------------------------------------------------------------
-constexpr int kGuWarps = 16;
-constexpr int kGuAhead = 4;
+// Eight streaming warps share an item (16 gate and 16 up rows of a chunk's
+// expert) along k, two blocks of 128 each: whole rows are in flight at a time,
+// which DRAM's pages want. Rows shorter than sixteen blocks are shared by fewer
+// warps, and more items are in flight. Four finishing warps take the items in
+// turn: one adds an item's partial sums, applies SwiGLU, stores h and counts
+// the block's items, so that the streaming warps never wait for a store, a
+// fence or an atomic (with a streaming warp finishing each item behind a CTA
+// barrier, 8 tokens of the 256-expert shape took 102 us here).
+constexpr int kGuWarps = 8, kGuFinish = 4;
+constexpr int kGuThreads = 32 * (kGuWarps + kGuFinish);
+constexpr int kGuRows = 16;                   // rows of gate, and of up, in an item
+constexpr int kGuAhead = 2;                   // slots per warp: 128 KB per SM
+constexpr int kGuSlot = 4 * kBox16;           // gate and up of two blocks
+constexpr int kGuArrivals = 5;                // the boxes' bytes, four scales
 
-struct GuItem {
-  int chunk, rb;  // chunk and block of 8 rows
+// SLOTS: items of a group between its warps and the finishers; four where
+// shared memory has room beside the tokens' codes, else two.
+template <int SLOTS>
+struct GuShared {
+  uint8_t ring[kGuWarps][kGuAhead][kGuSlot];
+  float4 part[SLOTS][kGuWarps][2][32];
+  uint64_t landed[kGuWarps][kGuAhead];
+  uint64_t full[SLOTS][kGuWarps], empty[SLOTS][kGuWarps];  // by group
+  float scale[kGuWarps][kGuAhead][4];                      // gate, up of two blocks
+  FewLists lists;
+  alignas(16) float xs[1];  // [T][KB], then the codes
 };
 
-struct GuUnit {
-  WeightBlock w;
-  float sg, su;
-};
-
-__global__ void __launch_bounds__(kGuWarps * 32, 1) f8_few_gateup_kernel(F8ExpertsArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  FewLists& L = *reinterpret_cast<FewLists*>(smem);
-  float4* part = reinterpret_cast<float4*>(smem + few_lists_bytes());  // [2][kGuWarps][32]
+template <int SLOTS>
+__global__ void __launch_bounds__(kGuThreads, 1)
+    f8_few_gateup_kernel(const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmU,
+                         const __grid_constant__ CUtensorMap tmSG, const __grid_constant__ CUtensorMap tmSU,
+                         const F8ExpertsArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  GuShared<SLOTS>& S = *reinterpret_cast<GuShared<SLOTS>*>(align1024(smem_raw));
+  FewLists& L = S.lists;
   const int KB = f8_blocks(a.d);
-  float* xs = reinterpret_cast<float*>(part + 2 * kGuWarps * 32);     // [T][KB]
+  float* xs = S.xs;                        // [T][KB]
   const int xstride = KB * kF8Block + 64;  // rows 64 B apart modulo the banks' 128 B
   uint8_t* xq = reinterpret_cast<uint8_t*>(xs) + ((a.T * KB * 4 + 15) & ~15);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int pairs = (KB + 1) / 2;
+  const int nsplit = pairs >= 8 ? 8 : (pairs >= 4 ? 4 : 2);  // warps of an item
+  const int groups = kGuWarps / nsplit;
+  if (tid == 0) {
+    for (int i = 0; i < kGuWarps * SLOTS; ++i) {
+      tc::mbar_init(&S.full[0][0] + i, nsplit);
+      tc::mbar_init(&S.empty[0][0] + i, 1);
+    }
+    for (int i = 0; i < kGuWarps * kGuAhead; ++i) tc::mbar_init(&S.landed[0][0] + i, kGuArrivals);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   pdl_wait();
   pdl_trigger();
-  build_lists(a, L);
 
-  // wpi warps share an item along k, the others take other items
-  int wpi = 1;
-  while (wpi * 2 <= KB && wpi < kGuWarps) wpi *= 2;
-  const int slots = kGuWarps / wpi, slot = warp / wpi, w = warp % wpi;
-  const int RB = a.I / 8, RBs = a.Is / 8;
-  const int routed_items = L.n_routed * RB;
-  const int items = routed_items + (L.n_chunks - L.n_routed) * RBs;
-  const int stride = (int)gridDim.x * slots;
-  const int rounds = (items + stride - 1) / stride;
-  const int steps = (KB + wpi - 1) / wpi;  // blocks of an item per warp
-  const int units = rounds * steps;
-  auto item_at = [&](int i) {
-    GuItem it;
-    if (i < routed_items) {
-      it.chunk = i / RB;
-      it.rb = i - it.chunk * RB;
-    } else {
-      const int j = i - routed_items;
-      it.chunk = L.n_routed + j / RBs;
-      it.rb = j - (j / RBs) * RBs;
-    }
-    return it;
+  // item i: 16 rows `rb` of chunk `c`; a group's items are `stride` apart
+  const int RB = a.I / kGuRows, RBs = a.Is / kGuRows;
+  const int stride = (int)gridDim.x * groups;
+  struct Walk {
+    int i, c, rb;
   };
-  const int first = slot * (int)gridDim.x + (int)blockIdx.x;
-  auto load = [&](GuUnit& u, int n) {
-    const int r = n / steps, kb = (n - r * steps) * wpi + w;
-    const int i = first + r * stride;
-    u.w.lo[0] = u.w.lo[1] = u.w.hi[0] = u.w.hi[1] = zero4();
-    u.sg = u.su = 0.f;
-    if (n >= units || i >= items || kb >= KB) return;
-    const GuItem it = item_at(i);
-    const int e = L.expert[it.chunk];
-    const bool sh = e == a.E;
-    const int rows = sh ? a.Is : a.I;
-    const size_t row = (sh ? 0 : (size_t)e * rows) + (size_t)it.rb * 8 + g;
-    const int k0 = kb * kF8Block + 16 * t;
-    const uint8_t* pg = (sh ? a.Wsg : a.Wg) + row * a.d + k0;
-    const uint8_t* pu = (sh ? a.Wsu : a.Wu) + row * a.d + k0;
-    if (k0 < a.d) {  // d is a multiple of 16
-      u.w.lo[0] = ldg_stream(pg);
-      u.w.hi[0] = ldg_stream(pu);
+  auto settle = [&](Walk& k) {  // chunk and rows of item k.i
+    const int routed = L.n_routed * RB;
+    if (k.i < routed) {
+      k.c = k.i / RB;
+      k.rb = k.i - k.c * RB;
+    } else if (RBs) {
+      const int j = k.i - routed;
+      k.c = L.n_routed + j / RBs;
+      k.rb = j - j / RBs * RBs;
     }
-    if (k0 + 64 < a.d) {
-      u.w.lo[1] = ldg_stream(pg + 64);
-      u.w.hi[1] = ldg_stream(pu + 64);
-    }
-    const size_t si = ((sh ? 0 : (size_t)e * f8_blocks(rows)) + it.rb / 16) * KB + kb;
-    u.sg = __ldg((sh ? a.Ssg : a.Sg) + si);
-    u.su = __ldg((sh ? a.Ssu : a.Su) + si);
   };
-  GuUnit ring[kGuAhead];
-#pragma unroll
-  for (int j = 0; j < kGuAhead; ++j) load(ring[j], j);
-
-  // the tokens' codes, sixteen lanes per block of 128
-  for (int b = tid >> 4; b - ((tid >> 4) & 1) < a.T * KB; b += kGuWarps * 2) {
-    const int tok = b / KB, kb = b - tok * KB, c = kb * kF8Block + (lane & 15) * 8;
-    float v[8];
-    uint4 raw = zero4();
-    if (b < a.T * KB && c < a.d)
-      raw = *reinterpret_cast<const uint4*>(a.x + (size_t)tok * a.d + c);
-    Chunk<__nv_bfloat16>::unpack(raw, v);
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, f8_mag(v[j]));
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const uint32_t sb = f8_scale_bits(m);
-    const float inv = f8_inverse(sb);
-    if (b < a.T * KB) {
-      *reinterpret_cast<uint2*>(xq + (size_t)tok * xstride + c) =
-          make_uint2(f8_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                     f8_pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
-      if ((lane & 15) == 0) xs[b] = __uint_as_float(sb);
+  const int step_c = stride / RB, step_rb = stride - step_c * RB;
+  auto advance = [&](Walk& k) {
+    k.i += stride;
+    k.c += step_c;
+    k.rb += step_rb;
+    if (k.rb >= RB) {
+      k.rb -= RB;
+      ++k.c;
     }
-  }
-  __syncthreads();
+    if (k.c >= L.n_routed) settle(k);  // among or past the shared expert's
+  };
+  auto item_count = [&]() { return L.n_routed * RB + (L.n_chunks - L.n_routed) * RBs; };
 
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int n0 = 0; n0 < units; n0 += kGuAhead) {
-#pragma unroll
-    for (int j = 0; j < kGuAhead; ++j) {
-      const int n = n0 + j;
-      if (n >= units) break;
-      const int r = n / steps, st = n - r * steps, kb = st * wpi + w;
-      const int i = first + r * stride;
-      const bool live = i < items;
-      const GuItem it = live ? item_at(i) : GuItem{0, 0};
-      const int start = L.start[it.chunk], cnt = L.count[it.chunk];
-      const bool sh = L.expert[it.chunk] == a.E;
-      if (live && kb < KB) {
-        auto token = [&](int s) {
-          const int p = start + min(s, cnt - 1);
-          return sh ? p : L.sorted[p] / a.k;
+  if (warp < kGuWarps) {
+    const int group = warp / nsplit, w = warp % nsplit;
+    build_lists<kGuWarps * 32>(a, L);
+    const int items = item_count();
+    Walk now{group * (int)gridDim.x + (int)blockIdx.x, 0, 0};
+    settle(now);
+    // the loads' walk, kGuAhead slots ahead of the arithmetic's
+    Walk ahead = now;
+    const int steps = (pairs - w + nsplit - 1) / nsplit;  // pairs of blocks of an item for this warp
+    const CUtensorMap *mg = &tmG, *mu = &tmU;
+    const float* ps = a.Sg;  // lanes 0, 1: gate's scales, lanes 2, 3: up's
+    int todo = 0, row = 0, kb = 0;
+    auto open = [&]() {
+      todo = ahead.i < items ? steps : 0;
+      if (todo == 0) return;
+      const int e = L.expert[ahead.c];
+      const bool sh = e == a.E;
+      const int rows = sh ? a.Is : a.I;
+      row = (sh ? 0 : e * rows) + ahead.rb * kGuRows;
+      kb = 2 * w;
+      mg = sh ? &tmSG : &tmG;
+      mu = sh ? &tmSU : &tmU;
+      const int si = ((sh ? 0 : e * f8_blocks(rows)) + ahead.rb * kGuRows / kF8Block) * KB;
+      ps = (sh ? (lane & 2 ? a.Ssu : a.Ssg) : (lane & 2 ? a.Su : a.Sg)) + si;
+    };
+    uint8_t* ring = S.ring[warp][0];
+    auto load = [&](int j) {
+      if (todo == 0) return;
+      uint64_t* bar = &S.landed[warp][j];
+      if (lane == 0) {
+        uint8_t* dst = ring + j * kGuSlot;
+        const int k = kb * kF8Block;
+        tc::mbar_expect_tx(bar, kGuSlot);
+        tc::tma_load_2d(dst, mg, bar, k, row);
+        tc::tma_load_2d(dst + kBox16, mu, bar, k, row);
+        tc::tma_load_2d(dst + 2 * kBox16, mg, bar, k + kF8Block, row);  // zeros past the last block
+        tc::tma_load_2d(dst + 3 * kBox16, mu, bar, k + kF8Block, row);
+      }
+      if (lane < 4) copy4(&S.scale[warp][j][lane], ps + min(kb + (lane & 1), KB - 1), bar);
+      kb += 2 * nsplit;
+      if (--todo == 0) {
+        advance(ahead);
+        open();
+      }
+    };
+    if (steps > 0) open();
+    for (int j = 0; j < kGuAhead; ++j) load(j);
+    __syncthreads();  // the tokens' codes are there
+
+    float acc[2][4] = {};
+    const uint32_t get = get_at(g, t);
+    const uint32_t xq32 = tc::smem_u32(xq) + 2 * w * kF8Block + 16 * t, xs32 = tc::smem_u32(xs) + 8 * w;
+    const uint32_t ring32 = tc::smem_u32(ring), sc32 = tc::smem_u32(S.scale[warp]);
+    uint32_t xr = 0, x0 = 0, x1 = 0, ph = 0;
+    int left = steps, r = 0, j = 0, kx = 2 * w;
+    bool fresh = true;
+    while (now.i < items) {
+      if (fresh) {  // the chunk's tokens: this lane's column, and its two sums' columns
+        const int start = L.start[now.c], last = L.count[now.c] - 1;
+        const bool sh = now.c >= L.n_routed;
+        auto token = [&](int q) {
+          const int p = start + min(q, last);
+          return sh ? p : (int)L.token[p];
         };
-        const uint8_t* xr = xq + (size_t)token(g) * xstride + kb * kF8Block + 16 * t;
-        float d[4];
-        block_mma(d, ring[j].w, *reinterpret_cast<const uint4*>(xr),
-                  *reinterpret_cast<const uint4*>(xr + 64));
-        const float s0 = xs[token(2 * t) * KB + kb], s1 = xs[token(2 * t + 1) * KB + kb];
-        acc[0] = fmaf(d[0], ring[j].sg * s0, acc[0]);
-        acc[1] = fmaf(d[1], ring[j].sg * s1, acc[1]);
-        acc[2] = fmaf(d[2], ring[j].su * s0, acc[2]);
-        acc[3] = fmaf(d[3], ring[j].su * s1, acc[3]);
+        xr = xq32 + token(g) * xstride;
+        x0 = xs32 + token(2 * t) * KB * 4;
+        x1 = xs32 + token(2 * t + 1) * KB * 4;
+        fresh = false;
       }
-      load(ring[j], n + kGuAhead);
-      if (st != steps - 1) continue;
-      // the item's sums: all warps write, one warp of the slot adds
-      float4* buf = part + (r & 1) * kGuWarps * 32;
-      buf[warp * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-      acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-      __syncthreads();
-      if (!live || w != r % wpi) continue;
-      float4 v = buf[slot * wpi * 32 + lane];
-      for (int q = 1; q < wpi; ++q) {
-        const float4 o = buf[(slot * wpi + q) * 32 + lane];
-        v.x += o.x;
-        v.y += o.y;
-        v.z += o.z;
-        v.w += o.w;
+      if (left) {
+        if (!f8_warp_wait(&S.landed[warp][j], ph, a.ctrl, kSiteFewFp8)) break;
+        const uint32_t slot = ring32 + j * kGuSlot;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (kx + h >= KB) break;  // the last pair's second block may not exist
+          const uint4 b0 = lds16<0>(xr + h * kF8Block), b1 = lds16<64>(xr + h * kF8Block);
+          const float sg = lds4<0>(sc32 + 16 * j + 4 * h), su = lds4<8>(sc32 + 16 * j + 4 * h);
+          const float s0 = lds4<0>(x0 + 4 * h), s1 = lds4<0>(x1 + 4 * h);
+          const float c0 = sg * s0, c1 = sg * s1, c2 = su * s0, c3 = su * s1;
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const uint32_t box = slot + 2 * h * kBox16 + m * kBox8;
+            float d[4];
+            block_mma(d, weights_of(box, box + kBox16, get), b0, b1);
+            acc[m][0] = fmaf(d[0], c0, acc[m][0]);
+            acc[m][1] = fmaf(d[1], c1, acc[m][1]);
+            acc[m][2] = fmaf(d[2], c2, acc[m][2]);
+            acc[m][3] = fmaf(d[3], c3, acc[m][3]);
+          }
+        }
+        xr += 2 * nsplit * kF8Block;
+        x0 += 8 * nsplit;
+        x1 += 8 * nsplit;
+        kx += 2 * nsplit;
+        reads_before_refill();
+        __syncwarp();
+        load(j);
+        if (++j == kGuAhead) {
+          j = 0;
+          ph ^= 1u;
+        }
+        if (--left) continue;
       }
+      // the item's partial sums go to a finisher
+      const int at = r % SLOTS;
+      if (!f8_warp_wait(&S.empty[at][group], (r / SLOTS & 1) ^ 1, a.ctrl, kSiteFewFp8)) break;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        S.part[at][warp][m][lane] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
+        acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.f;
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&S.full[at][group]);
+      left = steps;
+      kx = 2 * w;
+      advance(now);
+      ++r;
+      fresh = true;
+    }
+  } else {
+    // While the others group the pairs and wait for their first weights, this
+    // warpgroup quantises the tokens: sixteen lanes per block of 128, several
+    // blocks in flight. (The streaming warps' own loads of x came back behind
+    // their loads of cold weights: 20,000 cycles before the first product at 8
+    // tokens.)
+    const int blocks = a.T * KB;
+    constexpr int kHalves = 8, kFlight = 4;
+    for (int b0 = (tid >> 4) & (kHalves - 1); b0 - ((tid >> 4) & 1) < blocks; b0 += kHalves * kFlight) {
+      uint4 raw[kFlight];
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u) {
+        const int b = b0 + u * kHalves, tok = b / KB, c = (b - tok * KB) * kF8Block + (lane & 15) * 8;
+        raw[u] = b < blocks && c < a.d
+                     ? *reinterpret_cast<const uint4*>(a.x + (size_t)tok * a.d + c) : zero4();
+      }
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u) {
+        const int b = b0 + u * kHalves, tok = b / KB, c = (b - tok * KB) * kF8Block + (lane & 15) * 8;
+        float v[8];
+        Chunk<__nv_bfloat16>::unpack(raw[u], v);
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, f8_mag(v[j]));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const uint32_t sb = f8_scale_bits(m);
+        const float inv = f8_inverse(sb);
+        if (b < blocks) {
+          *reinterpret_cast<uint2*>(xq + tok * xstride + c) =
+              make_uint2(f8_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                         f8_pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+          if ((lane & 15) == 0) xs[b] = __uint_as_float(sb);
+        }
+      }
+    }
+    __syncthreads();
+    const int items = item_count();
+    // a finisher has a slot of its group to itself: no more take turns than
+    // there are slots
+    const int group = (warp - kGuWarps) % groups, turns = min(kGuFinish / groups, SLOTS);
+    int r = 0;
+    Walk now{group * (int)gridDim.x + (int)blockIdx.x, 0, 0};
+    for (settle(now); now.i < items; advance(now), ++r) {
+      if (r % turns != (warp - kGuWarps) / groups) continue;
+      const int c = now.c, rb = now.rb, start = L.start[c], cnt = L.count[c];
+      const bool sh = L.expert[c] == a.E;
+      const int slot = r % SLOTS;
+      if (!f8_warp_wait(&S.full[slot][group], r / SLOTS & 1, a.ctrl, kSiteFewFp8)) break;
+      const float4(*part)[2][32] = S.part[slot] + group * nsplit;
+      float4 v[2];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        v[m] = part[0][m][lane];
+        for (int q = 1; q < nsplit; ++q) {
+          const float4 o = part[q][m][lane];
+          v[m].x += o.x;
+          v[m].y += o.y;
+          v[m].z += o.z;
+          v[m].w += o.w;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&S.empty[slot][group]);
       const int row0 = (sh ? a.T * a.k : 0) + start;
-      const int col = it.rb * 8 + g;
-      if (2 * t < cnt) a.Hf[(size_t)(row0 + 2 * t) * a.ldh + col] = siluf_(v.x) * v.z;
-      if (2 * t + 1 < cnt) a.Hf[(size_t)(row0 + 2 * t + 1) * a.ldh + col] = siluf_(v.y) * v.w;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        float* h = a.Hf + (size_t)(row0 + 2 * t) * a.ldh + rb * kGuRows + 8 * m + g;
+        if (2 * t < cnt) h[0] = siluf_(v[m].x) * v[m].z;
+        if (2 * t + 1 < cnt) h[a.ldh] = siluf_(v[m].y) * v[m].w;
+      }
       // the last of a block's items quantises its 128 columns
-      const int width = sh ? a.Is : a.I, blk = it.rb / 16;
-      const int need = min(16, width / 8 - blk * 16);
+      const int width = sh ? a.Is : a.I, blk = rb * kGuRows / kF8Block;
+      const int need = min(kF8Block / kGuRows, width / kGuRows - blk * (kF8Block / kGuRows));
       __threadfence();
       __syncwarp();
       unsigned prev = 0;
-      unsigned* ctr = a.counters + (size_t)it.chunk * a.hblocks + blk;
+      unsigned* ctr = a.counters + (size_t)c * a.hblocks + blk;
       if (lane == 0) prev = atomicAdd(ctr, 1u);
       prev = __shfl_sync(0xffffffffu, prev, 0);
       if ((int)prev != need - 1) continue;
       if (lane == 0) *ctr = 0u;
       __threadfence();
-      const int c = blk * kF8Block + lane * 4;
-#pragma unroll 1
-      for (int s = 0; s < cnt; ++s) {
-        const size_t at = (size_t)(row0 + s) * a.ldh + c;
+      const int hc = blk * kF8Block + lane * 4;
+#pragma unroll 4
+      for (int q = 0; q < cnt; ++q) {
+        const size_t at = (size_t)(row0 + q) * a.ldh + hc;
         float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (c < width) h = __ldcg(reinterpret_cast<const float4*>(a.Hf + at));
+        if (hc < width) h = __ldcg(reinterpret_cast<const float4*>(a.Hf + at));
         const uint32_t m = __reduce_max_sync(
             0xffffffffu, max(max(f8_mag(h.x), f8_mag(h.y)), max(f8_mag(h.z), f8_mag(h.w))));
         const uint32_t sb = f8_scale_bits(m);
         const float inv = f8_inverse(sb);
         *reinterpret_cast<uint32_t*>(a.Hq + at) = f8_pack4(h.x * inv, h.y * inv, h.z * inv, h.w * inv);
-        if (lane == 0) a.Hs[(size_t)(row0 + s) * a.hblocks + blk] = __uint_as_float(sb);
+        if (lane == 0) a.Hs[(size_t)(row0 + q) * a.hblocks + blk] = __uint_as_float(sb);
       }
     }
   }
@@ -323,140 +507,206 @@ __global__ void __launch_bounds__(kGuWarps * 32, 1) f8_few_gateup_kernel(F8Exper
 // ---------------------------------------------------------------------------
 // 2. down + combine
 // ---------------------------------------------------------------------------
-constexpr int kDnWarps = 8;
-constexpr int kDnAhead = 4;
 constexpr int kDnCols = 16;
 constexpr int kDnPitch = kDnCols + 1;
 
-// A warp's walk over (chunk, k split) and the blocks of each.
-struct DnWalk {
-  int idx, kb;
-};
-struct DnUnit {
-  WeightBlock w;
-  float sw;
-  ActBlock x;
-  float s0, s1;
+constexpr int kDnSlot = 2 * (kBox16 + kBox8);  // weights and activations of two blocks
+constexpr int kDnArrivals = 20;  // weights, activations, 18 scales
+
+// WARPS warps with AHEAD slots in flight each. Eight warps where every CTA has
+// an SM of its own (96 KB of weights in flight), four where there are more CTAs
+// than SMs, so that two fit.
+template <int WARPS, int AHEAD>
+struct DnShared {
+  uint8_t ring[WARPS][AHEAD][kDnSlot];
+  uint64_t landed[WARPS][AHEAD];
+  float scale[WARPS][AHEAD][20];  // of eight activation rows, two blocks; [16], [17]: weights
+  FewLists lists;
+  float rowscale[1];  // [P + T] alpha | s_shared, then ysum [split][P + T][kDnPitch]
 };
 
-__global__ void __launch_bounds__(kDnWarps * 32) f8_few_down_kernel(F8ExpertsArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  FewLists& L = *reinterpret_cast<FewLists*>(smem);
-  float* ysum = reinterpret_cast<float*>(smem + few_lists_bytes());  // [split][P + T][kDnPitch]
+template <int WARPS, int AHEAD>
+__global__ void __launch_bounds__(WARPS * 32, 8 / WARPS)
+    f8_few_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmSW,
+                       const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmSX,
+                       const F8ExpertsArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  DnShared<WARPS, AHEAD>& S = *reinterpret_cast<DnShared<WARPS, AHEAD>*>(align1024(smem_raw));
+  FewLists& L = S.lists;
+  float* rowscale = S.rowscale;
+  float* ysum = rowscale + a.T * a.k + a.T;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  if (tid == 0) {
+    for (int i = 0; i < WARPS * AHEAD; ++i) tc::mbar_init(&S.landed[0][0] + i, kDnArrivals);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   const int P = a.T * a.k, rows_all = P + (a.Is > 0 ? a.T : 0);
   const int col0 = blockIdx.x * kDnCols;
   const int KBr = f8_blocks(a.I), KBs = f8_blocks(a.Is), NB = f8_blocks(a.d);
+  const int PRr = (KBr + 1) / 2, PRs = (KBs + 1) / 2;  // pairs of blocks
   // The ids and the weights are older than the gate/up kernel, which has
   // itself waited for its predecessor before letting this one start.
-  build_lists(a, L);
+  build_lists<WARPS * 32>(a, L);
   int split = 1;
-  while (L.n_chunks * split < kDnWarps && split * 2 <= (KBr > KBs ? KBr : KBs)) split *= 2;
+  while (L.n_chunks * split < WARPS && split * 2 <= (PRr > PRs ? PRr : PRs)) split *= 2;
   const int walks = L.n_chunks * split;
-  auto blocks_of = [&](int idx) { return L.expert[idx / split] == a.E ? KBs : KBr; };
-  auto settle = [&](DnWalk& k) {  // to the next block that exists, if any
-    while (k.idx < walks && k.kb >= blocks_of(k.idx)) {
-      k.idx += kDnWarps;
-      k.kb = k.idx % split;
-    }
+  // A warp's walk over (chunk, k split) and the pairs of blocks of each.
+  struct Walk {
+    int idx, c, left, kb;  // chunk c, pairs of it left for this warp, the first block of the next
   };
-  auto load_w = [&](DnUnit& u, const DnWalk& k) {
-    u.w.lo[0] = u.w.lo[1] = u.w.hi[0] = u.w.hi[1] = zero4();
-    u.sw = 0.f;
-    if (k.idx >= walks) return;
-    const int e = L.expert[k.idx / split];
+  auto settle = [&](Walk& k) {  // to the next part that has a pair, if any
+    for (; k.idx < walks; k.idx += WARPS) {
+      k.c = k.idx / split;
+      const int n = k.c >= L.n_routed ? PRs : PRr, s = k.idx - k.c * split;
+      k.left = (n - s + split - 1) / split;
+      k.kb = 2 * s;
+      if (k.left > 0) return;
+    }
+    k.left = 0;
+  };
+  // where a walk's next weights and activations lie
+  const CUtensorMap *mw = &tmW, *mx = &tmX;
+  const float *psw = a.Sd, *psx = a.Hs;
+  int wrow = 0, wb = 0, xrow = 0, xb = 0, last_w = 0, last_x = 0;
+  auto open_w = [&](const Walk& k) {
+    if (!k.left) return;
+    const int e = L.expert[k.c], blocks = e == a.E ? KBs : KBr;
     const bool sh = e == a.E;
-    const int K = sh ? a.Is : a.I;
-    const int k0 = k.kb * kF8Block + 16 * t;
-    const uint8_t* p = (sh ? a.Wsd : a.Wd) + ((sh ? 0 : (size_t)e * a.d) + col0 + g) * K + k0;
-    const size_t eight = (size_t)8 * K;
-    if (k0 < K) {
-      u.w.lo[0] = ldg_stream(p);
-      u.w.hi[0] = ldg_stream(p + eight);
-    }
-    if (k0 + 64 < K) {
-      u.w.lo[1] = ldg_stream(p + 64);
-      u.w.hi[1] = ldg_stream(p + eight + 64);
-    }
-    u.sw = __ldg((sh ? a.Ssd : a.Sd) +
-                 ((sh ? 0 : (size_t)e * NB) + col0 / kF8Block) * (sh ? KBs : KBr) + k.kb);
+    mw = sh ? &tmSW : &tmW;
+    wrow = (sh ? 0 : e * a.d) + col0;
+    wb = 2 * (k.idx - k.c * split);
+    last_w = blocks - 1;
+    psw = (sh ? a.Ssd : a.Sd) + ((sh ? 0 : (size_t)e * NB) + col0 / kF8Block) * blocks;
   };
-  auto load_x = [&](DnUnit& u, const DnWalk& k) {
-    u.x.v[0] = u.x.v[1] = zero4();
-    u.s0 = u.s1 = 0.f;
-    if (k.idx >= walks) return;
-    const int c = k.idx / split;
-    const int row0 = (L.expert[c] == a.E ? P : 0) + L.start[c], last = L.count[c] - 1;
-    const uint8_t* p = a.Hq + (size_t)(row0 + min(g, last)) * a.ldh + k.kb * kF8Block + 16 * t;
-    u.x.v[0] = __ldcg(reinterpret_cast<const uint4*>(p));
-    u.x.v[1] = __ldcg(reinterpret_cast<const uint4*>(p + 64));
-    u.s0 = __ldcg(a.Hs + (size_t)(row0 + min(2 * t, last)) * a.hblocks + k.kb);
-    u.s1 = __ldcg(a.Hs + (size_t)(row0 + min(2 * t + 1, last)) * a.hblocks + k.kb);
+  auto open_x = [&](const Walk& k) {
+    if (!k.left) return;
+    const bool sh = k.c >= L.n_routed;
+    mx = sh ? &tmSX : &tmX;
+    xrow = (sh ? P : 0) + L.start[k.c];
+    xb = 2 * (k.idx - k.c * split);
+    last_x = (sh ? KBs : KBr) - 1;
+    psx = a.Hs + (size_t)(xrow + min(lane & 7, L.count[k.c] - 1)) * a.hblocks;
   };
-  DnUnit ring[kDnAhead];
-  DnWalk at[kDnAhead];  // the block that each ring entry holds
-  DnWalk next{warp, warp % split};
-  settle(next);
-#pragma unroll
-  for (int j = 0; j < kDnAhead; ++j) {
-    at[j] = next;
-    load_w(ring[j], next);
-    next.kb += split;
-    settle(next);
+  uint8_t* ring = S.ring[warp][0];
+  // (boxes past the last block come as zeros)
+  auto load_w = [&](int j) {
+    uint64_t* bar = &S.landed[warp][j];
+    if (lane == 0) {
+      uint8_t* dst = ring + j * kDnSlot;
+      tc::mbar_expect_tx(bar, 2 * kBox16);
+      tc::tma_load_2d(dst, mw, bar, wb * kF8Block, wrow);
+      tc::tma_load_2d(dst + kBox16, mw, bar, (wb + 1) * kF8Block, wrow);
+    }
+    if (lane >= 16 && lane < 18) copy4(&S.scale[warp][j][lane], psw + min(wb + (lane & 1), last_w), bar);
+    wb += 2 * split;
+  };
+  auto load_x = [&](int j) {
+    uint64_t* bar = &S.landed[warp][j];
+    if (lane == 0) {
+      uint8_t* dst = ring + j * kDnSlot + 2 * kBox16;
+      tc::mbar_expect_tx(bar, 2 * kBox8);
+      tc::tma_load_2d(dst, mx, bar, xb * kF8Block, xrow);
+      tc::tma_load_2d(dst + kBox8, mx, bar, (xb + 1) * kF8Block, xrow);
+    }
+    if (lane < 16) copy4(&S.scale[warp][j][lane], psx + min(xb + (lane >> 3), last_x), bar);
+    xb += 2 * split;
+  };
+  Walk now{warp, 0, 0, 0};
+  settle(now);
+  Walk ahead = now;
+  open_w(ahead);
+  for (int j = 0; j < AHEAD && ahead.left; ++j) {
+    load_w(j);
+    if (--ahead.left == 0) {
+      ahead.idx += WARPS;
+      settle(ahead);
+      open_w(ahead);
+    }
   }
   pdl_wait();
   pdl_trigger();
-#pragma unroll
-  for (int j = 0; j < kDnAhead; ++j) load_x(ring[j], at[j]);
-
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  bool more = at[0].idx < walks;
-  while (more) {
-#pragma unroll
-    for (int j = 0; j < kDnAhead; ++j) {
-      if (at[j].idx >= walks) {
-        more = false;
-        break;
-      }
-      float d[4];
-      block_mma(d, ring[j].w, ring[j].x.v[0], ring[j].x.v[1]);
-      acc[0] = fmaf(d[0], ring[j].sw * ring[j].s0, acc[0]);
-      acc[1] = fmaf(d[1], ring[j].sw * ring[j].s1, acc[1]);
-      acc[2] = fmaf(d[2], ring[j].sw * ring[j].s0, acc[2]);
-      acc[3] = fmaf(d[3], ring[j].sw * ring[j].s1, acc[3]);
-      const int idx = at[j].idx;
-      if (at[j].kb + split >= blocks_of(idx)) {  // the walk's sums, weighted
-        const int c = idx / split, s = idx - c * split;
-        const bool sh = L.expert[c] == a.E;
-        const int start = L.start[c], cnt = L.count[c];
-#pragma unroll
-        for (int j2 = 0; j2 < 2; ++j2) {
-          if (2 * t + j2 < cnt) {
-            const int p = start + 2 * t + j2;
-            const float al = sh ? a.s_shared[p] : a.alpha[L.sorted[p]];
-            float* y = ysum + ((size_t)s * rows_all + (sh ? P : 0) + p) * kDnPitch;
-            y[g] = al * acc[j2];
-            y[g + 8] = al * acc[2 + j2];
-          }
-        }
-        acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-      }
-      at[j] = next;
-      load_w(ring[j], next);
-      load_x(ring[j], next);
-      next.kb += split;
-      settle(next);
+  ahead = now;
+  open_x(ahead);
+  for (int j = 0; j < AHEAD && ahead.left; ++j) {
+    load_x(j);
+    if (--ahead.left == 0) {
+      ahead.idx += WARPS;
+      settle(ahead);
+      open_x(ahead);
     }
   }
+  for (int p = tid; p < rows_all; p += WARPS * 32)
+    rowscale[p] = p < P ? a.alpha[L.sorted[p]] : a.s_shared[p - P];
   __syncthreads();
-  for (int i = tid; i < a.T * kDnCols; i += kDnWarps * 32) {
+
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  const uint32_t get = get_at(g, t);
+  const uint32_t ring32 = tc::smem_u32(ring), sc32 = tc::smem_u32(S.scale[warp]);
+  uint32_t ph = 0;
+  int j = 0;
+  while (now.left) {
+    if (!f8_warp_wait(&S.landed[warp][j], ph, a.ctrl, kSiteFewFp8)) break;
+    const uint32_t slot = ring32 + j * kDnSlot, sc = sc32 + 80 * j;
+    const int blocks = now.c >= L.n_routed ? KBs : KBr;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // the last pair's second block may not exist; the activations' rows may
+      // be longer, and what lies there is nobody's
+      if (now.kb + h >= blocks) break;
+      const uint32_t w = slot + h * kBox16, x = slot + 2 * kBox16 + h * kBox8;
+      float d[4];
+      block_mma(d, weights_of(w, w + kBox8, get), lds16<0>(x + get), lds16<0>(x + (get ^ 64u)));
+      const float sw = lds4<64>(sc + 4 * h);
+      const float s0 = sw * lds4<0>(sc + 32 * h + 8 * t), s1 = sw * lds4<4>(sc + 32 * h + 8 * t);
+      acc[0] = fmaf(d[0], s0, acc[0]);
+      acc[1] = fmaf(d[1], s1, acc[1]);
+      acc[2] = fmaf(d[2], s0, acc[2]);
+      acc[3] = fmaf(d[3], s1, acc[3]);
+    }
+    reads_before_refill();
+    __syncwarp();
+    if (ahead.left) {
+      load_w(j);
+      load_x(j);
+      if (--ahead.left == 0) {
+        ahead.idx += WARPS;
+        settle(ahead);
+        open_w(ahead);
+        open_x(ahead);
+      }
+    }
+    if (++j == AHEAD) {
+      j = 0;
+      ph ^= 1u;
+    }
+    now.kb += 2 * split;
+    if (--now.left) continue;
+    // the walk's sums, weighted
+    const int cnt = L.count[now.c], s = now.idx - now.c * split;
+    const int row0 = (now.c >= L.n_routed ? P : 0) + L.start[now.c];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if (2 * t + q < cnt) {
+        const int row = row0 + 2 * t + q;
+        const float al = rowscale[row];
+        float* y = ysum + ((size_t)s * rows_all + row) * kDnPitch;
+        y[g] = al * acc[q];
+        y[g + 8] = al * acc[2 + q];
+      }
+    }
+    acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+    now.idx += WARPS;
+    settle(now);
+  }
+  __syncthreads();
+  for (int i = tid; i < a.T * kDnCols; i += WARPS * 32) {
     const int tok = i / kDnCols, c = i - tok * kDnCols;
     float y = 0.f;
     for (int sl = 0; sl < a.k; ++sl) {
       const int p = L.pos[tok * a.k + sl];
-      for (int s = 0; s < min(split, KBr); ++s) y += ysum[((size_t)s * rows_all + p) * kDnPitch + c];
+      for (int s = 0; s < min(split, PRr); ++s) y += ysum[((size_t)s * rows_all + p) * kDnPitch + c];
     }
-    for (int s = 0; s < min(split, KBs); ++s)
+    for (int s = 0; s < min(split, PRs); ++s)
       y += ysum[((size_t)s * rows_all + P + tok) * kDnPitch + c];
     const size_t o = (size_t)tok * a.d + col0 + c;
     if (a.r_attn) y += a.r_attn[o];
@@ -470,162 +720,204 @@ __global__ void __launch_bounds__(kDnWarps * 32) f8_few_down_kernel(F8ExpertsArg
 // ---------------------------------------------------------------------------
 // product for a few rows
 // ---------------------------------------------------------------------------
-constexpr int kMmWarps = 16;
-constexpr int kMmAhead = 3;
-
-template <int NT>
-struct MmUnit {
-  WeightBlock w;
-  float sw;
-  ActBlock x[NT];
-  float s0[NT], s1[NT];
-};
+constexpr int kMmWarps = 8;
 
 // out[m][n] for M <= 8 NT rows: items of 16 output columns, k split over the
-// warps of an item.
+// `wpi` warps of an item, two blocks each, whose sums are added in warp order.
 template <int NT>
-__global__ void __launch_bounds__(kMmWarps * 32, 1) f8_few_matmul_kernel(F8MatmulArgs a) {
-  __shared__ float4 part[2][NT][kMmWarps][32];
+constexpr int mm_slot() { return 2 * (kBox16 + NT * kBox8); }
+template <int NT, int AHEAD>
+struct MmShared {
+  uint8_t ring[kMmWarps][AHEAD][mm_slot<NT>()];
+  float4 part[2][NT][kMmWarps][32];
+  uint64_t landed[kMmWarps][AHEAD];
+  float scale[kMmWarps][AHEAD][36];  // of the activation rows, two blocks; [32], [33]: weights
+};
+template <int NT, int AHEAD>
+__global__ void __launch_bounds__(kMmWarps * 32, 1)
+    f8_few_matmul_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                         const F8MatmulArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  MmShared<NT, AHEAD>& S = *reinterpret_cast<MmShared<NT, AHEAD>*>(align1024(smem_raw));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int KB = f8_blocks(a.K);
+  // arrivals: the boxes' bytes, each lane's scale (or two), two of the weights
+  if (tid == 0) {
+    for (int i = 0; i < kMmWarps * AHEAD; ++i) tc::mbar_init(&S.landed[0][0] + i, 3 + 16 * NT);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  const int KB = f8_blocks(a.K), pairs = (KB + 1) / 2;
   pdl_wait();
   pdl_trigger();
   int wpi = 1;
-  while (wpi * 2 <= KB && wpi < kMmWarps) wpi *= 2;
-  const int slots = kMmWarps / wpi, slot = warp / wpi, w = warp % wpi;
+  while (wpi * 2 <= pairs && wpi < kMmWarps) wpi *= 2;
+  const int teams = kMmWarps / wpi, team = warp / wpi, w = warp % wpi;
   const int items = (a.N + 15) / 16;
-  const int stride = (int)gridDim.x * slots, rounds = (items + stride - 1) / stride;
-  const int steps = (KB + wpi - 1) / wpi, units = rounds * steps;
-  const int first = slot * (int)gridDim.x + (int)blockIdx.x;
-  auto load = [&](MmUnit<NT>& u, int n) {
-    const int r = n / steps, kb = (n - r * steps) * wpi + w;
-    const int i = first + r * stride;
-    u.w.lo[0] = u.w.lo[1] = u.w.hi[0] = u.w.hi[1] = zero4();
-    u.sw = 0.f;
-#pragma unroll
-    for (int q = 0; q < NT; ++q) {
-      u.x[q].v[0] = u.x[q].v[1] = zero4();
-      u.s0[q] = u.s1[q] = 0.f;
+  const int stride = (int)gridDim.x * teams, rounds = (items + stride - 1) / stride;
+  const int first = team * (int)gridDim.x + (int)blockIdx.x;
+  const uint32_t get = get_at(g, t);
+  // lane's scales: row lane % 8 NT, blocks lane / 8 NT (and, for two tiles, + 2)
+  const float* xsc = a.a_scale + (size_t)min(lane & (8 * NT - 1), a.M - 1) * KB;
+  uint8_t* ring = S.ring[warp][0];
+  int li = first, lp = w;  // the loads' item and pair of blocks
+  auto load = [&](int j) {
+    if (li >= items) return;
+    uint64_t* bar = &S.landed[warp][j];
+    uint8_t* dst = ring + j * mm_slot<NT>();
+    const int kb = 2 * lp;
+    if (lane == 0) {
+      // rows and columns past the ends, a second block among them, come as zeros
+      tc::mbar_expect_tx(bar, mm_slot<NT>());
+      tc::tma_load_2d(dst, &tmB, bar, kb * kF8Block, li * 16);
+      tc::tma_load_2d(dst + kBox16, &tmB, bar, (kb + 1) * kF8Block, li * 16);
+      tc::tma_load_2d(dst + 2 * kBox16, &tmA, bar, kb * kF8Block, 0);
+      tc::tma_load_2d(dst + 2 * kBox16 + NT * kBox8, &tmA, bar, (kb + 1) * kF8Block, 0);
     }
-    if (n >= units || i >= items || kb >= KB) return;
-    const int k0 = kb * kF8Block + 16 * t;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = k0 + 64 * h, left = a.K - k;
-      if (left <= 0) continue;
-      const int lo = i * 16 + g, hi = lo + 8;
-      if (lo < a.N) u.w.lo[h] = keep_bytes(ldg_stream(a.b + (size_t)lo * a.ldb + k), left);
-      if (hi < a.N) u.w.hi[h] = keep_bytes(ldg_stream(a.b + (size_t)hi * a.ldb + k), left);
-#pragma unroll
-      for (int q = 0; q < NT; ++q)
-        u.x[q].v[h] = keep_bytes(
-            *reinterpret_cast<const uint4*>(a.a + (size_t)min(8 * q + g, a.M - 1) * a.lda + k),
-            left);
-    }
-    u.sw = __ldg(a.b_scale + (size_t)(i * 16 / kF8Block) * KB + kb);
-#pragma unroll
-    for (int q = 0; q < NT; ++q) {
-      u.s0[q] = a.a_scale[(size_t)min(8 * q + 2 * t, a.M - 1) * KB + kb];
-      u.s1[q] = a.a_scale[(size_t)min(8 * q + 2 * t + 1, a.M - 1) * KB + kb];
+    if (lane < 16 * NT) copy4(&S.scale[warp][j][lane], xsc + min(kb + lane / (8 * NT), KB - 1), bar);
+    if (lane < 2)
+      copy4(&S.scale[warp][j][32 + lane],
+            a.b_scale + (size_t)(li * 16 / kF8Block) * KB + min(kb + lane, KB - 1), bar);
+    lp += wpi;
+    if (lp >= pairs) {
+      lp = w;
+      li += stride;
     }
   };
-  MmUnit<NT> ring[kMmAhead];
-#pragma unroll
-  for (int j = 0; j < kMmAhead; ++j) load(ring[j], j);
+  for (int j = 0; j < AHEAD; ++j) load(j);
   float acc[NT][4] = {};
-  for (int n0 = 0; n0 < units; n0 += kMmAhead) {
+  const uint32_t ring32 = tc::smem_u32(ring), sc32 = tc::smem_u32(S.scale[warp]);
+  uint32_t ph = 0;
+  int r = 0, pr = w, j = 0;
+  bool alive = true;
+  while (r < rounds) {
+    const int i = first + r * stride;
+    if (alive && i < items && pr < pairs) {
+      alive = f8_warp_wait(&S.landed[warp][j], ph, a.ctrl, kSiteFewFp8);
+      const uint32_t slot = ring32 + j * mm_slot<NT>(), sc = sc32 + 144 * j;
 #pragma unroll
-    for (int j = 0; j < kMmAhead; ++j) {
-      const int n = n0 + j;
-      if (n >= units) break;
-      const int r = n / steps, st = n - r * steps;
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t wb = slot + h * kBox16;
+        const WeightBlock wgt = weights_of(wb, wb + kBox8, get);
+        const float sw = lds4<128>(sc + 4 * h);
 #pragma unroll
-      for (int q = 0; q < NT; ++q) {
-        float d[4];
-        block_mma(d, ring[j].w, ring[j].x[q].v[0], ring[j].x[q].v[1]);
-        const float c0 = ring[j].sw * ring[j].s0[q], c1 = ring[j].sw * ring[j].s1[q];
-        acc[q][0] = fmaf(d[0], c0, acc[q][0]);
-        acc[q][1] = fmaf(d[1], c1, acc[q][1]);
-        acc[q][2] = fmaf(d[2], c0, acc[q][2]);
-        acc[q][3] = fmaf(d[3], c1, acc[q][3]);
-      }
-      load(ring[j], n + kMmAhead);
-      if (st != steps - 1) continue;
-#pragma unroll
-      for (int q = 0; q < NT; ++q) {
-        part[r & 1][q][warp][lane] = make_float4(acc[q][0], acc[q][1], acc[q][2], acc[q][3]);
-        acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.f;
-      }
-      __syncthreads();
-      const int i = first + r * stride;
-      if (i >= items || w != r % wpi) continue;
-#pragma unroll
-      for (int q = 0; q < NT; ++q) {
-        float4 v = part[r & 1][q][slot * wpi][lane];
-        for (int p = 1; p < wpi; ++p) {
-          const float4 o = part[r & 1][q][slot * wpi + p][lane];
-          v.x += o.x;
-          v.y += o.y;
-          v.z += o.z;
-          v.w += o.w;
+        for (int q = 0; q < NT; ++q) {
+          const uint32_t x = slot + 2 * kBox16 + (h * NT + q) * kBox8;
+          const uint32_t sx = sc + 4 * (8 * NT * h + 8 * q + 2 * t);
+          float d[4];
+          block_mma(d, wgt, lds16<0>(x + get), lds16<0>(x + (get ^ 64u)));
+          const float c0 = sw * lds4<0>(sx), c1 = sw * lds4<4>(sx);
+          acc[q][0] = fmaf(d[0], c0, acc[q][0]);
+          acc[q][1] = fmaf(d[1], c1, acc[q][1]);
+          acc[q][2] = fmaf(d[2], c0, acc[q][2]);
+          acc[q][3] = fmaf(d[3], c1, acc[q][3]);
         }
-        const float y[4] = {v.x, v.y, v.z, v.w};
+      }
+      reads_before_refill();
+      __syncwarp();
+      load(j);
+      if (++j == AHEAD) {
+        j = 0;
+        ph ^= 1u;
+      }
+    }
+    pr += wpi;
+    if (pr - w < pairs) continue;
+    pr = w;
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          const int m = 8 * q + 2 * t + (z & 1), col = i * 16 + g + 8 * (z >> 1);
-          if (m < a.M && col < a.N) {
-            if (a.out_bf16)
-              static_cast<__nv_bfloat16*>(a.out)[(size_t)m * a.ldo + col] = __float2bfloat16_rn(y[z]);
-            else
-              static_cast<float*>(a.out)[(size_t)m * a.ldo + col] = y[z];
-          }
+    for (int q = 0; q < NT; ++q) {
+      S.part[r & 1][q][warp][lane] = make_float4(acc[q][0], acc[q][1], acc[q][2], acc[q][3]);
+      acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.f;
+    }
+    __syncthreads();
+    const int round = r++;
+    if (i >= items || w != round % wpi) continue;
+#pragma unroll
+    for (int q = 0; q < NT; ++q) {
+      float4 v = S.part[round & 1][q][team * wpi][lane];
+      for (int p = 1; p < wpi; ++p) {
+        const float4 o = S.part[round & 1][q][team * wpi + p][lane];
+        v.x += o.x;
+        v.y += o.y;
+        v.z += o.z;
+        v.w += o.w;
+      }
+      const float y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        const int m = 8 * q + 2 * t + (z & 1), col = i * 16 + g + 8 * (z >> 1);
+        if (m < a.M && col < a.N) {
+          if (a.out_bf16)
+            static_cast<__nv_bfloat16*>(a.out)[(size_t)m * a.ldo + col] = __float2bfloat16_rn(y[z]);
+          else
+            static_cast<float*>(a.out)[(size_t)m * a.ldo + col] = y[z];
         }
       }
     }
   }
 }
 
+template <int SLOTS>
 size_t gateup_smem(int T, int d) {
   const int KB = f8_blocks(d);
-  return few_lists_bytes() + 2 * kGuWarps * 32 * sizeof(float4) + (((size_t)T * KB * 4 + 15) & ~15) +
+  return 1024 + sizeof(GuShared<SLOTS>) + (((size_t)T * KB * 4 + 15) & ~15) +
          (size_t)T * (KB * kF8Block + 64);
 }
+constexpr size_t kSmemLimit = 227 * 1024;
+
+template <int SLOTS>
+cudaError_t launch_gateup(const F8FewMaps& m, const F8ExpertsArgs& a, cudaStream_t st) {
+  static int attr[64] = {};
+  const size_t smem = gateup_smem<SLOTS>(a.T, a.d);
+  cudaError_t e = ensure_smem_limit(f8_few_gateup_kernel<SLOTS>, (int)smem, attr);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(f8_few_gateup_kernel<SLOTS>, dim3(tc_sm_count()), kGuThreads, smem, st, m.g, m.u, m.sg,
+                    m.su, a);
+}
+
 // Rows of partial sums: all pairs and shared tokens once, or fewer of them
-// split up to kDnWarps ways (split x chunks stays below 2 kDnWarps, of 8 rows).
-size_t down_smem(int T, int k) {
-  const int rows = T * k + T;
-  return few_lists_bytes() + (size_t)(rows > 16 * kDnWarps ? rows : 16 * kDnWarps) * kDnPitch * 4;
+// split up to WARPS ways (split x chunks stays below 2 WARPS, of 8 rows).
+template <int WARPS, int AHEAD>
+cudaError_t launch_down(const F8FewMaps& m, const F8ExpertsArgs& a, cudaStream_t st) {
+  static int attr[64] = {};
+  const int rows = a.T * a.k + a.T;
+  const size_t smem = 1024 + sizeof(DnShared<WARPS, AHEAD>) + (size_t)rows * 4 +
+                      (size_t)(rows > 16 * WARPS ? rows : 16 * WARPS) * kDnPitch * 4;
+  cudaError_t e = ensure_smem_limit(f8_few_down_kernel<WARPS, AHEAD>, (int)smem, attr);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(f8_few_down_kernel<WARPS, AHEAD>, dim3(a.d / kDnCols), WARPS * 32, smem, st, m.w, m.sw,
+                    m.x, m.sx, a);
+}
+
+template <int NT, int AHEAD>
+cudaError_t launch_matmul(const F8MatmulArgs& a, cudaStream_t st) {
+  static int attr[64] = {};
+  const size_t smem = 1024 + sizeof(MmShared<NT, AHEAD>);
+  cudaError_t e = ensure_smem_limit(f8_few_matmul_kernel<NT, AHEAD>, (int)smem, attr);
+  if (e != cudaSuccess) return e;
+  CUtensorMap A, B;
+  if (!f8_make_map(&A, a.a, a.M, a.K, a.lda, 8 * NT) || !f8_make_map(&B, a.b, a.N, a.K, a.ldb, 16))
+    return cudaErrorInvalidValue;
+  const int items = (a.N + 15) / 16;
+  const int grid = items < tc_sm_count() ? items : tc_sm_count();
+  return launch_pdl(f8_few_matmul_kernel<NT, AHEAD>, dim3(grid), kMmWarps * 32, smem, st, A, B, a);
 }
 
 }  // namespace
 
-static_assert(sizeof(FewLists) <= few_lists_bytes(), "few_lists_bytes covers the lists");
-
 bool f8_few_ok(int T, int d, int k) {
-  return T <= kF8FewTokens && T * k <= kFewMaxPairs && gateup_smem(T, d) <= 220 * 1024;
+  return T <= kF8FewTokens && T * k <= kFewMaxPairs && gateup_smem<2>(T, d) <= kSmemLimit;
 }
 
-cudaError_t launch_f8_few_gateup(const F8ExpertsArgs& a, cudaStream_t st) {
-  static int attr[64] = {};
-  const size_t smem = gateup_smem(a.T, a.d);
-  cudaError_t e = ensure_smem_limit(f8_few_gateup_kernel, (int)smem, attr);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(f8_few_gateup_kernel, dim3(tc_sm_count()), kGuWarps * 32, smem, st, a);
+cudaError_t launch_f8_few_gateup(const F8FewMaps& m, const F8ExpertsArgs& a, cudaStream_t st) {
+  return gateup_smem<4>(a.T, a.d) <= kSmemLimit ? launch_gateup<4>(m, a, st) : launch_gateup<2>(m, a, st);
 }
 
-cudaError_t launch_f8_few_down(const F8ExpertsArgs& a, cudaStream_t st) {
-  static int attr[64] = {};
-  const size_t smem = down_smem(a.T, a.k);
-  cudaError_t e = ensure_smem_limit(f8_few_down_kernel, (int)smem, attr);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(f8_few_down_kernel, dim3(a.d / kDnCols), kDnWarps * 32, smem, st, a);
+cudaError_t launch_f8_few_down(const F8FewMaps& m, const F8ExpertsArgs& a, cudaStream_t st) {
+  return a.d / kDnCols <= tc_sm_count() ? launch_down<8, 3>(m, a, st) : launch_down<4, 3>(m, a, st);
 }
 
 cudaError_t launch_f8_few_matmul(const F8MatmulArgs& a, cudaStream_t st) {
-  const int items = (a.N + 15) / 16;
-  const int grid = items < tc_sm_count() ? items : tc_sm_count();
-  return a.M <= 8 ? launch_pdl(f8_few_matmul_kernel<1>, dim3(grid), kMmWarps * 32, 0, st, a)
-                  : launch_pdl(f8_few_matmul_kernel<2>, dim3(grid), kMmWarps * 32, 0, st, a);
+  return a.M <= 8 ? launch_matmul<1, 3>(a, st) : launch_matmul<2, 2>(a, st);
 }
 
 }  // namespace moe

@@ -142,25 +142,11 @@ __device__ __forceinline__ void give_up(const F8TcArgs& a, volatile int* abort_f
   report(a.ctrl, kDevTimeout, kSiteTcFp8);
 }
 
-// One thread waits for a phase of `bar`; false when the wait ran out of its
-// limit or another warp gave up.
+// Waits of one thread and of a whole warp; a warp that gives up raises the flag.
 __device__ __forceinline__ bool lane_wait(uint64_t* bar, uint32_t parity, const F8TcArgs& a,
                                           volatile int* abort_flag) {
-  if (mbar_try_wait(bar, parity)) return true;
-  uint64_t t0 = 0;
-  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
-    if ((n & 63u) == 0) {
-      if (*abort_flag) return false;
-      if (t0 == 0) t0 = globaltimer();
-      if (globaltimer() - t0 > a.wait_ns) return false;
-    }
-  }
-  return true;
+  return f8_lane_wait(bar, parity, a.wait_ns, abort_flag);
 }
-// The whole warp waits. Every lane polls: one lane's poll with its outcome
-// shuffled to the others took 1390 cycles for a round trip between one warp
-// and sixteen, this 260 (measured alone), and there are two such round trips a
-// step.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const F8TcArgs& a,
                                           volatile int* abort_flag) {
   const bool ok = __all_sync(0xffffffffu, lane_wait(bar, parity, a, abort_flag));

@@ -245,10 +245,13 @@ struct F8ExpertsArgs {
   int T, d, E, k, I, Is, ldh, hblocks, out_bf16;
 };
 constexpr int kF8FewTokens = 16;
-constexpr size_t few_lists_bytes() { return 13056; }
 bool f8_few_ok(int T, int d, int k);
-cudaError_t launch_f8_few_gateup(const F8ExpertsArgs& a, cudaStream_t st);
-cudaError_t launch_f8_few_down(const F8ExpertsArgs& a, cudaStream_t st);
+// Maps of the banks (routed and shared) in boxes of 16 rows; h codes in boxes of 8.
+struct F8FewMaps {
+  CUtensorMap g, u, sg, su, w, sw, x, sx;
+};
+cudaError_t launch_f8_few_gateup(const F8FewMaps& m, const F8ExpertsArgs& a, cudaStream_t st);
+cudaError_t launch_f8_few_down(const F8FewMaps& m, const F8ExpertsArgs& a, cudaStream_t st);
 
 // out = A B^T for at most kF8FewTokens rows (fp8_few.cu).
 struct F8MatmulArgs {
@@ -257,6 +260,7 @@ struct F8MatmulArgs {
   const uint8_t* b;       // [N][ldb]
   const float* b_scale;   // [N blocks][K blocks]
   void* out;              // [M][ldo]
+  Ctrl* ctrl;
   int M, N, K, out_bf16;
   long long lda, ldb, ldo;
 };

@@ -240,6 +240,7 @@ def test_linear_quantises_and_multiplies():
 SHAPES = {
     "tiny": (256, 16, 4, 64, 64), "ragged": (272, 5, 2, 144, 80), "one": (128, 1, 1, 128, 0),
     "wide": (512, 8, 2, 896, 0), "apart": (384, 12, 4, 128, 512), "many": (256, 300, 8, 128, 128),
+    "deep": (4096, 4, 2, 144, 400),
 }
 
 
@@ -283,7 +284,7 @@ CASES = [("tiny", 1), ("tiny", 2), ("tiny", 8), ("tiny", 9), ("tiny", 16), ("tin
          ("tiny", 700), ("ragged", 1), ("ragged", 5), ("ragged", 16), ("ragged", 40), ("ragged", 300),
          ("one", 1), ("one", 16), ("one", 129), ("wide", 1), ("wide", 3), ("wide", 64), ("wide", 257),
          ("apart", 1), ("apart", 10), ("apart", 33), ("apart", 260), ("many", 1), ("many", 16),
-         ("many", 64), ("many", 600)]
+         ("many", 64), ("many", 600), ("deep", 1), ("deep", 8), ("deep", 16), ("deep", 20)]
 
 
 @pytest.mark.parametrize("shape,T", CASES, ids=["%s-%d" % c for c in CASES])

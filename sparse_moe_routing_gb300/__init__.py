@@ -181,10 +181,27 @@ def _bank(b):
     return _Bank(_ptr(b), None, None)
 
 
+_raw_stream = None
+
+
 def _stream(stream):
-    import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    """The stream's handle; None: the current stream of the current device."""
+    global _raw_stream
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    if _raw_stream is None:
+        import torch
+        # the handle alone, where this torch gives it: making a Stream object of
+        # it costs 3 us, a call of the smallest kernels 3 us in all
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream
+        else:
+            device = torch._C._cuda_getDevice if torch.cuda.is_initialized() else None
+            if device is None:
+                return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+            _raw_stream = lambda: raw(device())
+    return ctypes.c_void_p(_raw_stream())
 
 
 def _check(status: int, where: str):
@@ -353,42 +370,48 @@ def _dtypes():
 
 
 def _dtype_of(t):
-    d = _dtypes().get(t.dtype)
+    d = (_dt or _dtypes()).get(t.dtype)
     if d is None:
         raise ValueError("expected a float32 or bfloat16 tensor, got %s" % t.dtype)
     return d
 
 
-def _rows_ptr(t, name):
-    """Pointer of a matrix (or a stack of them) with unit column stride."""
+def _ld(t, shape, name):
+    """Values between the rows of a matrix (or of a stack of them) on a CUDA
+    device with unit column stride; the row length where there is one row."""
     if not t.is_cuda:
         raise ValueError("%s must be on a CUDA device" % name)
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    stride = t.stride()
+    if stride[-1] != 1 and shape[-1] > 1:
         raise ValueError("%s must have contiguous rows" % name)
-    return t.data_ptr()
-
-
-def _ld(t):
-    """Values between rows; the row length where there is at most one row."""
-    return t.stride(-2) if t.shape[-2] > 1 else max(t.stride(-2), t.shape[-1])
+    return stride[-2] if shape[-2] > 1 else max(stride[-2], shape[-1])
 
 
 def _codes_dtype(t, name):
-    import torch
-    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+    if t.dtype not in (_codes_types or _code_types()):
         raise ValueError("%s must be float8_e4m3fn (or its bytes as uint8)" % name)
 
 
+_codes_types = None
+
+
+def _code_types():
+    global _codes_types
+    import torch
+    _codes_types = (torch.float8_e4m3fn, torch.uint8)
+    return _codes_types
+
+
 def _shape_is(t, shape, name):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
 
 
 def _scales_ok(t, shape, name):
-    import torch
-    if t.dtype != torch.float32:
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if (_dt or _dtypes()).get(t.dtype) != F32:
         raise ValueError("%s must be float32" % name)
-    _shape_is(t, shape, name)
 
 
 def fp8_empty(rows, cols, block_rows=1, count=None, device=None):
@@ -406,19 +429,24 @@ def fp8_empty(rows, cols, block_rows=1, count=None, device=None):
 def fp8_quantize(x, codes, scales, block_rows=1, stream=None):
     """moe_fp8_quantize: x [rows, cols] or [count, rows, cols] (float32 or
     bfloat16) into codes (float8_e4m3fn, same shape) and scales."""
-    if x.dim() not in (2, 3):
+    shape = x.shape
+    n = len(shape)
+    if n not in (2, 3):
         raise ValueError("x must have two or three dimensions")
     _codes_dtype(codes, "codes")
-    _shape_is(codes, x.shape, "codes")
-    rows, cols = x.shape[-2:]
-    count = x.shape[0] if x.dim() == 3 else 1
-    ldx, ldq = _ld(x), _ld(codes)
-    if x.dim() == 3 and count > 1 and (x.stride(0) != rows * ldx or codes.stride(0) != rows * ldq):
-        raise ValueError("stacked matrices must follow one another at rows * row stride")
-    _scales_ok(scales, x.shape[:-2] + (-(-rows // block_rows) if block_rows > 0 else 0, -(-cols // 128)),
-               "scales")
-    _check(lib().moe_fp8_quantize(_rows_ptr(x, "x"), _dtype_of(x), ldx, count, rows, cols, block_rows,
-                                  _rows_ptr(codes, "codes"), ldq, _ptr(scales), _stream(stream)),
+    _shape_is(codes, shape, "codes")
+    rows, cols = shape[-2], shape[-1]
+    nb = (-(-rows // block_rows) if block_rows > 0 else 0, -(-cols // 128))
+    _scales_ok(scales, nb if n == 2 else (shape[0],) + nb, "scales")
+    dtype = _dtype_of(x)
+    ldx, ldq = _ld(x, shape, "x"), _ld(codes, shape, "codes")
+    count = 1
+    if n == 3:
+        count = shape[0]
+        if count > 1 and (x.stride(0) != rows * ldx or codes.stride(0) != rows * ldq):
+            raise ValueError("stacked matrices must follow one another at rows * row stride")
+    _check(lib().moe_fp8_quantize(x.data_ptr(), dtype, ldx, count, rows, cols, block_rows,
+                                  codes.data_ptr(), ldq, _ptr(scales), _stream(stream)),
            "moe_fp8_quantize")
 
 
@@ -447,8 +475,7 @@ def fp8_matmul_workspace(M, N, K, device=None, stream=None):
 def fp8_matmul(a, a_scale, b, b_scale, out, workspace, stream=None):
     """moe_fp8_matmul: out [M, N] = a [M, K] b [N, K]^T, codes with scales per
     1 x 128 (a) and 128 x 128 (b); out float32 or bfloat16."""
-    M, K = a.shape
-    N = b.shape[0]
+    (M, K), N = a.shape, b.shape[0]
     _codes_dtype(a, "a")
     _codes_dtype(b, "b")
     _shape_is(b, (N, K), "b")
@@ -456,10 +483,11 @@ def fp8_matmul(a, a_scale, b, b_scale, out, workspace, stream=None):
     kb = -(-K // 128)
     _scales_ok(a_scale, (M, kb), "a_scale")
     _scales_ok(b_scale, (-(-N // 128), kb), "b_scale")
-    m = _matmul_args(M, N, K, _dtype_of(out), _ld(a), _ld(b), _ld(out), workspace)
-    _check(lib().moe_fp8_matmul(_rows_ptr(a, "a"), _ptr(a_scale), _rows_ptr(b, "b"), _ptr(b_scale),
-                                ctypes.byref(m), _rows_ptr(out, "out"), _stream(stream)),
-           "moe_fp8_matmul")
+    m = _Fp8Matmul(M, N, K, _dtype_of(out), _ld(a, (M, K), "a"), _ld(b, (N, K), "b"),
+                   _ld(out, (M, N), "out"), workspace.data_ptr(),
+                   workspace.numel() * workspace.element_size())
+    _check(lib().moe_fp8_matmul(a.data_ptr(), _ptr(a_scale), b.data_ptr(), _ptr(b_scale),
+                                ctypes.byref(m), out.data_ptr(), _stream(stream)), "moe_fp8_matmul")
 
 
 class Fp8Linear:
@@ -563,6 +591,7 @@ class Fp8Experts:
         self._c = cfg._c(self.ws)
         self._cp = ctypes.byref(self._c)
         self._x_shape = (cfg.T, cfg.d_model)
+        self._w_shared = _ptr(weights.get("w_shared"))
 
     @staticmethod
     def from_bf16(cfg: MoEConfig, weights: dict, device=None):
@@ -590,7 +619,7 @@ class Fp8Experts:
         self._rows(x, out, r_attn)
         _check(lib().moe_fp8_experts_forward(
             _ptr(x), _ptr(r_attn), _ptr(topk_ids), _ptr(weights), _ptr(s_shared), *self._banks,
-            _ptr(self.w.get("w_shared")), self._cp, _ptr(out), _dtype_of(out), _stream(stream)),
+            self._w_shared, self._cp, _ptr(out), _dtype_of(out), _stream(stream)),
             "moe_fp8_experts_forward")
         return out
 
@@ -601,7 +630,7 @@ class Fp8Experts:
         self._rows(x, out, r_attn)
         _check(lib().moe_fp8_layer_forward(
             _ptr(x), _ptr(r_attn), _ptr(self.w["W_router"]), _ptr(self.w.get("expert_bias")),
-            *self._banks, _ptr(self.w.get("w_shared")), self._cp, _ptr(out), _dtype_of(out),
+            *self._banks, self._w_shared, self._cp, _ptr(out), _dtype_of(out),
             _ptr(topk_ids), _ptr(weights), _stream(stream)), "moe_fp8_layer_forward")
         return out
 

@@ -39,15 +39,6 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ void mma_e4m3_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                               uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
@@ -59,13 +50,18 @@ struct WeightBlock {
   uint4 lo[2], hi[2];
 };
 
-__device__ __forceinline__ void block_mma(float (&d)[4], const WeightBlock& w, const uint4& b0,
-                                          const uint4& b1) {
-  mma_e4m3_first(d, w.lo[0].x, w.hi[0].x, w.lo[0].y, w.hi[0].y, b0.x, b0.y);
-  mma_e4m3(d, w.lo[0].z, w.hi[0].z, w.lo[0].w, w.hi[0].w, b0.z, b0.w);
-  mma_e4m3(d, w.lo[1].x, w.hi[1].x, w.lo[1].y, w.hi[1].y, b1.x, b1.y);
-  mma_e4m3(d, w.lo[1].z, w.hi[1].z, w.lo[1].w, w.hi[1].w, b1.z, b1.w);
-}
+// The four steps of 32 k, from zero each and added afterwards: a chain through
+// the accumulator waits 73 cycles a step, independent ones follow every 14.
+struct BlockSum {
+  float d[4][4];
+  __device__ __forceinline__ void mma(const WeightBlock& w, const uint4& b0, const uint4& b1) {
+    mma_e4m3(d[0], w.lo[0].x, w.hi[0].x, w.lo[0].y, w.hi[0].y, b0.x, b0.y);
+    mma_e4m3(d[1], w.lo[0].z, w.hi[0].z, w.lo[0].w, w.hi[0].w, b0.z, b0.w);
+    mma_e4m3(d[2], w.lo[1].x, w.hi[1].x, w.lo[1].y, w.hi[1].y, b1.x, b1.y);
+    mma_e4m3(d[3], w.lo[1].z, w.hi[1].z, w.lo[1].w, w.hi[1].w, b1.z, b1.w);
+  }
+  __device__ __forceinline__ float of(int i) const { return (d[0][i] + d[1][i]) + (d[2][i] + d[3][i]); }
+};
 
 __device__ __forceinline__ uint4 zero4() { return make_uint4(0u, 0u, 0u, 0u); }
 
@@ -364,15 +360,18 @@ __global__ void __launch_bounds__(kGuThreads, 1)
           const float sg = lds4<0>(sc32 + 16 * j + 4 * h), su = lds4<8>(sc32 + 16 * j + 4 * h);
           const float s0 = lds4<0>(x0 + 4 * h), s1 = lds4<0>(x1 + 4 * h);
           const float c0 = sg * s0, c1 = sg * s1, c2 = su * s0, c3 = su * s1;
+          BlockSum d[2];
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             const uint32_t box = slot + 2 * h * kBox16 + m * kBox8;
-            float d[4];
-            block_mma(d, weights_of(box, box + kBox16, get), b0, b1);
-            acc[m][0] = fmaf(d[0], c0, acc[m][0]);
-            acc[m][1] = fmaf(d[1], c1, acc[m][1]);
-            acc[m][2] = fmaf(d[2], c2, acc[m][2]);
-            acc[m][3] = fmaf(d[3], c3, acc[m][3]);
+            d[m].mma(weights_of(box, box + kBox16, get), b0, b1);
+          }
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            acc[m][0] = fmaf(d[m].of(0), c0, acc[m][0]);
+            acc[m][1] = fmaf(d[m].of(1), c1, acc[m][1]);
+            acc[m][2] = fmaf(d[m].of(2), c2, acc[m][2]);
+            acc[m][3] = fmaf(d[m].of(3), c3, acc[m][3]);
           }
         }
         xr += 2 * nsplit * kF8Block;
@@ -647,21 +646,26 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS)
   while (now.left) {
     if (!f8_warp_wait(&S.landed[warp][j], ph, a.ctrl, kSiteFewFp8)) break;
     const uint32_t slot = ring32 + j * kDnSlot, sc = sc32 + 80 * j;
-    const int blocks = now.c >= L.n_routed ? KBs : KBr;
+    // the last pair's second block may not exist; the activations' rows may be
+    // longer, and what lies there is nobody's
+    const bool second = now.kb + 1 < (now.c >= L.n_routed ? KBs : KBr);
+    BlockSum d[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      // the last pair's second block may not exist; the activations' rows may
-      // be longer, and what lies there is nobody's
-      if (now.kb + h >= blocks) break;
       const uint32_t w = slot + h * kBox16, x = slot + 2 * kBox16 + h * kBox8;
-      float d[4];
-      block_mma(d, weights_of(w, w + kBox8, get), lds16<0>(x + get), lds16<0>(x + (get ^ 64u)));
-      const float sw = lds4<64>(sc + 4 * h);
-      const float s0 = sw * lds4<0>(sc + 32 * h + 8 * t), s1 = sw * lds4<4>(sc + 32 * h + 8 * t);
-      acc[0] = fmaf(d[0], s0, acc[0]);
-      acc[1] = fmaf(d[1], s1, acc[1]);
-      acc[2] = fmaf(d[2], s0, acc[2]);
-      acc[3] = fmaf(d[3], s1, acc[3]);
+      if (h == 0 || second)
+        d[h].mma(weights_of(w, w + kBox8, get), lds16<0>(x + get), lds16<0>(x + (get ^ 64u)));
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (h == 0 || second) {
+        const float sw = lds4<64>(sc + 4 * h);
+        const float s0 = sw * lds4<0>(sc + 32 * h + 8 * t), s1 = sw * lds4<4>(sc + 32 * h + 8 * t);
+        acc[0] = fmaf(d[h].of(0), s0, acc[0]);
+        acc[1] = fmaf(d[h].of(1), s1, acc[1]);
+        acc[2] = fmaf(d[h].of(2), s0, acc[2]);
+        acc[3] = fmaf(d[h].of(3), s1, acc[3]);
+      }
     }
     reads_before_refill();
     __syncwarp();
@@ -803,13 +807,13 @@ __global__ void __launch_bounds__(kMmWarps * 32, 1)
         for (int q = 0; q < NT; ++q) {
           const uint32_t x = slot + 2 * kBox16 + (h * NT + q) * kBox8;
           const uint32_t sx = sc + 4 * (8 * NT * h + 8 * q + 2 * t);
-          float d[4];
-          block_mma(d, wgt, lds16<0>(x + get), lds16<0>(x + (get ^ 64u)));
+          BlockSum d;
+          d.mma(wgt, lds16<0>(x + get), lds16<0>(x + (get ^ 64u)));
           const float c0 = sw * lds4<0>(sx), c1 = sw * lds4<4>(sx);
-          acc[q][0] = fmaf(d[0], c0, acc[q][0]);
-          acc[q][1] = fmaf(d[1], c1, acc[q][1]);
-          acc[q][2] = fmaf(d[2], c0, acc[q][2]);
-          acc[q][3] = fmaf(d[3], c1, acc[q][3]);
+          acc[q][0] = fmaf(d.of(0), c0, acc[q][0]);
+          acc[q][1] = fmaf(d.of(1), c1, acc[q][1]);
+          acc[q][2] = fmaf(d.of(2), c0, acc[q][2]);
+          acc[q][3] = fmaf(d.of(3), c1, acc[q][3]);
         }
       }
       reads_before_refill();

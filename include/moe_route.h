@@ -364,13 +364,11 @@ MOE_API moe_status_t moe_fp8_matmul(const void* a, const float* a_scale, const v
                                     const float* b_scale, const moe_fp8_matmul_t* mm, void* out,
                                     void* stream);
 /* Workspace bytes of the product (0 if mm is invalid; mm's workspace fields
- * are ignored). A workspace of the most bytes needed serves several shapes
- * when it is initialised again, on the stream, before a call of another shape. */
+ * are ignored). One workspace serves any shapes that it is large enough for. */
 MOE_API size_t moe_fp8_matmul_workspace_bytes(const moe_fp8_matmul_t* mm);
-/* Zeroes the workspace's control words and counters; enqueued once before the
- * first use of a fresh workspace, and after a device timeout (which
- * moe_read_device_status reports for a moe_cfg_t with these workspace
- * fields). */
+/* Zeroes the workspace's control words; enqueued once before the first use of
+ * a fresh workspace. Its status is read with moe_read_device_status for a
+ * moe_cfg_t with these workspace fields. */
 MOE_API moe_status_t moe_fp8_matmul_init(const moe_fp8_matmul_t* mm, void* stream);
 
 /* Workspace of the two calls below for this cfg (0 if invalid), and its

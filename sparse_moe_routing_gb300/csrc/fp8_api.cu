@@ -43,27 +43,23 @@ moe_status_t validate_mm(const moe_fp8_matmul_t* m) {
 
 struct MmPlan {
   int tiles, ksplit;
-  size_t counters, partial, total;
+  size_t partial, total;
 };
-// Fewer tiles than half the SMs: k is split over CTAs, at least four blocks
+// Fewer tiles than half the SMs: k is split over CTAs, at least three blocks
 // each.
 MmPlan mm_plan(const moe_fp8_matmul_t& m) {
   MmPlan p{};
   p.tiles = ((m.M + kBm - 1) / kBm) * ((m.N + kBn - 1) / kBn);
   p.ksplit = 1;
-  p.counters = align256(sizeof(Ctrl));
-  p.partial = p.total = p.counters;
+  p.partial = p.total = align256(sizeof(Ctrl));
   if (m.M <= kF8FewTokens) return p;
   const int KB = f8_blocks(m.K);
   if (p.tiles > 0 && 2 * p.tiles <= kSms) {
     int s = kSms / p.tiles;
-    if (s > KB / 4) s = KB / 4;
+    if (s > KB / 3) s = KB / 3;
     if (s > 1) p.ksplit = s;
   }
-  if (p.ksplit > 1) {
-    p.partial = p.counters + align256((size_t)p.tiles * kF8TileCounters * sizeof(unsigned));
-    p.total = p.partial + (size_t)p.ksplit * p.tiles * kBm * kBn * 4;
-  }
+  if (p.ksplit > 1) p.total = p.partial + (size_t)p.ksplit * p.tiles * kBm * kBn * 4;
   return p;
 }
 
@@ -269,7 +265,6 @@ moe_status_t enqueue_tc(const void* x, const float* r_attn, const int32_t* ids, 
   a.E = E;
   a.T = T;
   a.P = P;
-  a.arows = kBm;
   a.ksplit = 1;
   const uint64_t rows = (uint64_t)P + T;
   const auto map = [&](CUtensorMap* m, const moe_bank_t& bk, uint64_t n, int K, uint32_t box) {
@@ -399,7 +394,7 @@ moe_status_t moe_fp8_matmul_init(const moe_fp8_matmul_t* mm, void* stream) {
   const MmPlan p = mm_plan(*mm);
   if (!mm->workspace || !aligned(mm->workspace, 256) || mm->workspace_bytes < p.total)
     return MOE_ERR_WORKSPACE;
-  return cuda_status(cudaMemsetAsync(mm->workspace, 0, p.partial, (cudaStream_t)stream));
+  return cuda_status(cudaMemsetAsync(mm->workspace, 0, sizeof(Ctrl), (cudaStream_t)stream));
 }
 
 moe_status_t moe_fp8_matmul(const void* a, const float* a_scale, const void* b, const float* b_scale,
@@ -434,8 +429,7 @@ moe_status_t moe_fp8_matmul(const void* a, const float* a_scale, const void* b, 
   g.a_scale = a_scale;
   g.b_scale0 = g.b_scale1 = g.b_scale2 = g.b_scale3 = b_scale;
   g.out = out;
-  g.partial = reinterpret_cast<float4*>(ws + p.partial);
-  g.counters = reinterpret_cast<unsigned*>(ws + p.counters);
+  g.partial = reinterpret_cast<float*>(ws + p.partial);
   g.ctrl = reinterpret_cast<Ctrl*>(ws);
   g.K = mm->K;
   g.rows = mm->M;
@@ -444,14 +438,16 @@ moe_status_t moe_fp8_matmul(const void* a, const float* a_scale, const void* b, 
   g.b_blocks = f8_blocks(mm->N);
   g.a_blocks = f8_blocks(mm->K);
   g.ldo = mm->ldo;
-  g.arows = kBm;
   g.ksplit = p.ksplit;
   g.out_bf16 = bf16 ? 1 : 0;
   g.out_vec = aligned(out, 16) && (mm->ldo * (bf16 ? 2 : 4)) % 16 == 0 ? 1 : 0;
   g.wait_ns = launch_wait_limit(MOE_KERNEL_F8_MATMUL, &g.stall);
-  return cuda_status(run_kernel(MOE_KERNEL_F8_MATMUL, st, [&] {
+  cudaError_t e = run_kernel(MOE_KERNEL_F8_MATMUL, st, [&] {
     return launch_f8_tc(kF8Dense, m, g, p.tiles * p.ksplit, st);
-  }));
+  });
+  if (e != cudaSuccess) return MOE_ERR_CUDA;
+  if (p.ksplit == 1) return MOE_OK;
+  return cuda_status(run_kernel(MOE_KERNEL_F8_MATMUL, st, [&] { return launch_f8_split_sum(g, st); }));
 }
 
 size_t moe_fp8_workspace_bytes(const moe_cfg_t* cfg) {

@@ -17,8 +17,11 @@
 //    form that the down product reads;
 //  * down: the routing weight (or the shared gate) applied, rows out in bf16;
 //  * dense: one product, bf16 or fp32 out, k split over CTAs when there are
-//    few tiles (fp32 partial sums; the part of a tile that ends last adds them
-//    in split order).
+//    few tiles (fp32 partial sums, which a second launch adds in split order).
+//
+// A thread's results are one row's, so that storing them as they lie would
+// touch 32 rows an instruction; eight lanes first exchange 16-byte pieces, and
+// an instruction then writes whole 128-byte lines of four rows.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -81,6 +84,64 @@ __device__ __forceinline__ void copy4_async(float* dst, const float* src, bool v
 // Arrives on `bar` once this thread's copies so far have landed.
 __device__ __forceinline__ void copies_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// c[j] is piece j of this lane's row; afterwards c[i] is piece lane % 8 of row
+// 8 (lane / 8) + i of the warp's 32.
+__device__ __forceinline__ void exchange8(uint4 (&c)[8], int lane) {
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int a = 0; a < 8; ++a) {
+      if (a & o) continue;
+      const int b = a | o;
+      uint4 send = up ? c[a] : c[b];
+      send.x = __shfl_xor_sync(0xffffffffu, send.x, o);
+      send.y = __shfl_xor_sync(0xffffffffu, send.y, o);
+      send.z = __shfl_xor_sync(0xffffffffu, send.z, o);
+      send.w = __shfl_xor_sync(0xffffffffu, send.w, o);
+      if (up)
+        c[a] = send;
+      else
+        c[b] = send;
+    }
+  }
+}
+__device__ __forceinline__ uint4 four_floats(const float* v) {
+  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                    __float_as_uint(v[3]));
+}
+__device__ __forceinline__ uint4 eight_bf16(const float* v, float s) {
+  return make_uint4(pack_bf16x2(s * v[0], s * v[1]), pack_bf16x2(s * v[2], s * v[3]),
+                    pack_bf16x2(s * v[4], s * v[5]), pack_bf16x2(s * v[6], s * v[7]));
+}
+// Stores the exchanged pieces: `at` the address of the lane's piece in the
+// warp's first row, rows `pitch` elements apart of which `rows` exist, `left`
+// columns from the lane's piece on; whole pieces where `vec`.
+template <typename T>
+__device__ __forceinline__ void store8(T* at, long long pitch, const uint4 (&c)[8], int rows, int left,
+                                       bool vec, int lane) {
+  constexpr int kPer = 16 / sizeof(T);
+  const int r0 = lane & 24;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (r0 + i >= rows) break;
+    T* dst = at + (r0 + i) * pitch;
+    if (vec && left >= kPer) {
+      st_global_v4(dst, c[i].x, c[i].y, c[i].z, c[i].w);
+    } else {
+      const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+#pragma unroll
+      for (int z = 0; z < kPer; ++z) {
+        if (z >= left) continue;
+        if (sizeof(T) == 4)
+          reinterpret_cast<uint32_t*>(dst)[z] = w[z & 3];
+        else
+          reinterpret_cast<uint16_t*>(dst)[z] = (uint16_t)(w[z >> 1] >> (16 * (z & 1)));
+      }
+    }
+  }
 }
 
 struct Item {
@@ -222,7 +283,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
       // -------------------------------------------------------------- producer
       if (lane == 0) {
-        const uint32_t bytes = (uint32_t)a.arows * BK + kStageB;
         int stage = 0;
         uint32_t ph = 0;
         bool alive = true;
@@ -240,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
             }
             uint64_t* bar = &full[stage];
-            mbar_expect_tx(bar, bytes);
+            mbar_expect_tx(bar, kStageA + kStageB);
             tma_load_2d(sA + stage * kStageA, &tmA, bar, kb * BK, arow);
             tma_load_2d(sB + stage * kStageB, b0, bar, kb * BK, brow);
             if (MODE == kF8GateUp)
@@ -438,89 +498,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (part == 0) a.out_scale[row * a.out_blocks + it.nt] = __uint_as_float(sbits);
         }
-      } else if (MODE == kF8Down) {
-        if (valid) {
-          const int col = it.nt * BN + part * kPartCols;
-          __nv_bfloat16* dst =
-              static_cast<__nv_bfloat16*>(a.out) + ((size_t)it.row0 + i) * a.ldo + col;
-#pragma unroll
-          for (int v = 0; v < kPartCols / 8; ++v) {
-            if (col + 8 * v < a.n_cols) {
-              uint32_t w[4];
-#pragma unroll
-              for (int z = 0; z < 4; ++z)
-                w[z] = pack_bf16x2(al * sum[8 * v + 2 * z], al * sum[8 * v + 2 * z + 1]);
-              st_global_v4(dst + 8 * v, w[0], w[1], w[2], w[3]);
-            }
-          }
-        }
       } else {
+        // this warp's 32 rows x 64 columns, the first at row wrow of the group
+        const int wrow = it.m * BM + q * 32, rows = it.rows - wrow;
         const int col = it.nt * BN + part * kPartCols;
-        bool write = true;
-        if (a.ksplit > 1) {
-          // this warp's 32 rows x 64 columns of the tile, fp32, columns in
-          // fours: [split][tile][64 column groups][128 rows]
-          const int tiles = n_rb * a.n_tiles;
-          float4* mine = a.partial + (((size_t)it.split * tiles + it.tile) * 64 + part * 16) * BM + r;
+        const int left = (MODE == kF8Dense && a.ksplit > 1 ? BN * a.n_tiles : a.n_cols) - col;
+        uint4 c[8];
+        if (MODE == kF8Down || (a.ksplit == 1 && a.out_bf16)) {
+          const int piece = 8 * (lane & 7);
 #pragma unroll
-          for (int j = 0; j < kPartCols / 4; ++j)
-            if (valid)
-              __stcg(mine + (size_t)j * BM, make_float4(sum[4 * j], sum[4 * j + 1], sum[4 * j + 2],
-                                                        sum[4 * j + 3]));
-          __threadfence();
-          __syncwarp();
-          unsigned prev = 0;
-          unsigned* ctr = a.counters + it.tile * kEpiWarps + (warp - kEpiWarp0);
-          if (lane == 0) prev = atomicAdd(ctr, 1u);
-          prev = __shfl_sync(0xffffffffu, prev, 0);
-          write = (int)prev == a.ksplit - 1;
-          if (write) {
-            if (lane == 0) *ctr = 0u;
-            __threadfence();
+          for (int j = 0; j < 8; ++j) c[j] = eight_bf16(sum + 8 * j, MODE == kF8Down ? al : 1.f);
+          exchange8(c, lane);
+          store8(static_cast<__nv_bfloat16*>(a.out) + ((size_t)it.row0 + wrow) * a.ldo + col + piece, a.ldo, c,
+                 rows, left - piece, MODE == kF8Down || a.out_vec, lane);
+        } else {
+          // split k: fp32 rows of the tile, [split][tile][128 rows][256 columns]
+          const bool part_sum = a.ksplit > 1;
+          float* out = part_sum ? a.partial + (((size_t)it.split * n_rb * a.n_tiles + it.tile) * BM + q * 32) * BN +
+                                      part * kPartCols
+                                : static_cast<float*>(a.out) + (size_t)wrow * a.ldo + col;
+          const long long pitch = part_sum ? BN : a.ldo;
 #pragma unroll
-            for (int j = 0; j < kPartCols; ++j) sum[j] = 0.f;
-            for (int s = 0; s < a.ksplit; ++s) {
-              const float4* o = a.partial + (((size_t)s * tiles + it.tile) * 64 + part * 16) * BM + r;
+          for (int h = 0; h < 2; ++h) {
+            const int piece = 32 * h + 4 * (lane & 7);
 #pragma unroll
-              for (int j = 0; j < kPartCols / 4; ++j) {
-                const float4 p = valid ? __ldcg(o + (size_t)j * BM) : make_float4(0.f, 0.f, 0.f, 0.f);
-                sum[4 * j] += p.x;
-                sum[4 * j + 1] += p.y;
-                sum[4 * j + 2] += p.z;
-                sum[4 * j + 3] += p.w;
-              }
-            }
-          }
-        }
-        if (write && valid) {
-          if (a.out_bf16) {
-            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (size_t)i * a.ldo + col;
-#pragma unroll
-            for (int v = 0; v < kPartCols / 8; ++v) {
-              if (a.out_vec && col + 8 * v + 8 <= a.n_cols) {
-                uint32_t w[4];
-#pragma unroll
-                for (int z = 0; z < 4; ++z) w[z] = pack_bf16x2(sum[8 * v + 2 * z], sum[8 * v + 2 * z + 1]);
-                st_global_v4(dst + 8 * v, w[0], w[1], w[2], w[3]);
-              } else {
-#pragma unroll
-                for (int z = 0; z < 8; ++z)
-                  if (col + 8 * v + z < a.n_cols) dst[8 * v + z] = __float2bfloat16_rn(sum[8 * v + z]);
-              }
-            }
-          } else {
-            float* dst = static_cast<float*>(a.out) + (size_t)i * a.ldo + col;
-#pragma unroll
-            for (int v = 0; v < kPartCols / 4; ++v) {
-              if (a.out_vec && col + 4 * v + 4 <= a.n_cols) {
-                *reinterpret_cast<float4*>(dst + 4 * v) =
-                    make_float4(sum[4 * v], sum[4 * v + 1], sum[4 * v + 2], sum[4 * v + 3]);
-              } else {
-#pragma unroll
-                for (int z = 0; z < 4; ++z)
-                  if (col + 4 * v + z < a.n_cols) dst[4 * v + z] = sum[4 * v + z];
-              }
-            }
+            for (int j = 0; j < 8; ++j) c[j] = four_floats(sum + 32 * h + 4 * j);
+            exchange8(c, lane);
+            store8(out + piece, pitch, c, rows, left - piece, part_sum || a.out_vec, lane);
           }
         }
       }
@@ -541,6 +545,53 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
                  "r"(kTmemCols));
+  }
+}
+
+// out = the splits' partial sums, added in split order; a thread per four
+// columns of a row.
+__global__ void __launch_bounds__(256) f8_split_sum_kernel(F8TcArgs a) {
+  const int fours = (a.n_cols + 3) / 4;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int row = (int)(i / fours), col = (int)(i - (long long)row * fours) * 4;
+  pdl_wait();
+  pdl_trigger();
+  if (row >= a.rows) return;
+  // the products' tile order (item_at)
+  const int n_rb = (a.rows + BM - 1) / BM, rb = row / BM, nt = col / BN;
+  const int band = rb / kBand, width = min(kBand, n_rb - band * kBand);
+  const int tile = band * kBand * a.n_tiles + nt * width + (rb - band * kBand);
+  const size_t plane = (size_t)n_rb * a.n_tiles * BM * BN;
+  const float* p = a.partial + ((size_t)tile * BM + row % BM) * BN + col % BN;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int s = 0; s < a.ksplit; ++s) {
+    const float4 o = __ldcg(reinterpret_cast<const float4*>(p + s * plane));
+    v.x += o.x;
+    v.y += o.y;
+    v.z += o.z;
+    v.w += o.w;
+  }
+  const float y[4] = {v.x, v.y, v.z, v.w};
+  const size_t at = (size_t)row * a.ldo + col;
+  if (a.out_bf16) {
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + at;
+    if (a.out_vec && col + 4 <= a.n_cols) {
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+    } else {
+#pragma unroll
+      for (int z = 0; z < 4; ++z)
+        if (col + z < a.n_cols) dst[z] = __float2bfloat16_rn(y[z]);
+    }
+  } else {
+    float* dst = static_cast<float*>(a.out) + at;
+    if (a.out_vec && col + 4 <= a.n_cols) {
+      *reinterpret_cast<float4*>(dst) = v;
+    } else {
+#pragma unroll
+      for (int z = 0; z < 4; ++z)
+        if (col + z < a.n_cols) dst[z] = y[z];
+    }
   }
 }
 
@@ -576,6 +627,11 @@ cudaError_t launch_f8_tc(int mode, const F8TcMaps& m, const F8TcArgs& a, int max
   if (mode == kF8Down) return launch_t<kF8Down>(m, a, max_items, st);
   if (mode == kF8Dense) return launch_t<kF8Dense>(m, a, max_items, st);
   return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_f8_split_sum(const F8TcArgs& a, cudaStream_t st) {
+  const long long n = (long long)a.rows * ((a.n_cols + 3) / 4);
+  return launch_pdl(f8_split_sum_kernel, dim3((unsigned)((n + 255) / 256)), 256, 0, st, a);
 }
 
 }  // namespace moe

@@ -268,7 +268,6 @@ cudaError_t launch_f8_few_matmul(const F8MatmulArgs& a, cudaStream_t st);
 
 // Tensor-core products (fp8_tc.cu).
 enum F8Mode { kF8GateUp = 0, kF8Down = 1, kF8Dense = 2 };
-constexpr int kF8TileCounters = 16;  // one per epilogue warp
 struct F8TcArgs {
   const int2* rowblocks;       // grouped: (group, row block) list
   const int32_t* n_rowblocks;
@@ -281,8 +280,7 @@ struct F8TcArgs {
   const float *b_scale2, *b_scale3;  // shared expert
   void* out;                   // codes | bf16 rows | dense out
   float* out_scale;            // gate/up: [rows][out_blocks]
-  float4* partial;             // dense, ksplit > 1
-  unsigned* counters;          // dense, ksplit > 1: [tiles][kF8TileCounters], zero between launches
+  float* partial;              // dense, ksplit > 1: [ksplit][tiles][128][256]
   Ctrl* ctrl;
   int E, T, P, K;
   int rows;                    // dense: rows of A
@@ -290,7 +288,7 @@ struct F8TcArgs {
   int brows, b_blocks;         // rows of one expert in B's view, scale rows of it
   int a_blocks, out_blocks;    // scales per row of a_scale and of out_scale
   long long ldo;
-  int shared_only, arows;      // arows: box height of A's map
+  int shared_only;
   int ksplit, out_bf16, out_vec;
   uint64_t wait_ns;
   int stall;
@@ -303,6 +301,8 @@ bool f8_make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
                  uint32_t box_rows);
 cudaError_t launch_f8_tc(int mode, const F8TcMaps& m, const F8TcArgs& a, int max_items,
                          cudaStream_t st);
+// Adds a dense product's partial sums (ksplit > 1) into its output.
+cudaError_t launch_f8_split_sum(const F8TcArgs& a, cudaStream_t st);
 
 // Raises `kernel`'s dynamic shared-memory opt-in limit to at least `bytes`
 // on the current device; `limits` holds the value set so far per device

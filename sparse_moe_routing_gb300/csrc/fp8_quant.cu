@@ -18,47 +18,78 @@
 namespace moe {
 namespace {
 
-// Eight consecutive values at p (16-byte aligned in the vector form).
+// Eight consecutive values of a row as they lie in memory, zeros past its end.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]);
+struct Eight;
 template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
-  Chunk<__nv_bfloat16>::unpack(ldg_stream(p), v);
-}
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
-  Chunk<float>::unpack(ldg_stream(p), v);
-  Chunk<float>::unpack(ldg_stream(p + 4), v + 4);
-}
-
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8_upto(const T* row, int c, int cols, float (&v)[8]) {
-  if (VEC) {
-    if (c < cols) {
-      load8(row + c, v);
+struct Eight<__nv_bfloat16> {
+  uint4 raw;
+  template <bool VEC>
+  __device__ __forceinline__ void load(const __nv_bfloat16* row, int c, int cols) {
+    raw = make_uint4(0u, 0u, 0u, 0u);
+    if (VEC) {
+      if (c < cols) raw = ldg_stream(row + c);
     } else {
+      uint32_t w[4] = {};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.f;
+      for (int j = 0; j < 8; ++j)
+        if (c + j < cols)
+          w[j >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[c + j] << (16 * (j & 1));
+      raw = make_uint4(w[0], w[1], w[2], w[3]);
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? load_act(row, (size_t)(c + j)) : 0.f;
   }
-}
-
-__device__ __forceinline__ uint32_t mag_max8(const float (&v)[8]) {
-  uint32_t m = 0;
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    Chunk<__nv_bfloat16>::unpack(raw, v);
+  }
+  // Largest magnitude's bits: those of a bf16 number order like its value too,
+  // two at a time.
+  __device__ __forceinline__ uint32_t mag() const {
+    constexpr uint32_t kAbs = 0x7FFF7FFFu;
+    const uint32_t m = __vmaxu2(__vmaxu2(raw.x & kAbs, raw.y & kAbs), __vmaxu2(raw.z & kAbs, raw.w & kAbs));
+    return max(m << 16, m & 0xFFFF0000u);
+  }
+};
+template <>
+struct Eight<float> {
+  uint4 raw[2];
+  template <bool VEC>
+  __device__ __forceinline__ void load(const float* row, int c, int cols) {
+    raw[0] = raw[1] = make_uint4(0u, 0u, 0u, 0u);
+    if (VEC) {
+      if (c < cols) {
+        raw[0] = ldg_stream(row + c);
+        raw[1] = ldg_stream(row + c + 4);
+      }
+    } else {
+      uint32_t w[8] = {};
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, f8_mag(v[j]));
-  return m;
-}
+      for (int j = 0; j < 8; ++j)
+        if (c + j < cols) w[j] = __float_as_uint(row[c + j]);
+      raw[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      raw[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    Chunk<float>::unpack(raw[0], v);
+    Chunk<float>::unpack(raw[1], v + 4);
+  }
+  __device__ __forceinline__ uint32_t mag() const {
+    constexpr uint32_t kAbs = 0x7FFFFFFFu;
+    return max(max(max(raw[0].x & kAbs, raw[0].y & kAbs), max(raw[0].z & kAbs, raw[0].w & kAbs)),
+               max(max(raw[1].x & kAbs, raw[1].y & kAbs), max(raw[1].z & kAbs, raw[1].w & kAbs)));
+  }
+};
+
 // Maximum over the 16 lanes of a half warp.
 __device__ __forceinline__ uint32_t half_max(uint32_t m) {
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
 }
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
+template <typename T>
+__device__ __forceinline__ uint2 codes8(const Eight<T>& e, float inv) {
+  float v[8];
+  e.values(v);
   return make_uint2(f8_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
                     f8_pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
 }
@@ -77,38 +108,38 @@ __device__ __forceinline__ void store_codes8(uint8_t* row, int c, int cols, uint
 }
 
 constexpr int kQuantThreads = 256;
-constexpr int kQuantUnroll = 4;  // blocks per half warp in flight
 
-template <typename T, bool VEC>
+// UNROLL blocks per half warp, all in flight at once. One pass per CTA: the
+// hardware hands CTAs out as others end (a grid of eight per SM that walked on
+// left the last of 1.7 rounds half empty: 17.5 us for 4097 x 4096 fp32).
+template <typename T, bool VEC, int UNROLL>
 __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(F8QuantArgs a) {
   pdl_wait();
   pdl_trigger();
+  constexpr int kHalves = kQuantThreads / 16;
   const int nb = f8_blocks(a.cols);
   const long long total = (long long)a.rows * nb;
   const int lane16 = threadIdx.x & 15;
-  const long long half = (long long)blockIdx.x * (kQuantThreads / 16) + (threadIdx.x >> 4);
-  const long long step = (long long)gridDim.x * (kQuantThreads / 16);
-  // whole warps stay in the loop: both halves of a warp shuffle together
-  for (long long b0 = half; b0 - (half & 1) < total; b0 += step * kQuantUnroll) {
-    float v[kQuantUnroll][8];
-    long long row[kQuantUnroll];
-    int blk[kQuantUnroll];
+  const long long b0 = (long long)blockIdx.x * (kHalves * UNROLL) + (threadIdx.x >> 4);
+  Eight<T> v[UNROLL];
+  long long row[UNROLL];
+  int blk[UNROLL];
 #pragma unroll
-    for (int u = 0; u < kQuantUnroll; ++u) {
-      const long long b = b0 + u * step;
-      row[u] = b < total ? b / nb : -1;
-      blk[u] = b < total ? (int)(b - row[u] * nb) : 0;
-      const T* src = static_cast<const T*>(a.x) + (row[u] < 0 ? 0 : row[u]) * a.ldx;
-      load8_upto<T, VEC>(src, blk[u] * kF8Block + lane16 * 8, row[u] < 0 ? 0 : a.cols, v[u]);
-    }
+  for (int u = 0; u < UNROLL; ++u) {
+    const long long b = b0 + u * kHalves;
+    const bool in = b < total;
+    row[u] = in ? (total <= 0x7FFFFFFF ? (long long)((int)b / nb) : b / nb) : -1;
+    blk[u] = in ? (int)(b - row[u] * nb) : 0;
+    const T* src = static_cast<const T*>(a.x) + (in ? row[u] : 0) * a.ldx;
+    v[u].template load<VEC>(src, blk[u] * kF8Block + lane16 * 8, in ? a.cols : 0);
+  }
 #pragma unroll
-    for (int u = 0; u < kQuantUnroll; ++u) {
-      const uint32_t sb = f8_scale_bits(half_max(mag_max8(v[u])));
-      if (row[u] < 0) continue;
-      store_codes8<VEC>(a.codes + row[u] * a.ldq, blk[u] * kF8Block + lane16 * 8, a.cols,
-                        codes8(v[u], f8_inverse(sb)));
-      if (lane16 == 0) a.scales[row[u] * nb + blk[u]] = __uint_as_float(sb);
-    }
+  for (int u = 0; u < UNROLL; ++u) {
+    const uint32_t sb = f8_scale_bits(half_max(v[u].mag()));
+    if (row[u] < 0) continue;
+    store_codes8<VEC>(a.codes + row[u] * a.ldq, blk[u] * kF8Block + lane16 * 8, a.cols,
+                      codes8(v[u], f8_inverse(sb)));
+    if (lane16 == 0) a.scales[row[u] * nb + blk[u]] = __uint_as_float(sb);
   }
 }
 
@@ -119,23 +150,22 @@ __global__ void __launch_bounds__(kQuantThreads) quant_tiles_kernel(F8QuantArgs 
   pdl_wait();
   pdl_trigger();
   const int nb = f8_blocks(a.cols), nr = f8_blocks(a.rows);
-  const long long tile = blockIdx.x;
-  const int cb = (int)(tile % nb);
-  const long long rest = tile / nb;
-  const int rb = (int)(rest % nr);
+  const int tile = blockIdx.x;
+  const int cb = tile % nb, rest = tile / nb;
+  const int rb = rest % nr;
   const long long mat = rest / nr;
   const int r0 = rb * kF8Block + (threadIdx.x >> 4), c = cb * kF8Block + (threadIdx.x & 15) * 8;
   const T* x = static_cast<const T*>(a.x) + mat * (long long)a.rows * a.ldx;
   uint8_t* codes = a.codes + mat * (long long)a.rows * a.ldq;
-  float v[8][8];
+  Eight<T> v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = r0 + 16 * i;
-    load8_upto<T, VEC>(x + (long long)min(r, a.rows - 1) * a.ldx, c, r < a.rows ? a.cols : 0, v[i]);
+    v[i].template load<VEC>(x + (long long)min(r, a.rows - 1) * a.ldx, c, r < a.rows ? a.cols : 0);
   }
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, mag_max8(v[i]));
+  for (int i = 0; i < 8; ++i) m = max(m, v[i].mag());
   m = __reduce_max_sync(0xffffffffu, m);
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
   __syncthreads();
@@ -160,11 +190,11 @@ __global__ void __launch_bounds__(kQuantThreads) quant_pack_kernel(F8PackArgs a)
   const int lane16 = threadIdx.x & 15;
   const long long half = (long long)blockIdx.x * (kQuantThreads / 16) + (threadIdx.x >> 4);
   const long long b = half;
-  float v[8];
+  Eight<__nv_bfloat16> v;
   const long long t = b < total ? b / nb : 0;
   const int blk = (int)(b - t * nb), c = blk * kF8Block + lane16 * 8;
-  load8_upto<__nv_bfloat16, true>(a.x + t * a.d, c, b < total ? a.d : 0, v);
-  const uint32_t sb = f8_scale_bits(half_max(mag_max8(v)));
+  v.load<true>(a.x + t * a.d, c, b < total ? a.d : 0);
+  const uint32_t sb = f8_scale_bits(half_max(v.mag()));
   if (b >= total) return;
   const uint2 q = codes8(v, f8_inverse(sb));
   for (int s = 0; s < a.k + a.own_rows; ++s) {
@@ -185,14 +215,16 @@ cudaError_t launch_quant_t(const F8QuantArgs& a, bool tiles, cudaStream_t st) {
                : launch_pdl(quant_tiles_kernel<T, false>, dim3((unsigned)n), kQuantThreads, 0, st, a);
   }
   const long long blocks = (long long)a.rows * f8_blocks(a.cols);
-  const long long per = (long long)(kQuantThreads / 16) * kQuantUnroll;
-  const long long most = (long long)tc_sm_count() * 8;
-  // small calls: one block per half warp, spread over the SMs
-  long long grid = (blocks + kQuantThreads / 16 - 1) / (kQuantThreads / 16);
-  if (grid > most) grid = (blocks + per - 1) / per;
-  if (grid > most) grid = most;
-  return vec ? launch_pdl(quant_rows_kernel<T, true>, dim3((unsigned)grid), kQuantThreads, 0, st, a)
-             : launch_pdl(quant_rows_kernel<T, false>, dim3((unsigned)grid), kQuantThreads, 0, st, a);
+  // one block per half warp until every SM has eight CTAs of them, then four
+  constexpr int kHalves = kQuantThreads / 16;
+  const bool one = blocks <= (long long)tc_sm_count() * 8 * kHalves;
+  const long long per = one ? kHalves : kHalves * 4;
+  const dim3 grid((unsigned)((blocks + per - 1) / per));
+  if (one)
+    return vec ? launch_pdl(quant_rows_kernel<T, true, 1>, grid, kQuantThreads, 0, st, a)
+               : launch_pdl(quant_rows_kernel<T, false, 1>, grid, kQuantThreads, 0, st, a);
+  return vec ? launch_pdl(quant_rows_kernel<T, true, 4>, grid, kQuantThreads, 0, st, a)
+             : launch_pdl(quant_rows_kernel<T, false, 4>, grid, kQuantThreads, 0, st, a);
 }
 
 }  // namespace

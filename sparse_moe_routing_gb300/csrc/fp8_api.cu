@@ -74,8 +74,17 @@ moe_cfg_t route_cfg(const moe_cfg_t& c) {
   return r;
 }
 
+// The two kernels for a few tokens, unless wide experts average three pairs or
+// more each: mma.sync then meets every weight with several chunks' worth of
+// columns, and the tensor-core products are faster. us, few / tensor cores: 256
+// experts T=8 48.6 / 62, T=16 78.5 / 85; 60 experts T=16 102 / 121; 64 experts
+// T=16 105 / 98; 8 wide experts T=4 182 / 220, T=8 253 / 265, T=16 313 / 236;
+// the tiny shape T=16 (4 pairs each) 12.5 / 20.
 bool use_few(const moe_cfg_t& c) {
-  return c.path != MOE_PATH_TC && f8_few_ok(c.T, c.d_model, c.top_k);
+  if (c.path == MOE_PATH_TC || !f8_few_ok(c.T, c.d_model, c.top_k)) return false;
+  if (c.path == MOE_PATH_GEMV) return true;
+  const bool wide = (long long)c.d_model * c.d_ff >= (4ll << 20);
+  return !(wide && c.T * c.top_k >= 3 * c.n_experts);
 }
 
 moe_status_t validate_f8(const moe_cfg_t* c) {

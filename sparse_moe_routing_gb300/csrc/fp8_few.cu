@@ -132,6 +132,19 @@ template <int N>
 __device__ __forceinline__ void lists_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
 }
+// The shared expert's chunks, after the n routed ones (one warp calls it).
+__device__ __forceinline__ void finish_lists(const F8ExpertsArgs& a, FewLists& L, int n, int lane) {
+  const int ns = a.Is > 0 ? (a.T + 7) / 8 : 0;
+  if (lane < ns) {
+    L.start[n + lane] = (short)(8 * lane);
+    L.expert[n + lane] = (short)a.E;
+    L.count[n + lane] = (short)min(8, a.T - 8 * lane);
+  }
+  if (lane == 0) {
+    L.n_routed = n;
+    L.n_chunks = n + ns;
+  }
+}
 template <int N>
 __device__ __forceinline__ void build_lists(const F8ExpertsArgs& a, FewLists& L) {
   const int P = a.T * a.k, tid = threadIdx.x, lane = tid & 31;
@@ -179,16 +192,7 @@ __device__ __forceinline__ void build_lists(const F8ExpertsArgs& a, FewLists& L)
     }
     __syncwarp();
     for (int c = lane; c < n; c += 32) L.count[c] = (short)((c + 1 < n ? L.start[c + 1] : P) - L.start[c]);
-    const int ns = a.Is > 0 ? (a.T + 7) / 8 : 0;
-    if (lane < ns) {
-      L.start[n + lane] = (short)(8 * lane);
-      L.expert[n + lane] = (short)a.E;
-      L.count[n + lane] = (short)min(8, a.T - 8 * lane);
-    }
-    if (lane == 0) {
-      L.n_routed = n;
-      L.n_chunks = n + ns;
-    }
+    finish_lists(a, L, n, lane);
   }
   lists_sync<N>();
 }
@@ -287,58 +291,59 @@ __global__ void __launch_bounds__(kGuThreads, 1)
     const int items = item_count();
     Walk now{group * (int)gridDim.x + (int)blockIdx.x, 0, 0};
     settle(now);
-    // the loads' walk, kGuAhead slots ahead of the arithmetic's
-    Walk ahead = now;
+    // One loop fills slots and works them off, so that every piece of its code
+    // exists once: a call of one token runs each instruction once or twice, and
+    // fetching them is much of its time.
+    Walk ahead = now;  // the loads' walk, kGuAhead slots ahead of the arithmetic's
     const int steps = (pairs - w + nsplit - 1) / nsplit;  // pairs of blocks of an item for this warp
     const CUtensorMap *mg = &tmG, *mu = &tmU;
     const float* ps = a.Sg;  // lanes 0, 1: gate's scales, lanes 2, 3: up's
-    int todo = 0, row = 0, kb = 0;
-    auto open = [&]() {
-      todo = ahead.i < items ? steps : 0;
-      if (todo == 0) return;
-      const int e = L.expert[ahead.c];
-      const bool sh = e == a.E;
-      const int rows = sh ? a.Is : a.I;
-      row = (sh ? 0 : e * rows) + ahead.rb * kGuRows;
-      kb = 2 * w;
-      mg = sh ? &tmSG : &tmG;
-      mu = sh ? &tmSU : &tmU;
-      const int si = ((sh ? 0 : e * f8_blocks(rows)) + ahead.rb * kGuRows / kF8Block) * KB;
-      ps = (sh ? (lane & 2 ? a.Ssu : a.Ssg) : (lane & 2 ? a.Su : a.Sg)) + si;
-    };
+    int todo = 0, row = 0, kb = 0, filled = 0, jf = 0;
     uint8_t* ring = S.ring[warp][0];
-    auto load = [&](int j) {
-      if (todo == 0) return;
-      uint64_t* bar = &S.landed[warp][j];
-      if (lane == 0) {
-        uint8_t* dst = ring + j * kGuSlot;
-        const int k = kb * kF8Block;
-        tc::mbar_expect_tx(bar, kGuSlot);
-        tc::tma_load_2d(dst, mg, bar, k, row);
-        tc::tma_load_2d(dst + kBox16, mu, bar, k, row);
-        tc::tma_load_2d(dst + 2 * kBox16, mg, bar, k + kF8Block, row);  // zeros past the last block
-        tc::tma_load_2d(dst + 3 * kBox16, mu, bar, k + kF8Block, row);
-      }
-      if (lane < 4) copy4(&S.scale[warp][j][lane], ps + min(kb + (lane & 1), KB - 1), bar);
-      kb += 2 * nsplit;
-      if (--todo == 0) {
-        advance(ahead);
-        open();
-      }
-    };
-    if (steps > 0) open();
-    for (int j = 0; j < kGuAhead; ++j) load(j);
-    __syncthreads();  // the tokens' codes are there
-
     float acc[2][4] = {};
     const uint32_t get = get_at(g, t);
     const uint32_t xq32 = tc::smem_u32(xq) + 2 * w * kF8Block + 16 * t, xs32 = tc::smem_u32(xs) + 8 * w;
     const uint32_t ring32 = tc::smem_u32(ring), sc32 = tc::smem_u32(S.scale[warp]);
     uint32_t xr = 0, x0 = 0, x1 = 0, ph = 0;
-    int left = steps, r = 0, j = 0, kx = 2 * w;
-    bool fresh = true;
-    while (now.i < items) {
-      if (fresh) {  // the chunk's tokens: this lane's column, and its two sums' columns
+    int left = 0, r = 0, j = 0, kx = 0;
+    bool codes = false;
+    while (true) {
+      if (filled < kGuAhead && ahead.i < items && steps) {
+        if (todo == 0) {  // a new item
+          const int e = L.expert[ahead.c];
+          const bool sh = e == a.E;
+          const int rows = sh ? a.Is : a.I;
+          todo = steps;
+          row = (sh ? 0 : e * rows) + ahead.rb * kGuRows;
+          kb = 2 * w;
+          mg = sh ? &tmSG : &tmG;
+          mu = sh ? &tmSU : &tmU;
+          const int si = ((sh ? 0 : e * f8_blocks(rows)) + ahead.rb * kGuRows / kF8Block) * KB;
+          ps = (sh ? (lane & 2 ? a.Ssu : a.Ssg) : (lane & 2 ? a.Su : a.Sg)) + si;
+        }
+        uint64_t* bar = &S.landed[warp][jf];
+        if (lane == 0) {
+          uint8_t* dst = ring + jf * kGuSlot;
+          tc::mbar_expect_tx(bar, kGuSlot);
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {  // (zeros past the last block)
+            tc::tma_load_2d(dst + 2 * h * kBox16, mg, bar, (kb + h) * kF8Block, row);
+            tc::tma_load_2d(dst + (2 * h + 1) * kBox16, mu, bar, (kb + h) * kF8Block, row);
+          }
+        }
+        __syncwarp();
+        if (lane < 4) copy4(&S.scale[warp][jf][lane], ps + min(kb + (lane & 1), KB - 1), bar);
+        kb += 2 * nsplit;
+        if (--todo == 0) advance(ahead);
+        if (++jf == kGuAhead) jf = 0;
+        if (++filled < kGuAhead) continue;
+      }
+      if (!codes) {
+        codes = true;
+        __syncthreads();  // the tokens' codes are there
+      }
+      if (now.i >= items) break;
+      if (left == 0) {  // the chunk's tokens: this lane's column, and its two sums' columns
         const int start = L.start[now.c], last = L.count[now.c] - 1;
         const bool sh = now.c >= L.n_routed;
         auto token = [&](int q) {
@@ -348,9 +353,10 @@ __global__ void __launch_bounds__(kGuThreads, 1)
         xr = xq32 + token(g) * xstride;
         x0 = xs32 + token(2 * t) * KB * 4;
         x1 = xs32 + token(2 * t + 1) * KB * 4;
-        fresh = false;
+        left = steps;
+        kx = 2 * w;
       }
-      if (left) {
+      if (steps) {
         if (!f8_warp_wait(&S.landed[warp][j], ph, a.ctrl, kSiteFewFp8)) break;
         const uint32_t slot = ring32 + j * kGuSlot;
 #pragma unroll
@@ -380,7 +386,7 @@ __global__ void __launch_bounds__(kGuThreads, 1)
         kx += 2 * nsplit;
         reads_before_refill();
         __syncwarp();
-        load(j);
+        --filled;
         if (++j == kGuAhead) {
           j = 0;
           ph ^= 1u;
@@ -397,11 +403,8 @@ __global__ void __launch_bounds__(kGuThreads, 1)
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&S.full[at][group]);
-      left = steps;
-      kx = 2 * w;
       advance(now);
       ++r;
-      fresh = true;
     }
   } else {
     // While the others group the pairs and wait for their first weights, this
@@ -512,28 +515,31 @@ constexpr int kDnPitch = kDnCols + 1;
 constexpr int kDnSlot = 2 * (kBox16 + kBox8);  // weights and activations of two blocks
 constexpr int kDnArrivals = 20;  // weights, activations, 18 scales
 
-// WARPS warps with AHEAD slots in flight each. Eight warps where every CTA has
-// an SM of its own (96 KB of weights in flight), four where there are more CTAs
-// than SMs, so that two fit.
+// WARPS warps with AHEAD slots in flight each. Sixteen warps where every CTA
+// has an SM of its own (128 KB of weights in flight), six where there are more
+// CTAs than SMs, so that two fit. A warp's walk through a slot is a chain of
+// latencies, so that warps count more than slots: eight warps of three slots
+// took 53.8 us where sixteen of two take 48.4 (8 tokens, 256-expert shape,
+// both kernels), four of three 198 where six of two take 182 (4 tokens, 8
+// wide experts).
 template <int WARPS, int AHEAD>
 struct DnShared {
   uint8_t ring[WARPS][AHEAD][kDnSlot];
   uint64_t landed[WARPS][AHEAD];
   float scale[WARPS][AHEAD][20];  // of eight activation rows, two blocks; [16], [17]: weights
   FewLists lists;
-  float rowscale[1];  // [P + T] alpha | s_shared, then ysum [split][P + T][kDnPitch]
+  float ysum[1];  // [split][P + T][kDnPitch]
 };
 
 template <int WARPS, int AHEAD>
-__global__ void __launch_bounds__(WARPS * 32, 8 / WARPS)
+__global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1)
     f8_few_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmSW,
                        const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmSX,
                        const F8ExpertsArgs a) {
   extern __shared__ uint8_t smem_raw[];
   DnShared<WARPS, AHEAD>& S = *reinterpret_cast<DnShared<WARPS, AHEAD>*>(align1024(smem_raw));
   FewLists& L = S.lists;
-  float* rowscale = S.rowscale;
-  float* ysum = rowscale + a.T * a.k + a.T;
+  float* ysum = S.ysum;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   if (tid == 0) {
     for (int i = 0; i < WARPS * AHEAD; ++i) tc::mbar_init(&S.landed[0][0] + i, kDnArrivals);
@@ -546,8 +552,17 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS)
   // The ids and the weights are older than the gate/up kernel, which has
   // itself waited for its predecessor before letting this one start.
   build_lists<WARPS * 32>(a, L);
-  int split = 1;
-  while (L.n_chunks * split < WARPS && split * 2 <= (PRr > PRs ? PRr : PRs)) split *= 2;
+  // k split of a chunk: the one that leaves the busiest warp the fewest pairs
+  const int PR = PRr > PRs ? PRr : PRs, room = max(rows_all, 16 * WARPS);
+  int lsplit = 0, least = 0x7FFFFFFF;
+  for (int l = 0; (1 << l) <= min(PR, WARPS) && (rows_all << l) <= room; ++l) {
+    const int n = ((L.n_chunks << l) + WARPS - 1) / WARPS * ((PR + (1 << l) - 1) >> l);
+    if (n < least) {
+      least = n;
+      lsplit = l;
+    }
+  }
+  const int split = 1 << lsplit;
   const int walks = L.n_chunks * split;
   // A warp's walk over (chunk, k split) and the pairs of blocks of each.
   struct Walk {
@@ -555,95 +570,89 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS)
   };
   auto settle = [&](Walk& k) {  // to the next part that has a pair, if any
     for (; k.idx < walks; k.idx += WARPS) {
-      k.c = k.idx / split;
-      const int n = k.c >= L.n_routed ? PRs : PRr, s = k.idx - k.c * split;
-      k.left = (n - s + split - 1) / split;
+      k.c = k.idx >> lsplit;
+      const int n = k.c >= L.n_routed ? PRs : PRr, s = k.idx & (split - 1);
+      k.left = (n - s + split - 1) >> lsplit;
       k.kb = 2 * s;
       if (k.left > 0) return;
     }
     k.left = 0;
   };
-  // where a walk's next weights and activations lie
-  const CUtensorMap *mw = &tmW, *mx = &tmX;
-  const float *psw = a.Sd, *psx = a.Hs;
-  int wrow = 0, wb = 0, xrow = 0, xb = 0, last_w = 0, last_x = 0;
-  auto open_w = [&](const Walk& k) {
-    if (!k.left) return;
-    const int e = L.expert[k.c], blocks = e == a.E ? KBs : KBr;
-    const bool sh = e == a.E;
-    mw = sh ? &tmSW : &tmW;
-    wrow = (sh ? 0 : e * a.d) + col0;
-    wb = 2 * (k.idx - k.c * split);
-    last_w = blocks - 1;
-    psw = (sh ? a.Ssd : a.Sd) + ((sh ? 0 : (size_t)e * NB) + col0 / kF8Block) * blocks;
-  };
-  auto open_x = [&](const Walk& k) {
-    if (!k.left) return;
-    const bool sh = k.c >= L.n_routed;
-    mx = sh ? &tmSX : &tmX;
-    xrow = (sh ? P : 0) + L.start[k.c];
-    xb = 2 * (k.idx - k.c * split);
-    last_x = (sh ? KBs : KBr) - 1;
-    psx = a.Hs + (size_t)(xrow + min(lane & 7, L.count[k.c] - 1)) * a.hblocks;
-  };
-  uint8_t* ring = S.ring[warp][0];
-  // (boxes past the last block come as zeros)
-  auto load_w = [&](int j) {
-    uint64_t* bar = &S.landed[warp][j];
-    if (lane == 0) {
-      uint8_t* dst = ring + j * kDnSlot;
-      tc::mbar_expect_tx(bar, 2 * kBox16);
-      tc::tma_load_2d(dst, mw, bar, wb * kF8Block, wrow);
-      tc::tma_load_2d(dst + kBox16, mw, bar, (wb + 1) * kF8Block, wrow);
-    }
-    if (lane >= 16 && lane < 18) copy4(&S.scale[warp][j][lane], psw + min(wb + (lane & 1), last_w), bar);
-    wb += 2 * split;
-  };
-  auto load_x = [&](int j) {
-    uint64_t* bar = &S.landed[warp][j];
-    if (lane == 0) {
-      uint8_t* dst = ring + j * kDnSlot + 2 * kBox16;
-      tc::mbar_expect_tx(bar, 2 * kBox8);
-      tc::tma_load_2d(dst, mx, bar, xb * kF8Block, xrow);
-      tc::tma_load_2d(dst + kBox8, mx, bar, (xb + 1) * kF8Block, xrow);
-    }
-    if (lane < 16) copy4(&S.scale[warp][j][lane], psx + min(xb + (lane >> 3), last_x), bar);
-    xb += 2 * split;
+  auto step = [&](Walk& k) {  // one pair on; true if the chunk's part ends
+    k.kb += 2 * split;
+    if (--k.left) return false;
+    k.idx += WARPS;
+    return true;
   };
   Walk now{warp, 0, 0, 0};
   settle(now);
-  Walk ahead = now;
-  open_w(ahead);
-  for (int j = 0; j < AHEAD && ahead.left; ++j) {
-    load_w(j);
-    if (--ahead.left == 0) {
-      ahead.idx += WARPS;
-      settle(ahead);
-      open_w(ahead);
-    }
-  }
-  pdl_wait();
-  pdl_trigger();
-  ahead = now;
-  open_x(ahead);
-  for (int j = 0; j < AHEAD && ahead.left; ++j) {
-    load_x(j);
-    if (--ahead.left == 0) {
-      ahead.idx += WARPS;
-      settle(ahead);
-      open_x(ahead);
-    }
-  }
-  for (int p = tid; p < rows_all; p += WARPS * 32)
-    rowscale[p] = p < P ? a.alpha[L.sorted[p]] : a.s_shared[p - P];
-  __syncthreads();
-
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  const uint32_t get = get_at(g, t);
+  // The loads' walks, ahead of the arithmetic's: weights from the start, the
+  // activations once the gate/up kernel has ended. One loop fills slots and
+  // works them off, every piece of its code once.
+  Walk aw = now, ax = now;
+  uint8_t* ring = S.ring[warp][0];
   const uint32_t ring32 = tc::smem_u32(ring), sc32 = tc::smem_u32(S.scale[warp]);
+  const uint32_t get = get_at(g, t);
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
   uint32_t ph = 0;
-  int j = 0;
-  while (now.left) {
+  int j = 0, jw = 0, jx = 0, filled_w = 0, filled_x = 0;
+  bool waited = false, new_w = true, new_x = true, shared_w = false, shared_x = false;
+  const CUtensorMap *mw = &tmW, *mx = &tmX;
+  const float *psw = a.Sd, *psx = a.Hs;  // lanes 16, 17: the weights'; lanes 0-15: the rows'
+  int row_w = 0, row_x = 0;
+  while (true) {
+    if (filled_w < AHEAD && aw.left) {
+      if (new_w) {
+        const int e = L.expert[aw.c];
+        shared_w = e == a.E;
+        mw = shared_w ? &tmSW : &tmW;
+        row_w = (shared_w ? 0 : e * a.d) + col0;
+        psw = (shared_w ? a.Ssd : a.Sd) +
+              ((shared_w ? 0 : (size_t)e * NB) + col0 / kF8Block) * (shared_w ? KBs : KBr);
+      }
+      uint64_t* bar = &S.landed[warp][jw];
+      if (lane == 0) {
+        uint8_t* dst = ring + jw * kDnSlot;
+        tc::mbar_expect_tx(bar, 2 * kBox16);
+        tc::tma_load_2d(dst, mw, bar, aw.kb * kF8Block, row_w);
+        tc::tma_load_2d(dst + kBox16, mw, bar, (aw.kb + 1) * kF8Block, row_w);  // (zeros past the last)
+      }
+      __syncwarp();
+      if (lane >= 16 && lane < 18)
+        copy4(&S.scale[warp][jw][lane], psw + min(aw.kb + (lane & 1), (shared_w ? KBs : KBr) - 1), bar);
+      new_w = step(aw);
+      if (new_w) settle(aw);
+      if (++jw == AHEAD) jw = 0;
+      if (++filled_w < AHEAD && !waited) continue;
+    }
+    if (!waited) {
+      waited = true;
+      pdl_wait();
+      pdl_trigger();
+    }
+    if (filled_x < AHEAD && ax.left) {
+      if (new_x) {
+        shared_x = ax.c >= L.n_routed;
+        mx = shared_x ? &tmSX : &tmX;
+        row_x = (shared_x ? P : 0) + L.start[ax.c];
+        psx = a.Hs + (size_t)(row_x + min(lane & 7, L.count[ax.c] - 1)) * a.hblocks;
+      }
+      uint64_t* bar = &S.landed[warp][jx];
+      if (lane == 0) {
+        uint8_t* dst = ring + jx * kDnSlot + 2 * kBox16;
+        tc::mbar_expect_tx(bar, 2 * kBox8);
+        tc::tma_load_2d(dst, mx, bar, ax.kb * kF8Block, row_x);
+        tc::tma_load_2d(dst + kBox8, mx, bar, (ax.kb + 1) * kF8Block, row_x);
+      }
+      __syncwarp();
+      if (lane < 16)
+        copy4(&S.scale[warp][jx][lane], psx + min(ax.kb + (lane >> 3), (shared_x ? KBs : KBr) - 1), bar);
+      new_x = step(ax);
+      if (new_x) settle(ax);
+      if (++jx == AHEAD) jx = 0;
+      if (++filled_x < filled_w) continue;
+    }
+    if (now.left == 0) break;
     if (!f8_warp_wait(&S.landed[warp][j], ph, a.ctrl, kSiteFewFp8)) break;
     const uint32_t slot = ring32 + j * kDnSlot, sc = sc32 + 80 * j;
     // the last pair's second block may not exist; the activations' rows may be
@@ -669,51 +678,49 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS)
     }
     reads_before_refill();
     __syncwarp();
-    if (ahead.left) {
-      load_w(j);
-      load_x(j);
-      if (--ahead.left == 0) {
-        ahead.idx += WARPS;
-        settle(ahead);
-        open_w(ahead);
-        open_x(ahead);
-      }
-    }
+    --filled_w;
+    --filled_x;
     if (++j == AHEAD) {
       j = 0;
       ph ^= 1u;
     }
-    now.kb += 2 * split;
-    if (--now.left) continue;
-    // the walk's sums, weighted
-    const int cnt = L.count[now.c], s = now.idx - now.c * split;
-    const int row0 = (now.c >= L.n_routed ? P : 0) + L.start[now.c];
+    const int c = now.c, s = now.idx & (split - 1);
+    if (!step(now)) continue;
+    // the part's sums; their weights are applied when the slots are added
+    const int cnt = L.count[c], row0 = (c >= L.n_routed ? P : 0) + L.start[c];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       if (2 * t + q < cnt) {
-        const int row = row0 + 2 * t + q;
-        const float al = rowscale[row];
-        float* y = ysum + ((size_t)s * rows_all + row) * kDnPitch;
-        y[g] = al * acc[q];
-        y[g + 8] = al * acc[2 + q];
+        float* y = ysum + ((size_t)s * rows_all + row0 + 2 * t + q) * kDnPitch;
+        y[g] = acc[q];
+        y[g + 8] = acc[2 + q];
       }
     }
     acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-    now.idx += WARPS;
     settle(now);
   }
   __syncthreads();
+  const int parts_r = min(split, PRr), parts_s = min(split, PRs);
   for (int i = tid; i < a.T * kDnCols; i += WARPS * 32) {
     const int tok = i / kDnCols, c = i - tok * kDnCols;
-    float y = 0.f;
-    for (int sl = 0; sl < a.k; ++sl) {
-      const int p = L.pos[tok * a.k + sl];
-      for (int s = 0; s < min(split, PRr); ++s) y += ysum[((size_t)s * rows_all + p) * kDnPitch + c];
-    }
-    for (int s = 0; s < min(split, PRs); ++s)
-      y += ysum[((size_t)s * rows_all + P + tok) * kDnPitch + c];
     const size_t o = (size_t)tok * a.d + col0 + c;
-    if (a.r_attn) y += a.r_attn[o];
+    const float res = a.r_attn ? a.r_attn[o] : 0.f;
+    const int plane = rows_all * kDnPitch;
+    float y = 0.f;
+#pragma unroll 4
+    for (int sl = 0; sl < a.k; ++sl) {
+      const float* p = ysum + L.pos[tok * a.k + sl] * kDnPitch + c;
+      float v = p[0];
+      for (int s = 1; s < parts_r; ++s) v += p[s * plane];
+      y = fmaf(a.alpha[tok * a.k + sl], v, y);
+    }
+    if (parts_s) {
+      const float* p = ysum + (P + tok) * kDnPitch + c;
+      float v = p[0];
+      for (int s = 1; s < parts_s; ++s) v += p[s * plane];
+      y = fmaf(a.s_shared[tok], v, y);
+    }
+    y += res;
     if (a.out_bf16)
       static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(y);
     else
@@ -878,13 +885,13 @@ cudaError_t launch_gateup(const F8FewMaps& m, const F8ExpertsArgs& a, cudaStream
                     m.su, a);
 }
 
-// Rows of partial sums: all pairs and shared tokens once, or fewer of them
-// split up to WARPS ways (split x chunks stays below 2 WARPS, of 8 rows).
+// Rows of partial sums: all pairs and shared tokens once, or as many splits of
+// them as 16 WARPS rows hold.
 template <int WARPS, int AHEAD>
 cudaError_t launch_down(const F8FewMaps& m, const F8ExpertsArgs& a, cudaStream_t st) {
   static int attr[64] = {};
   const int rows = a.T * a.k + a.T;
-  const size_t smem = 1024 + sizeof(DnShared<WARPS, AHEAD>) + (size_t)rows * 4 +
+  const size_t smem = 1024 + sizeof(DnShared<WARPS, AHEAD>) +
                       (size_t)(rows > 16 * WARPS ? rows : 16 * WARPS) * kDnPitch * 4;
   cudaError_t e = ensure_smem_limit(f8_few_down_kernel<WARPS, AHEAD>, (int)smem, attr);
   if (e != cudaSuccess) return e;
@@ -917,7 +924,7 @@ cudaError_t launch_f8_few_gateup(const F8FewMaps& m, const F8ExpertsArgs& a, cud
 }
 
 cudaError_t launch_f8_few_down(const F8FewMaps& m, const F8ExpertsArgs& a, cudaStream_t st) {
-  return a.d / kDnCols <= tc_sm_count() ? launch_down<8, 3>(m, a, st) : launch_down<4, 3>(m, a, st);
+  return a.d / kDnCols <= tc_sm_count() ? launch_down<16, 2>(m, a, st) : launch_down<6, 2>(m, a, st);
 }
 
 cudaError_t launch_f8_few_matmul(const F8MatmulArgs& a, cudaStream_t st) {

@@ -61,7 +61,11 @@ __global__ void __launch_bounds__(256) combine_bf16_kernel(CombineArgs a) {
 
 // The same sum for the 8-bit layer: bf16 rows, the shared expert's after the
 // routed pairs', the residual optional, fp32 or bf16 out. One thread per 8
-// columns (16-byte loads), fp32 sums in the same fixed order.
+// columns (16-byte loads), fp32 sums in the same fixed order (eight slots'
+// loads in flight per thread cost occupancy: a prefill of 4096 tokens 308 ->
+// 317 us). The slots' rows are bf16 because writing and reading them in fp32
+// would add 270 MB to that prefill; their rounding and the one of a bf16 result
+// are of the same size.
 __device__ __forceinline__ void add_bf16x8(float (&acc)[8], const __nv_bfloat16* p) {
   float v[8];
   Chunk<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(p), v);

@@ -436,17 +436,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
+        uint32_t v[2][16];
+        auto col = [&](int c) {
+          return tq + (uint32_t)(acc * BN + (MODE == kF8GateUp ? (c >> 1) * 128 + part * 32 + (c & 1) * 16
+                                                               : part * kPartCols + c * 16));
+        };
+        tmem_ld16(col(0), v[0]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          // gate/up: 32 gate columns and the same 32 of up
-          const int col = MODE == kF8GateUp ? (c >> 1) * 128 + part * 32 + (c & 1) * 16
-                                            : part * kPartCols + c * 16;
-          uint32_t v[16];
-          tmem_ld16(tq + (uint32_t)(acc * BN + col), v);
           tmem_ld_wait();
+          if (c < 3) tmem_ld16(col(c + 1), v[(c + 1) & 1]);
           const float s = c >= 2 ? c1 : c0;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) sum[c * 16 + j] = fmaf(__uint_as_float(v[j]), s, sum[c * 16 + j]);
+          for (int j = 0; j < 16; ++j)
+            sum[c * 16 + j] = fmaf(__uint_as_float(v[c & 1][j]), s, sum[c * 16 + j]);
         }
         tc_fence_before();
         __syncwarp();

@@ -191,16 +191,14 @@ def _stream(stream):
         return ctypes.c_void_p(stream.cuda_stream)
     if _raw_stream is None:
         import torch
+        torch.cuda.init()
         # the handle alone, where this torch gives it: making a Stream object of
         # it costs 3 us, a call of the smallest kernels 3 us in all
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         if raw is None:
-            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
         else:
-            device = torch._C._cuda_getDevice if torch.cuda.is_initialized() else None
-            if device is None:
-                return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-            _raw_stream = lambda: raw(device())
+            _raw_stream = lambda: raw(torch.cuda.current_device())  # noqa: E731
     return ctypes.c_void_p(_raw_stream())
 
 

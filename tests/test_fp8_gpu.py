@@ -470,3 +470,22 @@ def test_a_wait_that_runs_out_is_reported(kernel):
     call()
     assert status()[0] == 0
     assert torch.equal(out, want)
+
+
+def test_example_runs_the_operators_together():
+    """examples/fp8_layer.py on a small shape: quantised layer and projection.
+    The projection's input and weights each round by at most 2^-4 of a value,
+    2^-4 / sqrt(3) in the mean at worst, independently; bf16 out 2^-8 more."""
+    import importlib.util
+    import os
+
+    import moe_inputs as mi
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    spec = importlib.util.spec_from_file_location("fp8_layer", os.path.join(root, "examples", "fp8_layer.py"))
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    for tokens in (3, 40):
+        off, off_y, us = ex.run(mi.DEEPSEEK_GROUP.with_(n_experts=16, d_model=1024), tokens, steps=2)
+        # five roundings to e4m3 (x, gate and up as one, h, down, and the shared expert's in parallel)
+        assert off < 3 * 2.0 ** -4 / math.sqrt(3)
+        assert off_y < 2.0 ** -4 / math.sqrt(3) * math.sqrt(2) + 2.0 ** -8 and us > 0

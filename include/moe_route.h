@@ -382,9 +382,12 @@ MOE_API moe_status_t moe_fp8_workspace_init(const moe_cfg_t* cfg, void* stream);
  * per 1 x 128 as moe_fp8_quantize does, and so is h = SiLU(gate) * up (from
  * f32) before the down product. The shared expert's matrices are banks of one
  * expert. r_attn may be NULL (no residual); out [T][d] is out_dtype (F32 or
- * BF16) and may alias r_attn when it is F32. Up to 16 tokens take two kernels
- * (gate/up; down + combine; MOE_PATH_GEMV asks for them), more take grouped
- * products on tcgen05 (MOE_PATH_TC); MOE_PATH_FUSED is MOE_ERR_UNSUPPORTED. */
+ * BF16) and may alias r_attn when it is F32. MOE_PATH_AUTO takes two kernels
+ * (gate/up; down + combine) for up to 16 tokens, MOE_PATH_GEMV asks for them;
+ * more tokens, and 16 or fewer where wide experts (d_model * d_ff of 4 Mi or
+ * more) average three pairs each, take grouped products on tcgen05
+ * (MOE_PATH_TC); MOE_PATH_FUSED is MOE_ERR_UNSUPPORTED. Ids outside [0, E) are
+ * reported as by moe_experts_forward. Deterministic. */
 MOE_API moe_status_t moe_fp8_experts_forward(
     const void* x, const float* r_attn, const int32_t* topk_ids, const float* weights,
     const float* s_shared, moe_bank_t W_gate, moe_bank_t W_up, moe_bank_t W_down,

@@ -7,11 +7,19 @@
 // in which order k is visited as long as both operands agree, so a lane's
 // fragment registers are simply 16-byte pieces of the rows: no conversion, no
 // shuffles. Every warp owns a ring of slots that its lane 0 fills by TMA
-// (128-byte swizzle). What such a stream can lose to is instruction issue: an
-// SM has some 350 issue slots for every 2 KB that HBM brings it. So a slot holds
-// two blocks of k, and a gate/up item two m16 tiles (with single blocks and
-// tiles, whether loaded into registers, by cp.async or by TMA, 280 instructions
-// per 2 KB kept 8 tokens of the 256-expert shape at 3 TB/s).
+// (128-byte swizzle). Such a stream loses to the latencies of a warp's walk
+// through a slot and to instruction issue before it loses to HBM (an SM has
+// some 350 issue slots for every 2 KB that HBM brings it). So a slot holds two
+// blocks of k, a gate/up item two m16 tiles, and the loops exist once, compact:
+// at one token a kernel fetches each of its instructions for a use or two.
+// (Single blocks and tiles, whether loaded into registers, by cp.async or by
+// TMA, took 280 instructions per 2 KB, 3 TB/s at 8 tokens of the 256-expert
+// shape.)
+//
+// Measured, weights rotated beyond L2: 256 experts, one token 15.3 us (28 MB;
+// latency of two dependent kernels, 5 us of them before the first weight
+// lands), 8 tokens 48.4 us (3.8 TB/s), 16 tokens 78.6 us; 8 wide experts, 4 tokens
+// 182 us (5.3 TB/s); products 1 x 5632 x 2048 5.5 us, 8 x 4096 x 14336 16.6 us.
 //
 // The products of one 128-wide block are summed by the tensor core and then
 // scaled by the block's two scales into fp32 sums held in registers.
@@ -20,10 +28,10 @@
 //  1. f8_few_gateup: every CTA groups the (token, slot) pairs by expert into
 //     chunks of at most 8 (ranking by counting), quantises the tokens into
 //     shared memory, then takes items of 16 gate and 16 up rows of a chunk's
-//     expert (eight and eight make an m16 tile, so a lane holds a row's gate and up sums). The
-//     warps split k; their sums meet in shared memory and are added in warp
-//     order. h needs one scale per 128 columns, which 16 items share: the item
-//     that finishes a block last (a counter that it also resets) quantises it.
+//     expert (eight and eight make an m16 tile, so that a lane holds a row's
+//     gate and up sums). The warps split k; their sums are added in warp order.
+//     h needs one scale per 128 columns, which 8 items share: the item that
+//     finishes a block last (a counter that it also resets) quantises it.
 //  2. f8_few_down: a CTA owns 16 output columns of every chunk and adds the
 //     slots, the shared expert and the residual in a fixed order.
 #include "fp8_common.cuh"

@@ -11,7 +11,9 @@
 //    own rows for the shared expert): the row is read and quantised once and
 //    its codes are written k (+ 1) times.
 //
-// All are bound by HBM: bytes in plus one byte per value out.
+// All are bound by HBM: bytes in plus one byte per value out. Measured:
+// 14336 x 4096 bf16 in 128 x 128 blocks 28.0 us (6.3 TB/s), 4097 x 4096 fp32 rows
+// 14.9 us (5.7 TB/s), 8 x 2048 1.9 us (launch).
 #include "fp8_common.cuh"
 #include "kernels.h"
 

@@ -3,12 +3,20 @@
 // that block), A with a scale per 1 x 128 and B with one per 128 x 128.
 //
 // One persistent CTA per SM. TMA brings 128 x 128 A and 256 x 128 B codes per
-// step (128-byte swizzle, 4 stages of 48 KB); one thread issues the four
+// step (128-byte swizzle, 4 stages of 48 KB); a thread issues the four
 // tcgen05.mma (e4m3, fp32, K = 32) of a step into one of two 256-column TMEM
 // buffers. The scales change with every block of 128 k, so a buffer holds one
 // step's products only: sixteen epilogue warps read it back, multiply by the two
 // scales and add into fp32 sums that stay in their registers (64 a thread),
 // while the tensor core fills the other buffer.
+//
+// What bounds it where HBM does not: the step. Its MMAs take 512 cycles, a
+// step about 1,000: the read-back, the sums and the hand-overs between issuer
+// and epilogue (issue slots 68 % busy, the tensor pipe 36-50 %). 8192 x 14336 x 4096
+// 480-500 us (1.9-2.0 PFLOP/s), grouped gate/up of 8 wide experts at
+// 2048 tokens 1.7 PFLOP/s; decode batches stream weights at 5.7 TB/s (gate/up,
+// 64 tokens of the 256-expert shape). Tried and slower: two column halves with
+// an issuer and two 128-column buffers each (504 us).
 //
 // Three uses:
 //  * gate/up: B = 128 gate and 128 up rows; the epilogue applies SwiGLU and
@@ -43,9 +51,10 @@ constexpr int kParts = kEpiWarps / 4;     // column parts of a tile, one per war
 constexpr int kPartCols = BN / kParts;    // 64
 // Warp 0 is the producer, warps 1 and 2 issue the MMAs, warp 3 brings the
 // scales, warps 4-19 are the epilogue: four a scheduler, so that one warp's
-// wait for TMEM is covered by the others' arithmetic. Launched with 96
+// wait for TMEM is covered by the others' arithmetic (eight warps: 959 us where
+// sixteen took 668 on the 8192 x 14336 x 4096 product). Launched with 96
 // registers a thread (61,440 in all); the first warpgroup hands some to the
-// epilogue, which holds 64 fp32 sums and 16 values in flight a thread:
+// epilogue, which holds 64 fp32 sums and 32 values in flight a thread:
 // 128 x 64 + 512 x 104 = 61,440.
 constexpr int kEpiWarp0 = 4;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
@@ -273,13 +282,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int total = n_rb * a.n_tiles * (MODE == kF8Dense ? a.ksplit : 1);
   const int KB = (a.K + BK - 1) / BK;
 
-  // Every role loop is run by its whole warp, so that each warp reaches the
-  // closing CTA barrier converged.
   if (warp < kEpiWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     // The producer's and the issuer's loops are lane 0's alone: an issue waits
-    // for room in the tensor core's short queue, and every cycle between two
-    // issues leaves it idle (votes and shuffles there cost 400 a step).
+    // for room in the tensor core's short queue, and cycles between two issues
+    // leave it idle.
     if (warp == 0) {
       // -------------------------------------------------------------- producer
       if (lane == 0) {

@@ -482,7 +482,7 @@ def fp8_matmul(a, a_scale, b, b_scale, out, workspace, stream=None):
     _scales_ok(a_scale, (M, kb), "a_scale")
     _scales_ok(b_scale, (-(-N // 128), kb), "b_scale")
     m = _Fp8Matmul(M, N, K, _dtype_of(out), _ld(a, (M, K), "a"), _ld(b, (N, K), "b"),
-                   _ld(out, (M, N), "out"), workspace.data_ptr(),
+                   _ld(out, (M, N), "out"), _ptr(workspace),
                    workspace.numel() * workspace.element_size())
     _check(lib().moe_fp8_matmul(a.data_ptr(), _ptr(a_scale), b.data_ptr(), _ptr(b_scale),
                                 ctypes.byref(m), out.data_ptr(), _stream(stream)), "moe_fp8_matmul")
@@ -547,11 +547,34 @@ def _banks8(cfg, W_gate, W_up, W_down, Ws_gate, Ws_up, Ws_down):
             sh(Ws_gate, (1, Is, d)), sh(Ws_up, (1, Is, d)), sh(Ws_down, (1, d, Is)))
 
 
+_layer_types = None
+
+
+def _check_layer(cfg, x, topk_ids, weights, out, s_shared, r_attn):
+    """Types and shapes of the 8-bit layer's tensors."""
+    global _layer_types
+    if _layer_types is None:
+        import torch
+        _layer_types = torch.bfloat16, torch.int32, torch.float32
+    bf16, i32, f32 = _layer_types
+    xs, ks = (cfg.T, cfg.d_model), (cfg.T, cfg.top_k)
+    if x.dtype != bf16 or x.shape != xs or out.shape != xs:
+        raise ValueError("x must be bfloat16 [%d, %d], and out as large" % xs)
+    if topk_ids.dtype != i32 or topk_ids.shape != ks or weights.dtype != f32 or weights.shape != ks:
+        raise ValueError("topk_ids must be int32 and weights float32 [%d, %d]" % ks)
+    if r_attn is not None and (r_attn.dtype != f32 or r_attn.shape != xs):
+        raise ValueError("r_attn must be float32 [%d, %d]" % xs)
+    if s_shared is not None and (s_shared.dtype != f32 or s_shared.numel() != cfg.T):
+        raise ValueError("s_shared must be float32 [%d]" % cfg.T)
+
+
 def fp8_experts_forward(cfg, workspace, x, topk_ids, weights, W_gate, W_up, W_down, out,
                         s_shared=None, r_attn=None, Ws_gate=None, Ws_up=None, Ws_down=None,
                         w_shared=None, stream=None):
     """moe_fp8_experts_forward: banks are (codes, scales) pairs; out float32 or
     bfloat16 [T, d_model]; r_attn optional."""
+    _check_layer(cfg, x, topk_ids, weights, out, s_shared, r_attn)
+    _ptr(workspace)
     b = _banks8(cfg, W_gate, W_up, W_down, Ws_gate, Ws_up, Ws_down)
     _check(lib().moe_fp8_experts_forward(
         _ptr(x), _ptr(r_attn), _ptr(topk_ids), _ptr(weights), _ptr(s_shared), *b, _ptr(w_shared),
@@ -563,6 +586,8 @@ def fp8_layer_forward(cfg, workspace, x, W_router, W_gate, W_up, W_down, out, to
                       r_attn=None, expert_bias=None, Ws_gate=None, Ws_up=None, Ws_down=None,
                       w_shared=None, stream=None):
     """moe_fp8_layer_forward: the whole layer with 8-bit banks."""
+    _check_layer(cfg, x, topk_ids, weights, out, None, r_attn)
+    _ptr(workspace)
     b = _banks8(cfg, W_gate, W_up, W_down, Ws_gate, Ws_up, Ws_down)
     _check(lib().moe_fp8_layer_forward(
         _ptr(x), _ptr(r_attn), _ptr(W_router), _ptr(expert_bias), *b, _ptr(w_shared),
@@ -582,6 +607,10 @@ class Fp8Experts:
         import torch
         self.cfg = cfg
         self.w = weights
+        for name, shape in (("W_router", (cfg.n_experts, cfg.d_model)), ("w_shared", (cfg.d_model,))):
+            t = weights.get(name)
+            if t is not None and (t.dtype != torch.bfloat16 or t.shape != shape):
+                raise ValueError("%s must be bfloat16 %s" % (name, shape))
         self.device = device or torch.device("cuda", torch.cuda.current_device())
         self.ws = fp8_alloc_workspace(cfg, self.device)
         self._banks = _banks8(cfg, weights["W_gate"], weights["W_up"], weights["W_down"],
@@ -605,16 +634,11 @@ class Fp8Experts:
             w[name] = (codes, scales)
         return Fp8Experts(cfg, w, device)
 
-    def _rows(self, x, out, r_attn):
-        if x.shape != self._x_shape or out.shape != self._x_shape or \
-                (r_attn is not None and r_attn.shape != self._x_shape):
-            raise ValueError("x, out and r_attn must be [%d, %d]" % self._x_shape)
-
     def forward(self, x, topk_ids, weights, s_shared=None, r_attn=None, out=None, stream=None):
         import torch
         if out is None:
             out = torch.empty(self._x_shape, dtype=torch.bfloat16, device=self.device)
-        self._rows(x, out, r_attn)
+        _check_layer(self.cfg, x, topk_ids, weights, out, s_shared, r_attn)
         _check(lib().moe_fp8_experts_forward(
             _ptr(x), _ptr(r_attn), _ptr(topk_ids), _ptr(weights), _ptr(s_shared), *self._banks,
             self._w_shared, self._cp, _ptr(out), _dtype_of(out), _stream(stream)),
@@ -625,7 +649,7 @@ class Fp8Experts:
         import torch
         if out is None:
             out = torch.empty(self._x_shape, dtype=torch.bfloat16, device=self.device)
-        self._rows(x, out, r_attn)
+        _check_layer(self.cfg, x, topk_ids, weights, out, None, r_attn)
         _check(lib().moe_fp8_layer_forward(
             _ptr(x), _ptr(r_attn), _ptr(self.w["W_router"]), _ptr(self.w.get("expert_bias")),
             *self._banks, self._w_shared, self._cp, _ptr(out), _dtype_of(out),

@@ -181,6 +181,25 @@ def test_binding_refuses_wrong_tensors(L):
     assert codes.shape == (3, 10, 100) and codes.stride(1) == 112 and scales.shape == (3, 1, 1)
 
 
+def test_binding_refuses_wrong_layer_tensors(L):
+    """Types and shapes of x, ids, weights, out, gate and residual."""
+    c = cfg(T=4)
+    good = dict(x=torch.zeros(4, 256, dtype=torch.bfloat16), topk_ids=torch.zeros(4, 4, dtype=torch.int32),
+                weights=torch.zeros(4, 4), out=torch.zeros(4, 256), s_shared=torch.zeros(4),
+                r_attn=torch.zeros(4, 256))
+    smr._check_layer(c, **good)
+    for name, bad in (("x", good["x"].float()), ("x", good["x"][:3]), ("topk_ids", good["topk_ids"].long()),
+                      ("topk_ids", good["topk_ids"][:, :3]), ("weights", good["weights"].double()),
+                      ("weights", good["weights"][:2]), ("out", good["out"][:, :128]),
+                      ("s_shared", torch.zeros(3)), ("s_shared", torch.zeros(4).half()),
+                      ("r_attn", good["r_attn"].bfloat16()), ("r_attn", good["r_attn"][:1])):
+        with pytest.raises(ValueError):
+            smr._check_layer(c, **dict(good, **{name: bad}))
+    with pytest.raises(ValueError):  # the workspace on the host
+        smr.fp8_experts_forward(c, torch.zeros(8, dtype=torch.uint8), good["x"], good["topk_ids"], good["weights"],
+                                None, None, None, good["out"])
+
+
 @pytest.mark.parametrize("kid", [16, 17, 18])
 def test_failure_self_test_takes_the_new_kernels(L, kid):
     assert L.moe_inject_stall(kid, 100) == 0

@@ -452,6 +452,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           tmem_ld_wait();
+          // The read's registers hold their values from here on: the compiler
+          // sees this as their definition and moves no use above the wait.
+#pragma unroll
+          for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(v[c & 1][j]));
           if (c < 3) tmem_ld16(col(c + 1), v[(c + 1) & 1]);
           const float s = c >= 2 ? c1 : c0;
 #pragma unroll

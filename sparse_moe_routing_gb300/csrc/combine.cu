@@ -59,51 +59,39 @@ __global__ void __launch_bounds__(256) combine_bf16_kernel(CombineArgs a) {
   reinterpret_cast<float4*>(a.out + (size_t)t * a.d)[c] = o;
 }
 
-// The same sum for the 8-bit layer: bf16 rows, the shared expert's after the
-// routed pairs', the residual optional, fp32 or bf16 out. One thread per 8
-// columns (16-byte loads), fp32 sums in the same fixed order (eight slots'
-// loads in flight per thread cost occupancy: a prefill of 4096 tokens 308 ->
-// 317 us). The slots' rows are bf16 because writing and reading them in fp32
-// would add 270 MB to that prefill; their rounding and the one of a bf16 result
-// are of the same size.
-__device__ __forceinline__ void add_bf16x8(float (&acc)[8], const __nv_bfloat16* p) {
-  float v[8];
-  Chunk<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(p), v);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) acc[j] += v[j];
+// The same sum for the 8-bit layer: the shared expert's rows after the routed
+// pairs', the residual optional, fp32 or bf16 out. One thread per 4 columns,
+// fp32 rows and sums in the same fixed order. (bf16 rows are half the bytes, 308
+// us for 4096 tokens of the 256-expert shape where these take 359, but their
+// rounding reaches the result, also where it is fp32. Eight columns a thread:
+// 64 tokens 160 us instead of 153.)
+__device__ __forceinline__ void add_f32x4(float4& acc, const float* p) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
 }
 
 __global__ void __launch_bounds__(256) combine_rows_kernel(CombineRowsArgs a) {
   const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const int vecs = a.d / 8;
-  const int t = (int)(i / vecs), c = (int)(i - (long long)t * vecs) * 8;
+  const int vecs = a.d / 4;
+  const int t = (int)(i / vecs), c = (int)(i - (long long)t * vecs) * 4;
   pdl_wait();
   pdl_trigger();
   if (t >= a.T) return;
-  float acc[8] = {};
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s = 0; s < a.k; ++s)
-    add_bf16x8(acc, a.Y + (size_t)a.pos[(size_t)t * a.k + s] * a.d + c);
-  if (a.own_rows) add_bf16x8(acc, a.Y + ((size_t)a.T * a.k + t) * a.d + c);
+    add_f32x4(acc, a.Y + (size_t)a.pos[(size_t)t * a.k + s] * a.d + c);
+  if (a.own_rows) add_f32x4(acc, a.Y + ((size_t)a.T * a.k + t) * a.d + c);
   const size_t o = (size_t)t * a.d + c;
-  if (a.r_attn) {
-    const float4 r0 = *reinterpret_cast<const float4*>(a.r_attn + o);
-    const float4 r1 = *reinterpret_cast<const float4*>(a.r_attn + o + 4);
-    acc[0] += r0.x; acc[1] += r0.y; acc[2] += r0.z; acc[3] += r0.w;
-    acc[4] += r1.x; acc[5] += r1.y; acc[6] += r1.z; acc[7] += r1.w;
-  }
-  if (a.out_bf16) {
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + o) =
-        make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
-                   pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7]));
-  } else {
-    float4* out = reinterpret_cast<float4*>(static_cast<float*>(a.out) + o);
-    out[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    out[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-  }
+  if (a.r_attn) add_f32x4(acc, a.r_attn + o);
+  if (a.out_bf16)
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + o) =
+        make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+  else
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + o) = acc;
 }
 
 cudaError_t launch_combine_rows(const CombineRowsArgs& a, cudaStream_t st) {
-  const long long n = (long long)a.T * (a.d / 8);
+  const long long n = (long long)a.T * (a.d / 4);
   return launch_pdl(combine_rows_kernel, dim3((unsigned)((n + 255) / 256)), 256, 0, st, a);
 }
 

@@ -131,7 +131,7 @@ F8Plan f8_plan(const moe_cfg_t& c) {
   p.Hf = take(few ? (P + T) * ldh * 4 : 0);
   p.Hq = take((P + T) * ldh);
   p.Hs = take((P + T) * p.hblocks * 4);
-  p.Y = take((P + T) * d * 2);
+  p.Y = take((P + T) * d * 4);
   p.total = off;
   return p;
 }
@@ -255,7 +255,7 @@ moe_status_t enqueue_tc(const void* x, const float* r_attn, const int32_t* ids, 
   if (s != MOE_OK) return s;
   uint8_t* xq = at<uint8_t>(c, p.xq);
   uint8_t* Hq = at<uint8_t>(c, p.Hq);
-  __nv_bfloat16* Y = at<__nv_bfloat16>(c, p.Y);
+  float* Y = at<float>(c, p.Y);
   const F8PackArgs pk{static_cast<const __nv_bfloat16*>(x), at<int32_t>(c, p.r.pos), xq,
                       at<float>(c, p.xs), T, d, k, Is > 0 ? 1 : 0};
   cudaError_t e = run_kernel(MOE_KERNEL_F8_QUANT, st, [&] { return launch_f8_pack(pk, st); });

@@ -23,7 +23,7 @@
 //    quantises h: a thread holds 32 of a row's 128 columns, the others'
 //    maxima come through shared memory, and codes and scale go out in the
 //    form that the down product reads;
-//  * down: the routing weight (or the shared gate) applied, rows out in bf16;
+//  * down: the routing weight (or the shared gate) applied, rows out in fp32;
 //  * dense: one product, bf16 or fp32 out, k split over CTAs when there are
 //    few tiles (fp32 partial sums, which a second launch adds in split order).
 //
@@ -121,9 +121,9 @@ __device__ __forceinline__ uint4 four_floats(const float* v) {
   return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
                     __float_as_uint(v[3]));
 }
-__device__ __forceinline__ uint4 eight_bf16(const float* v, float s) {
-  return make_uint4(pack_bf16x2(s * v[0], s * v[1]), pack_bf16x2(s * v[2], s * v[3]),
-                    pack_bf16x2(s * v[4], s * v[5]), pack_bf16x2(s * v[6], s * v[7]));
+__device__ __forceinline__ uint4 eight_bf16(const float* v) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
 }
 // Stores the exchanged pieces: `at` the address of the lane's piece in the
 // warp's first row, rows `pitch` elements apart of which `rows` exist, `left`
@@ -518,19 +518,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int col = it.nt * BN + part * kPartCols;
         const int left = (MODE == kF8Dense && a.ksplit > 1 ? BN * a.n_tiles : a.n_cols) - col;
         uint4 c[8];
-        if (MODE == kF8Down || (a.ksplit == 1 && a.out_bf16)) {
+        if (MODE == kF8Dense && a.ksplit == 1 && a.out_bf16) {
           const int piece = 8 * (lane & 7);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) c[j] = eight_bf16(sum + 8 * j, MODE == kF8Down ? al : 1.f);
+          for (int j = 0; j < 8; ++j) c[j] = eight_bf16(sum + 8 * j);
           exchange8(c, lane);
-          store8(static_cast<__nv_bfloat16*>(a.out) + ((size_t)it.row0 + wrow) * a.ldo + col + piece, a.ldo, c,
-                 rows, left - piece, MODE == kF8Down || a.out_vec, lane);
+          store8(static_cast<__nv_bfloat16*>(a.out) + (size_t)wrow * a.ldo + col + piece, a.ldo, c, rows,
+                 left - piece, a.out_vec, lane);
         } else {
           // split k: fp32 rows of the tile, [split][tile][128 rows][256 columns]
-          const bool part_sum = a.ksplit > 1;
+          const bool part_sum = MODE == kF8Dense && a.ksplit > 1;
           float* out = part_sum ? a.partial + (((size_t)it.split * n_rb * a.n_tiles + it.tile) * BM + q * 32) * BN +
                                       part * kPartCols
-                                : static_cast<float*>(a.out) + (size_t)wrow * a.ldo + col;
+                                : static_cast<float*>(a.out) + ((size_t)it.row0 + wrow) * a.ldo + col;
+          if (MODE == kF8Down) {
+#pragma unroll
+            for (int j = 0; j < kPartCols; ++j) sum[j] *= al;
+          }
           const long long pitch = part_sum ? BN : a.ldo;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -538,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 8; ++j) c[j] = four_floats(sum + 32 * h + 4 * j);
             exchange8(c, lane);
-            store8(out + piece, pitch, c, rows, left - piece, part_sum || a.out_vec, lane);
+            store8(out + piece, pitch, c, rows, left - piece, MODE == kF8Down || part_sum || a.out_vec, lane);
           }
         }
       }

@@ -278,7 +278,7 @@ struct F8TcArgs {
   const float* a_scale;        // [rows of A][a_blocks]
   const float *b_scale0, *b_scale1;  // routed (gate, up | down) or dense B
   const float *b_scale2, *b_scale3;  // shared expert
-  void* out;                   // codes | bf16 rows | dense out
+  void* out;                   // codes | fp32 rows | dense out
   float* out_scale;            // gate/up: [rows][out_blocks]
   float* partial;              // dense, ksplit > 1: [ksplit][tiles][128][256]
   Ctrl* ctrl;
@@ -391,10 +391,10 @@ cudaError_t launch_gemv_small(const GemvArgs& a, int act, int wdt, bool down, cu
 // True when the GEMV kernels can stage at least one token of width d and kmax.
 bool gemv_supported(int d, int kmax);
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t st);
-// out[t] = [r_attn[t] +] the sum over slots of Y[pos[t*k+s]] [+ Y[T*k+t]], bf16 rows in.
+// out[t] = [r_attn[t] +] the sum over slots of Y[pos[t*k+s]] [+ Y[T*k+t]].
 struct CombineRowsArgs {
   const float* r_attn;       // [T][d] or null
-  const __nv_bfloat16* Y;    // [T*k + T][d]
+  const float* Y;            // [T*k + T][d]
   const int32_t* pos;        // [T*k]
   void* out;                 // [T][d] f32, or bf16 when out_bf16
   int T, d, k, own_rows, out_bf16;

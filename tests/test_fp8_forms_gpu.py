@@ -1,0 +1,125 @@
+"""The 8-bit operators on the GPU where their form or their state matters:
+precision of fp32 results, many slots, streams, workspaces, timeouts, large
+grids, the layer's own shapes and its other routing rule."""
+import gc
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+import torch  # noqa: E402
+
+import sparse_moe_routing_gb300 as smr  # noqa: E402
+from fp8_util import (F8, bank, blocks, experts_ref, pitched, quantize64, random_matrix,  # noqa: E402
+                      round_e4m3, values)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from sparse_moe_routing_gb300 import build
+    build.build()
+
+
+@pytest.fixture(autouse=True)
+def disarmed():
+    yield
+    smr.inject_stall(None, 0)
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+# (d, E, k, width, shared width)
+SHAPES = {"tiny": (256, 16, 4, 64, 64), "ragged": (272, 5, 2, 144, 80), "wide": (512, 8, 2, 896, 0),
+          "apart": (384, 12, 4, 128, 512), "slots": (256, 40, 32, 64, 64), "e256": (2048, 256, 8, 512, 512)}
+
+
+def config(shape, T, path=smr.PATH_AUTO, **kw):
+    d, E, k, width, shared = SHAPES[shape]
+    return smr.MoEConfig(**(dict(T=T, d_model=d, n_experts=E, top_k=k, d_ff=width, d_ff_shared=shared,
+                                 expert_dtype=smr.F8_E4M3_B128, path=path) | kw))
+
+
+# ---------------------------------------------------------------------------
+# a layer whose h has exact codes
+# ---------------------------------------------------------------------------
+def exact_bank(g, E, N, K, gate):
+    """Codes 64, 128 or 256 (gate), or 1 to 15 with either sign (up); scales 2^-3."""
+    if gate:
+        v = torch.exp2(torch.randint(6, 9, (E, N, K), generator=g, device="cuda").float())
+    else:
+        v = torch.randint(1, 16, (E, N, K), generator=g, device="cuda").float()
+        v = v * (1 - 2 * torch.randint(0, 2, (E, N, K), generator=g, device="cuda").float())
+    return v.to(F8), torch.full((E, blocks(N), blocks(K)), 2.0 ** -3, device="cuda")
+
+
+def make_exact(shape, T, k=None, seed=0):
+    """Inputs for which every code of h is beyond doubt. x has one value, 8, a
+    row: a gate sum is 64, 128 or 256, whose SiLU is itself to 1e-27, an up sum a
+    whole number of magnitude 1 to 15; their product has four significant bits and
+    so an e4m3 code of its own, which an error of some ulps does not change. What
+    is left to differ are the sums of down and over the slots."""
+    d, E, k0, width, shared = SHAPES[shape]
+    k = k or k0
+    g = gen(31 * T + seed)
+    x = torch.zeros(T, d, device="cuda")
+    x[torch.arange(T, device="cuda"), torch.randint(0, d, (T,), generator=g, device="cuda")] = 8.0
+    w = {"W_gate": exact_bank(g, E, width, d, True), "W_up": exact_bank(g, E, width, d, False),
+         "W_down": bank(g, E, d, width)}
+    gate = None
+    if shared:
+        w |= {"Ws_gate": exact_bank(g, 1, shared, d, True),
+              "Ws_up": exact_bank(g, 1, shared, d, False), "Ws_down": bank(g, 1, d, shared)}
+        gate = torch.sigmoid(torch.randn(T, generator=g, device="cuda"))
+    ids = torch.rand(T, E, generator=g, device="cuda").topk(k, dim=-1).indices.to(torch.int32)
+    alpha = torch.rand(T, k, generator=g, device="cuda") + 0.1
+    return x.to(torch.bfloat16), ids, alpha, w, gate
+
+
+def check_sums(out, x, ids, alpha, w, gate, r=None):
+    """Elementwise: the additions of a block of 128 products, of the blocks and of
+    the slots (a k split adds no more), each off by 2^-23 of the sum of magnitudes
+    at most, and five roundings of a term (two scales, the weight, the split's and
+    the residual's sum); a bf16 result is off by half a step, 2^-8, more."""
+    ref = experts_ref(x, ids, alpha, w, gate, r)
+    plain = {n: (c.float().abs().to(F8), s) for n, (c, s) in w.items()}
+    mag = experts_ref(x, ids, alpha, plain, gate, None if r is None else r.abs())
+    width = max(w["W_down"][0].shape[-1], w["Ws_down"][0].shape[-1] if "Ws_down" in w else 0)
+    n = min(width, 128) + blocks(width) + ids.shape[1] + 1 + 5
+    tol = n * 2.0 ** -23 * mag + 1e-30
+    if out.dtype == torch.bfloat16:
+        tol = tol + 2.0 ** -8 * (ref.abs() + tol)
+    err = (out.double() - ref).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+
+
+PRECISE = [("tiny", 1), ("tiny", 16), ("tiny", 17), ("tiny", 200), ("ragged", 5), ("ragged", 40), ("wide", 3),
+           ("wide", 64), ("wide", 300), ("apart", 10), ("apart", 33), ("apart", 260), ("e256", 1), ("e256", 8),
+           ("e256", 17), ("e256", 64)]
+
+
+@pytest.mark.parametrize("shape,T", PRECISE, ids=["%s-%d" % c for c in PRECISE])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_slot_rows_are_summed_in_fp32(shape, T, out_dtype):
+    """Nothing between h's codes and the result is rounded to fewer than 32 bits."""
+    x, ids, alpha, w, gate = make_exact(shape, T)
+    r = torch.randn(x.shape, generator=gen(T), device="cuda") if out_dtype == torch.float32 else None
+    layer = smr.Fp8Experts(config(shape, T), w)
+    out = torch.full(x.shape, 9.0, dtype=out_dtype, device="cuda")
+    layer.forward(x, ids, alpha, s_shared=gate, r_attn=r, out=out)
+    check_sums(out, x, ids, alpha, w, gate, r)
+
+
+@pytest.mark.parametrize("path", [smr.PATH_GEMV, smr.PATH_TC], ids=["few", "tc"])
+@pytest.mark.parametrize("T", [3, 16])
+def test_slot_rows_are_summed_in_fp32_on_either_path(path, T):
+    x, ids, alpha, w, gate = make_exact("tiny", T)
+    out = torch.empty(x.shape, device="cuda")
+    smr.Fp8Experts(config("tiny", T, path), w).forward(x, ids, alpha, s_shared=gate, out=out)
+    check_sums(out, x, ids, alpha, w, gate)

@@ -525,7 +525,8 @@ constexpr int kDnArrivals = 20;  // weights, activations, 18 scales
 
 // WARPS warps with AHEAD slots in flight each. Sixteen warps where every CTA
 // has an SM of its own (128 KB of weights in flight), six where there are more
-// CTAs than SMs, so that two fit. A warp's walk through a slot is a chain of
+// CTAs than SMs, so that two fit, and where the sums of many slots (more than 356
+// pairs and shared tokens) leave no room for sixteen warps' slots. A warp's walk through a slot is a chain of
 // latencies, so that warps count more than slots: eight warps of three slots
 // took 53.8 us where sixteen of two take 48.4 (8 tokens, 256-expert shape,
 // both kernels), four of three 198 where six of two take 182 (4 tokens, 8
@@ -896,11 +897,18 @@ cudaError_t launch_gateup(const F8FewMaps& m, const F8ExpertsArgs& a, cudaStream
 // Rows of partial sums: all pairs and shared tokens once, or as many splits of
 // them as 16 WARPS rows hold.
 template <int WARPS, int AHEAD>
+constexpr size_t down_smem(int T, int k) {
+  const int rows = T * k + T;
+  return 1024 + sizeof(DnShared<WARPS, AHEAD>) +
+         (size_t)(rows > 16 * WARPS ? rows : 16 * WARPS) * kDnPitch * 4;
+}
+// six warps take whatever f8_few_ok lets through
+static_assert(down_smem<6, 2>(kF8FewTokens, kFewMaxPairs / kF8FewTokens) <= kSmemLimit, "down's plan exceeds 227 KB");
+
+template <int WARPS, int AHEAD>
 cudaError_t launch_down(const F8FewMaps& m, const F8ExpertsArgs& a, cudaStream_t st) {
   static int attr[64] = {};
-  const int rows = a.T * a.k + a.T;
-  const size_t smem = 1024 + sizeof(DnShared<WARPS, AHEAD>) +
-                      (size_t)(rows > 16 * WARPS ? rows : 16 * WARPS) * kDnPitch * 4;
+  const size_t smem = down_smem<WARPS, AHEAD>(a.T, a.k);
   cudaError_t e = ensure_smem_limit(f8_few_down_kernel<WARPS, AHEAD>, (int)smem, attr);
   if (e != cudaSuccess) return e;
   return launch_pdl(f8_few_down_kernel<WARPS, AHEAD>, dim3(a.d / kDnCols), WARPS * 32, smem, st, m.w, m.sw,
@@ -932,7 +940,8 @@ cudaError_t launch_f8_few_gateup(const F8FewMaps& m, const F8ExpertsArgs& a, cud
 }
 
 cudaError_t launch_f8_few_down(const F8FewMaps& m, const F8ExpertsArgs& a, cudaStream_t st) {
-  return a.d / kDnCols <= tc_sm_count() ? launch_down<16, 2>(m, a, st) : launch_down<6, 2>(m, a, st);
+  const bool sixteen = a.d / kDnCols <= tc_sm_count() && down_smem<16, 2>(a.T, a.k) <= kSmemLimit;
+  return sixteen ? launch_down<16, 2>(m, a, st) : launch_down<6, 2>(m, a, st);
 }
 
 cudaError_t launch_f8_few_matmul(const F8MatmulArgs& a, cudaStream_t st) {

@@ -123,3 +123,19 @@ def test_slot_rows_are_summed_in_fp32_on_either_path(path, T):
     out = torch.empty(x.shape, device="cuda")
     smr.Fp8Experts(config("tiny", T, path), w).forward(x, ids, alpha, s_shared=gate, out=out)
     check_sums(out, x, ids, alpha, w, gate)
+
+
+# ---------------------------------------------------------------------------
+# many slots a token
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("T,k", [(16, 20), (16, 22), (16, 32), (15, 23), (11, 32), (10, 32), (1, 32), (17, 32)])
+def test_experts_with_many_slots(T, k):
+    """top_k up to 32 at every number of tokens."""
+    x, ids, alpha, w, gate = make_exact("slots", T, k)
+    out = torch.empty(x.shape, device="cuda")
+    for path in (smr.PATH_AUTO,) + ((smr.PATH_GEMV,) if T <= 16 else ()):
+        layer = smr.Fp8Experts(config("slots", T, path, top_k=k), w)
+        out.fill_(9.0)
+        layer.forward(x, ids, alpha, s_shared=gate, out=out)
+        check_sums(out, x, ids, alpha, w, gate)
+        assert layer.device_status()[0] == 0

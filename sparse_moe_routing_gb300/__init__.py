@@ -528,7 +528,8 @@ def fp8_alloc_workspace(cfg: MoEConfig, device=None, stream=None):
 
 
 def _bank8(b, shape):
-    """An 8-bit bank from (codes, scales); None stands for no shared expert."""
+    """An 8-bit bank from (codes, scales); None stands for no shared expert. A bank
+    of one matrix may come without its first dimension."""
     if b is None:
         return _Bank(None, None, None)
     codes, scales = b
@@ -536,7 +537,7 @@ def _bank8(b, shape):
     if tuple(codes.shape) not in (tuple(shape), tuple(shape)[1:] if shape[0] == 1 else None):
         raise ValueError("a bank's codes have shape %s, expected %s" % (tuple(codes.shape), tuple(shape)))
     want = (shape[0], -(-shape[1] // 128), -(-shape[2] // 128))
-    _scales_ok(scales, want if scales.dim() == 3 else want[1:], "a bank's scales")
+    _scales_ok(scales, want[1:] if shape[0] == 1 and scales.dim() == 2 else want, "a bank's scales")
     return _Bank(_ptr(codes), _ptr(scales), None)
 
 

@@ -569,12 +569,25 @@ def _check_layer(cfg, x, topk_ids, weights, out, s_shared, r_attn):
         raise ValueError("s_shared must be float32 [%d]" % cfg.T)
 
 
+def _check_routing(cfg, W_router, expert_bias, w_shared):
+    """Types and shapes of the 8-bit layer's routing tensors, where given."""
+    import torch
+    E, d = cfg.n_experts, cfg.d_model
+    if W_router is not None and (W_router.dtype != torch.bfloat16 or W_router.shape != (E, d)):
+        raise ValueError("W_router must be bfloat16 [%d, %d]" % (E, d))
+    if expert_bias is not None and (expert_bias.dtype != torch.float32 or expert_bias.numel() != E):
+        raise ValueError("expert_bias must be float32 [%d]" % E)
+    if w_shared is not None and (w_shared.dtype != torch.bfloat16 or w_shared.numel() != d):
+        raise ValueError("w_shared must be bfloat16 [%d]" % d)
+
+
 def fp8_experts_forward(cfg, workspace, x, topk_ids, weights, W_gate, W_up, W_down, out,
                         s_shared=None, r_attn=None, Ws_gate=None, Ws_up=None, Ws_down=None,
                         w_shared=None, stream=None):
     """moe_fp8_experts_forward: banks are (codes, scales) pairs; out float32 or
     bfloat16 [T, d_model]; r_attn optional."""
     _check_layer(cfg, x, topk_ids, weights, out, s_shared, r_attn)
+    _check_routing(cfg, None, None, w_shared)
     _ptr(workspace)
     b = _banks8(cfg, W_gate, W_up, W_down, Ws_gate, Ws_up, Ws_down)
     _check(lib().moe_fp8_experts_forward(
@@ -588,6 +601,7 @@ def fp8_layer_forward(cfg, workspace, x, W_router, W_gate, W_up, W_down, out, to
                       w_shared=None, stream=None):
     """moe_fp8_layer_forward: the whole layer with 8-bit banks."""
     _check_layer(cfg, x, topk_ids, weights, out, None, r_attn)
+    _check_routing(cfg, W_router, expert_bias, w_shared)
     _ptr(workspace)
     b = _banks8(cfg, W_gate, W_up, W_down, Ws_gate, Ws_up, Ws_down)
     _check(lib().moe_fp8_layer_forward(
@@ -608,10 +622,7 @@ class Fp8Experts:
         import torch
         self.cfg = cfg
         self.w = weights
-        for name, shape in (("W_router", (cfg.n_experts, cfg.d_model)), ("w_shared", (cfg.d_model,))):
-            t = weights.get(name)
-            if t is not None and (t.dtype != torch.bfloat16 or t.shape != shape):
-                raise ValueError("%s must be bfloat16 %s" % (name, shape))
+        _check_routing(cfg, weights.get("W_router"), weights.get("expert_bias"), weights.get("w_shared"))
         self.device = device or torch.device("cuda", torch.cuda.current_device())
         self.ws = fp8_alloc_workspace(cfg, self.device)
         self._banks = _banks8(cfg, weights["W_gate"], weights["W_up"], weights["W_down"],

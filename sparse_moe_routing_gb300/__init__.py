@@ -207,6 +207,20 @@ def _check(status: int, where: str):
         raise MoEError(status, where)
 
 
+def _empty(shape, dtype, device, stream):
+    """torch.empty for a call on `stream` (None: the current one): from that
+    stream's memory, so that a block handed out or given back early is used
+    again in its order only; not before what the current stream has in hand at
+    that time either."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device or "cuda")
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device or "cuda")
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def workspace_bytes(cfg: MoEConfig) -> int:
     n = lib().moe_workspace_bytes(ctypes.byref(cfg._c()))
     if n == 0:
@@ -215,10 +229,9 @@ def workspace_bytes(cfg: MoEConfig) -> int:
 
 
 def alloc_workspace(cfg: MoEConfig, device=None, stream=None):
-    """Allocates (with torch) and initialises a workspace for cfg."""
+    """Allocates (with torch) and initialises a workspace for cfg on `stream`."""
     import torch
-    n = workspace_bytes(cfg)
-    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    ws = _empty(workspace_bytes(cfg), torch.uint8, device, stream)
     _check(lib().moe_workspace_init(ctypes.byref(cfg._c(ws)), _stream(stream)),
            "moe_workspace_init")
     return ws
@@ -459,12 +472,12 @@ def _matmul_args(M, N, K, out_dtype=BF16, lda=0, ldb=0, ldo=0, workspace=None):
 
 def fp8_matmul_workspace(M, N, K, device=None, stream=None):
     """Allocates (with torch) and initialises the workspace of an M x N x K
-    product."""
+    product on `stream`."""
     import torch
     n = lib().moe_fp8_matmul_workspace_bytes(ctypes.byref(_matmul_args(M, N, K)))
     if n == 0:
         raise MoEError(1, "moe_fp8_matmul_workspace_bytes")
-    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    ws = _empty(n, torch.uint8, device, stream)
     _check(lib().moe_fp8_matmul_init(ctypes.byref(_matmul_args(M, N, K, workspace=ws)),
                                      _stream(stream)), "moe_fp8_matmul_init")
     return ws
@@ -519,9 +532,10 @@ def fp8_workspace_bytes(cfg: MoEConfig) -> int:
 
 
 def fp8_alloc_workspace(cfg: MoEConfig, device=None, stream=None):
-    """Allocates (with torch) and initialises a workspace of the 8-bit layer."""
+    """Allocates (with torch) and initialises a workspace of the 8-bit layer on
+    `stream`."""
     import torch
-    ws = torch.empty(fp8_workspace_bytes(cfg), dtype=torch.uint8, device=device or "cuda")
+    ws = _empty(fp8_workspace_bytes(cfg), torch.uint8, device, stream)
     _check(lib().moe_fp8_workspace_init(ctypes.byref(cfg._c(ws)), _stream(stream)),
            "moe_fp8_workspace_init")
     return ws
@@ -616,7 +630,12 @@ class Fp8Experts:
 
     weights: dict of (codes, scales) pairs W_gate, W_up, W_down and, with a
     shared expert, Ws_gate, Ws_up, Ws_down; for `layer` also W_router,
-    expert_bias and w_shared tensors. `from_bf16` quantises a bf16 layer's."""
+    expert_bias and w_shared tensors. `from_bf16` quantises a bf16 layer's.
+
+    Calls run on `stream` (None: the current one), after what is on it: a caller
+    who changes streams orders them, the object's making and its calls among
+    themselves (they share a workspace). A result that a call allocates (out not
+    given) belongs to the call's stream."""
 
     def __init__(self, cfg: MoEConfig, weights: dict, device=None):
         import torch
@@ -649,7 +668,7 @@ class Fp8Experts:
     def forward(self, x, topk_ids, weights, s_shared=None, r_attn=None, out=None, stream=None):
         import torch
         if out is None:
-            out = torch.empty(self._x_shape, dtype=torch.bfloat16, device=self.device)
+            out = _empty(self._x_shape, torch.bfloat16, self.device, stream)
         _check_layer(self.cfg, x, topk_ids, weights, out, s_shared, r_attn)
         _check(lib().moe_fp8_experts_forward(
             _ptr(x), _ptr(r_attn), _ptr(topk_ids), _ptr(weights), _ptr(s_shared), *self._banks,
@@ -660,7 +679,7 @@ class Fp8Experts:
     def layer(self, x, topk_ids, weights, r_attn=None, out=None, stream=None):
         import torch
         if out is None:
-            out = torch.empty(self._x_shape, dtype=torch.bfloat16, device=self.device)
+            out = _empty(self._x_shape, torch.bfloat16, self.device, stream)
         _check_layer(self.cfg, x, topk_ids, weights, out, None, r_attn)
         _check(lib().moe_fp8_layer_forward(
             _ptr(x), _ptr(r_attn), _ptr(self.w["W_router"]), _ptr(self.w.get("expert_bias")),

@@ -139,3 +139,29 @@ def test_experts_with_many_slots(T, k):
         layer.forward(x, ids, alpha, s_shared=gate, out=out)
         check_sums(out, x, ids, alpha, w, gate)
         assert layer.device_status()[0] == 0
+
+
+# ---------------------------------------------------------------------------
+# streams
+# ---------------------------------------------------------------------------
+def test_results_are_allocated_on_the_calls_stream():
+    """A result that the call allocates and the caller drops early is not handed
+    out on the current stream while the call's stream may still write it."""
+    T = 700
+    x, ids, alpha, w, gate = make_exact("tiny", T)
+    w["W_router"], w["w_shared"] = (torch.zeros(n, dtype=torch.bfloat16, device="cuda") for n in ((16, 256), 256))
+    layer = smr.Fp8Experts(config("tiny", T), w)
+    ids2, alpha2 = ids.clone(), alpha.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for call in (lambda: layer.forward(x, ids, alpha, s_shared=gate, stream=side),
+                 lambda: layer.layer(x, ids2, alpha2, stream=side),
+                 lambda: smr.fp8_matmul_workspace(64, 512, 8192, stream=side),
+                 lambda: smr.fp8_alloc_workspace(config("tiny", T), stream=side),
+                 lambda: smr.alloc_workspace(smr.MoEConfig(T=T, d_model=256, n_experts=16, top_k=4, d_ff=64),
+                                             stream=side)):
+        out = call()
+        at, size, dtype = out.data_ptr(), out.shape, out.dtype
+        del out
+        assert torch.empty(size, dtype=dtype, device="cuda").data_ptr() != at
+        torch.cuda.synchronize()

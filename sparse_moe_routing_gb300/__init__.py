@@ -503,24 +503,38 @@ def fp8_matmul(a, a_scale, b, b_scale, out, workspace, stream=None):
 
 class Fp8Linear:
     """y = x W^T with W [N, K] held in 8 bits and x quantised on the way:
-    fp8_quantize, then fp8_matmul, for up to max_rows rows."""
+    fp8_quantize, then fp8_matmul, for up to max_rows rows. The quantised x and
+    the workspace belong to the object: calls on several streams are ordered by
+    the caller."""
 
     def __init__(self, weight, max_rows, device=None):
+        if device is not None:
+            weight = weight.to(device)
         N, K = weight.shape
-        self.N, self.K = N, K
+        self.N, self.K, self.max_rows = N, K, max_rows
         self.codes, self.scales = fp8_empty(N, K, 128, device=weight.device)
         fp8_quantize(weight, self.codes, self.scales, block_rows=128)
         self.x, self.x_scales = fp8_empty(max_rows, K, 1, device=weight.device)
-        self._ws = {}
+        # One workspace for every number of rows. What a product needs depends on
+        # its row blocks only and does not grow with them alone (fewer tiles are
+        # split more), but past 152 of them k is not split.
+        size = lambda M: lib().moe_fp8_matmul_workspace_bytes(  # noqa: E731
+            ctypes.byref(_matmul_args(M, N, K)))
+        most = max((1, *range(128, min(max_rows, 152 * 128) + 1, 128), max_rows), key=size)
+        self.ws = fp8_matmul_workspace(most, N, K, weight.device)
 
     def __call__(self, x, out, stream=None):
         M = x.shape[0]
-        if M not in self._ws:
-            self._ws[M] = fp8_matmul_workspace(M, self.N, self.K, x.device, stream)
+        if M > self.max_rows:
+            raise ValueError("x has %d rows, made for %d" % (M, self.max_rows))
         xq, xs = self.x[:M], self.x_scales[:M]
         fp8_quantize(x, xq, xs, stream=stream)
-        fp8_matmul(xq, xs, self.codes, self.scales, out, self._ws[M], stream)
+        fp8_matmul(xq, xs, self.codes, self.scales, out, self.ws, stream)
         return out
+
+    def device_status(self, stream=None):
+        """(status, raw word) of the products since the last call, as read_device_status."""
+        return read_device_status(MoEConfig(T=1, d_model=128, n_experts=1, top_k=1, d_ff=128), self.ws, stream)
 
 
 def fp8_workspace_bytes(cfg: MoEConfig) -> int:

@@ -165,3 +165,52 @@ def test_results_are_allocated_on_the_calls_stream():
         del out
         assert torch.empty(size, dtype=dtype, device="cuda").data_ptr() != at
         torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------------------
+# Fp8Linear
+# ---------------------------------------------------------------------------
+def test_linear_keeps_one_workspace_and_captures():
+    """One workspace for every row count, made with the object: other row counts
+    allocate nothing, not even inside a capture, and give the product's bits."""
+    g = gen(6)
+    N, K, rows = 512, 4096, 300
+    w = torch.randn(N, K, generator=g, device="cuda").to(torch.bfloat16) * 0.02
+    lin = smr.Fp8Linear(w, rows)
+    x = torch.randn(rows, K, generator=g, device="cuda").to(torch.bfloat16)
+    want = {}
+    for M in (1, 16, 17, 128, 129, 300):
+        xq, xs = smr.fp8_empty(M, K)
+        smr.fp8_quantize(x[:M], xq, xs)
+        want[M] = torch.empty(M, N, device="cuda")
+        smr.fp8_matmul(xq, xs, lin.codes, lin.scales, want[M], smr.fp8_matmul_workspace(M, N, K))
+    out = torch.empty(rows, N, device="cuda")
+    torch.cuda.synchronize()
+    gc.collect()
+    before = torch.cuda.memory_allocated()
+    for M in want:
+        lin(x[:M], out[:M])
+        assert torch.equal(out[:M], want[M])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lin(x[:100], out[:100])
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out[:100], want[128][:100])
+    del graph
+    assert torch.cuda.memory_allocated() == before
+    with pytest.raises(ValueError):
+        lin(torch.zeros(rows + 1, K, device="cuda"), torch.empty(rows + 1, N, device="cuda"))
+
+
+def test_linear_reports_a_timeout():
+    g = gen(7)
+    lin = smr.Fp8Linear(torch.randn(300, 512, generator=g, device="cuda"), 200)
+    x, out = torch.randn(200, 512, generator=g, device="cuda"), torch.empty(200, 300, device="cuda")
+    want = lin(x, out).clone()
+    assert lin.device_status()[0] == 0
+    smr.inject_stall("f8_matmul", 2000)
+    lin(x, out)
+    assert lin.device_status()[0] == smr._STATUS.index("MOE_ERR_DEVICE_TIMEOUT")
+    assert torch.equal(lin(x, out), want) and lin.device_status()[0] == 0

@@ -813,6 +813,7 @@ moe_status_t moe_read_device_status(const moe_cfg_t* cfg, void* stream, uint32_t
   // this workspace is running once the stream has synchronised)
   const size_t clear = (word & kDevTimeout) ? sizeof(Ctrl) : sizeof(word);
   if (cudaMemsetAsync(cfg->workspace, 0, clear, st) != cudaSuccess) return MOE_ERR_CUDA;
+  if ((word & kDevTimeout) && f8_reset_counters(*cfg, st) != cudaSuccess) return MOE_ERR_CUDA;
   if (cudaStreamSynchronize(st) != cudaSuccess) return MOE_ERR_CUDA;
   if (info) *info = word;
   if (word & kDevTimeout) return MOE_ERR_DEVICE_TIMEOUT;

@@ -367,6 +367,15 @@ moe_status_t enqueue_experts(const void* x, const float* r_attn, const int32_t* 
 }
 
 }  // namespace
+
+cudaError_t f8_reset_counters(const moe_cfg_t& c, cudaStream_t st) {
+  if (c.expert_dtype != MOE_F8_E4M3_B128 || validate_f8(&c) != MOE_OK || check_workspace(&c) != MOE_OK)
+    return cudaSuccess;
+  const F8Plan p = f8_plan(c);
+  if (!p.counters_bytes) return cudaSuccess;
+  return cudaMemsetAsync(at<char>(&c, p.counters), 0, p.counters_bytes, st);
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -470,11 +479,8 @@ moe_status_t moe_fp8_workspace_init(const moe_cfg_t* cfg, void* stream) {
   const moe_status_t e = check_workspace(cfg);
   if (e != MOE_OK) return e;
   cudaStream_t st = (cudaStream_t)stream;
-  const F8Plan p = f8_plan(*cfg);
-  cudaError_t c = cudaMemsetAsync(cfg->workspace, 0, sizeof(Ctrl), st);
-  if (c == cudaSuccess && p.counters_bytes)
-    c = cudaMemsetAsync(at<char>(cfg, p.counters), 0, p.counters_bytes, st);
-  return cuda_status(c);
+  const cudaError_t c = cudaMemsetAsync(cfg->workspace, 0, sizeof(Ctrl), st);
+  return cuda_status(c == cudaSuccess ? f8_reset_counters(*cfg, st) : c);
 }
 
 moe_status_t moe_fp8_experts_forward(const void* x, const float* r_attn, const int32_t* topk_ids,

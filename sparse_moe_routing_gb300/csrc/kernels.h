@@ -369,6 +369,10 @@ moe_status_t route_chain(const void* x, const void* W_router, const float* bias,
                          const void* w_shared, const moe_cfg_t* c, int32_t* ids, float* w,
                          float* s_shared, cudaStream_t st);
 
+// Zeroes the counters that the 8-bit layer's workspace holds outside its control
+// block; nothing for a workspace of other calls.
+cudaError_t f8_reset_counters(const moe_cfg_t& c, cudaStream_t st);
+
 // One launcher per kernel; each returns the launch's cudaError_t.
 cudaError_t launch_router_logits(const RouterArgs& ra, bool bf16, cudaStream_t st);
 cudaError_t launch_router_topk(const TopkArgs& ta, cudaStream_t st);

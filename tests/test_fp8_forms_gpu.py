@@ -214,3 +214,21 @@ def test_linear_reports_a_timeout():
     lin(x, out)
     assert lin.device_status()[0] == smr._STATUS.index("MOE_ERR_DEVICE_TIMEOUT")
     assert torch.equal(lin(x, out), want) and lin.device_status()[0] == 0
+
+
+# ---------------------------------------------------------------------------
+# after a timeout
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("shape,T", [("tiny", 5), ("apart", 16), ("tiny", 40)])
+def test_reading_a_timeout_makes_the_workspace_usable(shape, T):
+    """What a kernel that gave up leaves behind, made on the host: the status bit
+    and counts of finished items (here ones that never come to an end)."""
+    x, ids, alpha, w, gate = make_exact(shape, T)
+    layer = smr.Fp8Experts(config(shape, T), w)
+    want = layer.forward(x, ids, alpha, s_shared=gate).clone()
+    layer.ws.fill_(0)
+    layer.ws[256:].view(torch.int32).fill_(1000)
+    layer.ws[:4].view(torch.int32).fill_(2)
+    assert layer.device_status()[0] == smr._STATUS.index("MOE_ERR_DEVICE_TIMEOUT")
+    assert torch.equal(layer.forward(x, ids, alpha, s_shared=gate), want)
+    assert layer.device_status()[0] == 0

@@ -432,9 +432,10 @@ moe_status_t moe_fp8_matmul(const void* a, const float* a_scale, const void* b, 
     return MOE_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   if (mm->M <= kF8FewTokens) {
-    const F8MatmulArgs f{static_cast<const uint8_t*>(a), a_scale, static_cast<const uint8_t*>(b),
-                         b_scale, out, static_cast<Ctrl*>(mm->workspace), mm->M, mm->N, mm->K, bf16 ? 1 : 0,
-                         mm->lda, mm->ldb, mm->ldo};
+    F8MatmulArgs f{static_cast<const uint8_t*>(a), a_scale, static_cast<const uint8_t*>(b),
+                   b_scale, out, static_cast<Ctrl*>(mm->workspace), mm->M, mm->N, mm->K, bf16 ? 1 : 0,
+                   mm->lda, mm->ldb, mm->ldo, 0, 0};
+    f.wait_ns = launch_wait_limit(MOE_KERNEL_F8_MATMUL, &f.stall);
     return cuda_status(run_kernel(MOE_KERNEL_F8_MATMUL, st, [&] { return launch_f8_few_matmul(f, st); }));
   }
   F8TcMaps m{};

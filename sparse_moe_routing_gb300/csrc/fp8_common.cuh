@@ -69,9 +69,9 @@ __device__ __forceinline__ bool f8_lane_wait(uint64_t* bar, uint32_t parity, uin
 // The whole warp waits. Every lane polls: one lane's poll with its outcome
 // shuffled to the others took 1390 cycles for a round trip between one warp
 // and sixteen, this 260 (measured alone).
-__device__ __forceinline__ bool f8_warp_wait(uint64_t* bar, uint32_t parity, Ctrl* ctrl,
+__device__ __forceinline__ bool f8_warp_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns, Ctrl* ctrl,
                                              uint32_t site) {
-  const bool ok = __all_sync(0xffffffffu, f8_lane_wait(bar, parity, kWaitLimitNs, nullptr));
+  const bool ok = __all_sync(0xffffffffu, f8_lane_wait(bar, parity, limit_ns, nullptr));
   if (!ok) {
     if ((threadIdx.x & 31) == 0) report(ctrl, kDevTimeout, site);
     // copies already in flight land before the warp can leave

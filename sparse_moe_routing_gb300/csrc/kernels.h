@@ -263,6 +263,8 @@ struct F8MatmulArgs {
   Ctrl* ctrl;
   int M, N, K, out_bf16;
   long long lda, ldb, ldo;
+  uint64_t wait_ns;
+  int stall;
 };
 cudaError_t launch_f8_few_matmul(const F8MatmulArgs& a, cudaStream_t st);
 

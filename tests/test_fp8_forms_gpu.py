@@ -232,3 +232,19 @@ def test_reading_a_timeout_makes_the_workspace_usable(shape, T):
     assert layer.device_status()[0] == smr._STATUS.index("MOE_ERR_DEVICE_TIMEOUT")
     assert torch.equal(layer.forward(x, ids, alpha, s_shared=gate), want)
     assert layer.device_status()[0] == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 640, 256), (8, 4096, 2048), (16, 300, 1000)])
+def test_few_row_product_wait_that_runs_out_is_reported(M, N, K):
+    g = gen(M)
+    (a, sa), (b, sb) = random_matrix(g, M, K, 1), random_matrix(g, N, K, 128)
+    out, ws = torch.empty(M, N, device="cuda"), smr.fp8_matmul_workspace(M, N, K)
+    smr.fp8_matmul(a, sa, b, sb, out, ws)
+    want = out.clone()
+    cfg = smr.MoEConfig(T=1, d_model=128, n_experts=1, top_k=1, d_ff=128)
+    smr.inject_stall("f8_matmul", 2000)
+    smr.fp8_matmul(a, sa, b, sb, out, ws)
+    assert smr.read_device_status(cfg, ws)[0] == smr._STATUS.index("MOE_ERR_DEVICE_TIMEOUT")
+    smr.fp8_matmul(a, sa, b, sb, out, ws)
+    assert smr.read_device_status(cfg, ws)[0] == 0
+    assert torch.equal(out, want)

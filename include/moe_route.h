@@ -217,8 +217,9 @@ MOE_API moe_status_t moe_trace_kernel(int kernel, void* const* starts, void* con
 
 /* Failure-detection self-test: the next launch of kernel family `kernel`
  * (MOE_KERNEL_TC_GATEUP, MOE_KERNEL_TC_DOWN, MOE_KERNEL_DECODE,
- * MOE_KERNEL_F8_TC_GATEUP, MOE_KERNEL_F8_TC_DOWN or MOE_KERNEL_F8_MATMUL)
- * waits on a flag that nothing sets, and every bounded wait of that launch gives up
+ * MOE_KERNEL_F8_TC_GATEUP, MOE_KERNEL_F8_TC_DOWN or MOE_KERNEL_F8_MATMUL; the
+ * few-token gate/up and down take the stall of the tensor-core ones in whose
+ * place they run) waits on a flag that nothing sets, and every bounded wait of that launch gives up
  * after wait_us microseconds instead of about one second. The launch then
  * records MOE_ERR_DEVICE_TIMEOUT in its workspace's status word, lets its
  * copies in flight land, frees its tensor memory and returns; the call's

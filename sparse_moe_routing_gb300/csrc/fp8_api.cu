@@ -210,9 +210,12 @@ moe_status_t enqueue_few(const void* x, const float* r_attn, const int32_t* ids,
     m.sw = m.w;
   }
   m.sx = m.x;
+  // (armed as the layer's gate/up and down, whichever kernels run them)
+  a.wait_ns = launch_wait_limit(MOE_KERNEL_F8_TC_GATEUP, &a.stall);
   cudaError_t e =
       run_kernel(MOE_KERNEL_F8_FEW_GATEUP, st, [&] { return launch_f8_few_gateup(m, a, st); });
   if (e != cudaSuccess) return MOE_ERR_CUDA;
+  a.wait_ns = launch_wait_limit(MOE_KERNEL_F8_TC_DOWN, &a.stall);
   return cuda_status(run_kernel(MOE_KERNEL_F8_FEW_DOWN, st, [&] { return launch_f8_few_down(m, a, st); }));
 }
 

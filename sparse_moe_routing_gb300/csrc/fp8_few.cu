@@ -99,6 +99,12 @@ __device__ __forceinline__ void reads_before_refill() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Arrivals that complete slot i's barrier. Failure self-test: the first slot of
+// the first warp waits for one that never comes.
+__device__ __forceinline__ uint32_t few_arrivals(uint32_t n, int i, int stall) {
+  return n + (stall && i == 0 ? 1u : 0u);
+}
+
 // A box of rows of 128 bytes, 1024-byte aligned; TMA puts piece p (16 bytes) of
 // row r at p ^ (r % 8).
 constexpr int kBox8 = 1024, kBox16 = 2048;
@@ -257,7 +263,8 @@ __global__ void __launch_bounds__(kGuThreads, 1)
       tc::mbar_init(&S.full[0][0] + i, nsplit);
       tc::mbar_init(&S.empty[0][0] + i, 1);
     }
-    for (int i = 0; i < kGuWarps * kGuAhead; ++i) tc::mbar_init(&S.landed[0][0] + i, kGuArrivals);
+    for (int i = 0; i < kGuWarps * kGuAhead; ++i)
+      tc::mbar_init(&S.landed[0][0] + i, few_arrivals(kGuArrivals, i, a.stall));
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_wait();
@@ -365,7 +372,7 @@ __global__ void __launch_bounds__(kGuThreads, 1)
         kx = 2 * w;
       }
       if (steps) {
-        if (!f8_warp_wait(&S.landed[warp][j], ph, kWaitLimitNs, a.ctrl, kSiteFewFp8)) break;
+        if (!f8_warp_wait(&S.landed[warp][j], ph, a.wait_ns, a.ctrl, kSiteFewFp8)) break;
         const uint32_t slot = ring32 + j * kGuSlot;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -403,7 +410,7 @@ __global__ void __launch_bounds__(kGuThreads, 1)
       }
       // the item's partial sums go to a finisher
       const int at = r % SLOTS;
-      if (!f8_warp_wait(&S.empty[at][group], (r / SLOTS & 1) ^ 1, kWaitLimitNs, a.ctrl, kSiteFewFp8)) break;
+      if (!f8_warp_wait(&S.empty[at][group], (r / SLOTS & 1) ^ 1, a.wait_ns, a.ctrl, kSiteFewFp8)) break;
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         S.part[at][warp][m][lane] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
@@ -462,7 +469,7 @@ __global__ void __launch_bounds__(kGuThreads, 1)
       const int c = now.c, rb = now.rb, start = L.start[c], cnt = L.count[c];
       const bool sh = L.expert[c] == a.E;
       const int slot = r % SLOTS;
-      if (!f8_warp_wait(&S.full[slot][group], r / SLOTS & 1, kWaitLimitNs, a.ctrl, kSiteFewFp8)) break;
+      if (!f8_warp_wait(&S.full[slot][group], r / SLOTS & 1, a.wait_ns, a.ctrl, kSiteFewFp8)) break;
       const float4(*part)[2][32] = S.part[slot] + group * nsplit;
       float4 v[2];
 #pragma unroll
@@ -551,7 +558,8 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1)
   float* ysum = S.ysum;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   if (tid == 0) {
-    for (int i = 0; i < WARPS * AHEAD; ++i) tc::mbar_init(&S.landed[0][0] + i, kDnArrivals);
+    for (int i = 0; i < WARPS * AHEAD; ++i)
+      tc::mbar_init(&S.landed[0][0] + i, few_arrivals(kDnArrivals, i, a.stall));
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   const int P = a.T * a.k, rows_all = P + (a.Is > 0 ? a.T : 0);
@@ -662,7 +670,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1)
       if (++filled_x < filled_w) continue;
     }
     if (now.left == 0) break;
-    if (!f8_warp_wait(&S.landed[warp][j], ph, kWaitLimitNs, a.ctrl, kSiteFewFp8)) break;
+    if (!f8_warp_wait(&S.landed[warp][j], ph, a.wait_ns, a.ctrl, kSiteFewFp8)) break;
     const uint32_t slot = ring32 + j * kDnSlot, sc = sc32 + 80 * j;
     // the last pair's second block may not exist; the activations' rows may be
     // longer, and what lies there is nobody's
@@ -751,7 +759,6 @@ struct MmShared {
   uint8_t ring[kMmWarps][AHEAD][mm_slot<NT>()];
   float4 part[2][NT][kMmWarps][32];
   uint64_t landed[kMmWarps][AHEAD];
-  uint64_t never;
   float scale[kMmWarps][AHEAD][36];  // of the activation rows, two blocks; [32], [33]: weights
 };
 template <int NT, int AHEAD>
@@ -763,8 +770,8 @@ __global__ void __launch_bounds__(kMmWarps * 32, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   // arrivals: the boxes' bytes, each lane's scale (or two), two of the weights
   if (tid == 0) {
-    for (int i = 0; i < kMmWarps * AHEAD; ++i) tc::mbar_init(&S.landed[0][0] + i, 3 + 16 * NT);
-    tc::mbar_init(&S.never, 1);
+    for (int i = 0; i < kMmWarps * AHEAD; ++i)
+      tc::mbar_init(&S.landed[0][0] + i, few_arrivals(3 + 16 * NT, i, a.stall));
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
@@ -813,11 +820,8 @@ __global__ void __launch_bounds__(kMmWarps * 32, 1)
   bool alive = true;
   while (r < rounds) {
     const int i = first + r * stride;
-    if (alive && i < items && pr < pairs) {
-      // failure self-test: the first warp waits on a barrier that nothing completes
-      uint64_t* bar = a.stall && warp == 0 ? &S.never : &S.landed[warp][j];
-      alive = f8_warp_wait(bar, ph, a.wait_ns, a.ctrl, kSiteFewFp8);
-    }
+    if (alive && i < items && pr < pairs)
+      alive = f8_warp_wait(&S.landed[warp][j], ph, a.wait_ns, a.ctrl, kSiteFewFp8);
     // (a warp whose wait gave up loads nothing more and goes along to the barriers)
     if (alive && i < items && pr < pairs) {
       const uint32_t slot = ring32 + j * mm_slot<NT>(), sc = sc32 + 144 * j;

@@ -243,6 +243,8 @@ struct F8ExpertsArgs {
   void* out;               // [T][d]
   Ctrl* ctrl;
   int T, d, E, k, I, Is, ldh, hblocks, out_bf16;
+  uint64_t wait_ns;
+  int stall;
 };
 constexpr int kF8FewTokens = 16;
 bool f8_few_ok(int T, int d, int k);

@@ -234,6 +234,22 @@ def test_reading_a_timeout_makes_the_workspace_usable(shape, T):
     assert layer.device_status()[0] == 0
 
 
+@pytest.mark.parametrize("kernel,shape,T", [("f8_tc_gateup", "tiny", 5), ("f8_tc_gateup", "e256", 8),
+                                            ("f8_tc_down", "tiny", 5), ("f8_tc_down", "e256", 16)])
+def test_few_token_waits_that_run_out_are_reported(kernel, shape, T):
+    """The few-token kernels take the stall of the layer's gate/up and down."""
+    x, ids, alpha, w, gate = make_exact(shape, T)
+    layer = smr.Fp8Experts(config(shape, T), w)
+    out = torch.empty(x.shape, dtype=torch.bfloat16, device="cuda")
+    want = layer.forward(x, ids, alpha, s_shared=gate, out=out).clone()
+    smr.inject_stall(kernel, 2000)
+    layer.forward(x, ids, alpha, s_shared=gate, out=out)
+    assert layer.device_status()[0] == smr._STATUS.index("MOE_ERR_DEVICE_TIMEOUT")
+    layer.forward(x, ids, alpha, s_shared=gate, out=out)
+    assert layer.device_status()[0] == 0
+    assert torch.equal(out, want)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 640, 256), (8, 4096, 2048), (16, 300, 1000)])
 def test_few_row_product_wait_that_runs_out_is_reported(M, N, K):
     g = gen(M)

@@ -330,7 +330,8 @@ MOE_API moe_status_t moe_layer_forward(const void* x, const float* r_attn,
  * A matrix in 8 bits is codes (e4m3: 4 exponent and 3 fraction bits, largest
  * number 448, no infinity) and f32 scales, one per block of 128 columns and
  * of 1 row (activations) or 128 rows (weights); blocks at the ends are cut.
- * It stands for code * scale. Any f32 scales are taken as inputs.
+ * It stands for code * scale. Any f32 scales are taken as inputs; a block's
+ * sum is multiplied by the f32 product of its two scales.
  * ------------------------------------------------------------------------ */
 
 /* Quantises x [count][rows][ldx] (F32 or BF16, the first `cols` of every ldx

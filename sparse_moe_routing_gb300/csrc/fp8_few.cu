@@ -73,10 +73,12 @@ struct BlockSum {
 
 __device__ __forceinline__ uint4 zero4() { return make_uint4(0u, 0u, 0u, 0u); }
 
-// Scales come by 4-byte asynchronous copies; each copying lane arrives on the
-// slot's barrier once its copy has landed.
-__device__ __forceinline__ void copy4(float* dst, const float* src, uint64_t* bar) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
+// Scales come by 4-byte asynchronous copies (or as zero); each copying lane
+// arrives on the slot's barrier once its copy has landed.
+__device__ __forceinline__ void copy4(float* dst, const float* src, uint64_t* bar, bool valid = true) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(dst)), "l"(src),
+               "r"(valid ? 4 : 0)
+               : "memory");
   asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
 }
 template <int OFF>
@@ -795,17 +797,19 @@ __global__ void __launch_bounds__(kMmWarps * 32, 1)
     uint8_t* dst = ring + j * mm_slot<NT>();
     const int kb = 2 * lp;
     if (lane == 0) {
-      // rows and columns past the ends, a second block among them, come as zeros
+      // rows and columns past the ends, a second block among them, come as zeros,
+      // and so do that block's scales (zero codes with infinite ones were NaN)
       tc::mbar_expect_tx(bar, mm_slot<NT>());
       tc::tma_load_2d(dst, &tmB, bar, kb * kF8Block, li * 16);
       tc::tma_load_2d(dst + kBox16, &tmB, bar, (kb + 1) * kF8Block, li * 16);
       tc::tma_load_2d(dst + 2 * kBox16, &tmA, bar, kb * kF8Block, 0);
       tc::tma_load_2d(dst + 2 * kBox16 + NT * kBox8, &tmA, bar, (kb + 1) * kF8Block, 0);
     }
-    if (lane < 16 * NT) copy4(&S.scale[warp][j][lane], xsc + min(kb + lane / (8 * NT), KB - 1), bar);
+    const int kx = kb + lane / (8 * NT);
+    if (lane < 16 * NT) copy4(&S.scale[warp][j][lane], xsc + min(kx, KB - 1), bar, kx < KB);
     if (lane < 2)
       copy4(&S.scale[warp][j][32 + lane],
-            a.b_scale + (size_t)(li * 16 / kF8Block) * KB + min(kb + lane, KB - 1), bar);
+            a.b_scale + (size_t)(li * 16 / kF8Block) * KB + min(kb + lane, KB - 1), bar, kb + lane < KB);
     lp += wpi;
     if (lp >= pairs) {
       lp = w;

@@ -142,6 +142,29 @@ def test_experts_with_many_slots(T, k):
 
 
 # ---------------------------------------------------------------------------
+# products: infinite scales
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("M", [1, 9, 16, 17, 40])
+@pytest.mark.parametrize("K", [128, 100, 256, 640])
+def test_matmul_infinite_scales_and_sums(M, K):
+    """A row with an infinite scale (positive codes) gives infinity, and so does a
+    product of scales above fp32's range, also where the number of blocks is odd."""
+    g = gen(M + K)
+    a = pitched((torch.rand(M, K, generator=g, device="cuda") * 100 + 1).to(F8))
+    b = pitched((torch.rand(33, K, generator=g, device="cuda") * 100 + 1).to(F8))
+    sa, sb = torch.ones(M, blocks(K), device="cuda"), torch.ones(1, blocks(K), device="cuda")
+    out = torch.empty(M, 33, device="cuda")
+    ws = smr.fp8_matmul_workspace(M, 33, K)
+    sa[0] = math.inf
+    smr.fp8_matmul(a, sa, b, sb, out, ws)
+    assert bool((out[0] == math.inf).all()) and bool(out[1:].isfinite().all())
+    sa.fill_(2.0 ** 70)
+    sb.fill_(2.0 ** 70)
+    smr.fp8_matmul(a, sa, b, sb, out, ws)
+    assert bool((out == math.inf).all())
+
+
+# ---------------------------------------------------------------------------
 # streams
 # ---------------------------------------------------------------------------
 def test_results_are_allocated_on_the_calls_stream():

@@ -654,7 +654,7 @@ class Fp8Experts:
     def __init__(self, cfg: MoEConfig, weights: dict, device=None):
         import torch
         self.cfg = cfg
-        self.w = weights
+        self.w = dict(weights)  # (the calls go by the banks' addresses)
         _check_routing(cfg, weights.get("W_router"), weights.get("expert_bias"), weights.get("w_shared"))
         self.device = device or torch.device("cuda", torch.cuda.current_device())
         self.ws = fp8_alloc_workspace(cfg, self.device)

@@ -287,3 +287,17 @@ def test_few_row_product_wait_that_runs_out_is_reported(M, N, K):
     smr.fp8_matmul(a, sa, b, sb, out, ws)
     assert smr.read_device_status(cfg, ws)[0] == 0
     assert torch.equal(out, want)
+
+
+# ---------------------------------------------------------------------------
+# the object's own weights
+# ---------------------------------------------------------------------------
+def test_experts_hold_their_weights_themselves():
+    """The banks stay alive and in use when the caller empties its dict."""
+    x, ids, alpha, w, gate = make_exact("tiny", 5)
+    layer = smr.Fp8Experts(config("tiny", 5), w)
+    banks = dict(w)
+    want = layer.forward(x, ids, alpha, s_shared=gate).clone()
+    w.clear()
+    assert all(layer.w[n][i] is banks[n][i] for n in banks for i in (0, 1))
+    assert torch.equal(layer.forward(x, ids, alpha, s_shared=gate), want)

@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, replace
 
 __all__ = [
     "MoEConfig", "MoEError", "lib", "lib_path", "abi_version", "status_string",
@@ -580,7 +580,8 @@ _layer_types = None
 
 
 def _check_layer(cfg, x, topk_ids, weights, out, s_shared, r_attn):
-    """Types and shapes of the 8-bit layer's tensors."""
+    """Types and shapes of the 8-bit layer's tensors; cfg a MoEConfig or the
+    structure that the call gets."""
     global _layer_types
     if _layer_types is None:
         import torch
@@ -653,7 +654,7 @@ class Fp8Experts:
 
     def __init__(self, cfg: MoEConfig, weights: dict, device=None):
         import torch
-        self.cfg = cfg
+        self.cfg = replace(cfg)
         self.w = dict(weights)  # (the calls go by the banks' addresses)
         _check_routing(cfg, weights.get("W_router"), weights.get("expert_bias"), weights.get("w_shared"))
         self.device = device or torch.device("cuda", torch.cuda.current_device())
@@ -683,7 +684,7 @@ class Fp8Experts:
         import torch
         if out is None:
             out = _empty(self._x_shape, torch.bfloat16, self.device, stream)
-        _check_layer(self.cfg, x, topk_ids, weights, out, s_shared, r_attn)
+        _check_layer(self._c, x, topk_ids, weights, out, s_shared, r_attn)
         _check(lib().moe_fp8_experts_forward(
             _ptr(x), _ptr(r_attn), _ptr(topk_ids), _ptr(weights), _ptr(s_shared), *self._banks,
             self._w_shared, self._cp, _ptr(out), _dtype_of(out), _stream(stream)),
@@ -694,7 +695,7 @@ class Fp8Experts:
         import torch
         if out is None:
             out = _empty(self._x_shape, torch.bfloat16, self.device, stream)
-        _check_layer(self.cfg, x, topk_ids, weights, out, None, r_attn)
+        _check_layer(self._c, x, topk_ids, weights, out, None, r_attn)
         _check(lib().moe_fp8_layer_forward(
             _ptr(x), _ptr(r_attn), _ptr(self.w["W_router"]), _ptr(self.w.get("expert_bias")),
             *self._banks, self._w_shared, self._cp, _ptr(out), _dtype_of(out),

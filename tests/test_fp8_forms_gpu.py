@@ -301,3 +301,16 @@ def test_experts_hold_their_weights_themselves():
     w.clear()
     assert all(layer.w[n][i] is banks[n][i] for n in banks for i in (0, 1))
     assert torch.equal(layer.forward(x, ids, alpha, s_shared=gate), want)
+
+
+def test_experts_hold_their_configuration_themselves():
+    """The sizes that a call checks are those that it was made for."""
+    x, ids, alpha, w, gate = make_exact("tiny", 5)
+    cfg = config("tiny", 5)
+    layer = smr.Fp8Experts(cfg, w)
+    want = layer.forward(x, ids, alpha, s_shared=gate).clone()
+    for c in (cfg, layer.cfg):
+        c.T = 3
+        with pytest.raises(ValueError):
+            layer.forward(x[:3], ids[:3], alpha[:3], s_shared=gate[:3])
+        assert torch.equal(layer.forward(x, ids, alpha, s_shared=gate), want)

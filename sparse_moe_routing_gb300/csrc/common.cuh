@@ -109,7 +109,11 @@ __device__ __forceinline__ float siluf_(float v) { return __fdividef(v, 1.0f + _
 // until the predecessor grid has completed and its writes are visible, and
 // must come before the kernel's first global memory access; pdl_trigger()
 // then lets the successor grid be scheduled. Both are no-ops for a plain
-// launch.
+// launch. Every kernel triggers after its own wait only: when a kernel starts,
+// all but its direct predecessor have completed. One kernel relies on that:
+// f8_few_down reads, before it waits, what is older than its direct predecessor,
+// f8_few_gateup, which the same call launches (the ids, the weights and their
+// scales; nothing that gate/up writes).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

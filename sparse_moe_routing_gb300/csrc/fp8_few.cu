@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kGuThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_wait();
-  pdl_trigger();
+  pdl_trigger();  // (not before the wait: f8_few_down relies on it)
 
   // item i: 16 rows `rb` of chunk `c`; a group's items are `stride` apart
   const int RB = a.I / kGuRows, RBs = a.Is / kGuRows;
@@ -568,8 +568,10 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS <= 8 ? 2 : 1)
   const int col0 = blockIdx.x * kDnCols;
   const int KBr = f8_blocks(a.I), KBs = f8_blocks(a.Is), NB = f8_blocks(a.d);
   const int PRr = (KBr + 1) / 2, PRs = (KBs + 1) / 2;  // pairs of blocks
-  // The ids and the weights are older than the gate/up kernel, which has
-  // itself waited for its predecessor before letting this one start.
+  // The ids and the weights, read before pdl_wait, are older than the gate/up
+  // kernel, which has itself waited for its predecessor before letting this one
+  // start (f8_few_gateup triggers after its wait; nothing may be launched between
+  // the two).
   build_lists<WARPS * 32>(a, L);
   // k split of a chunk: the one that leaves the busiest warp the fewest pairs
   const int PR = PRr > PRs ? PRr : PRs, room = max(rows_all, 16 * WARPS);
@@ -770,7 +772,7 @@ __global__ void __launch_bounds__(kMmWarps * 32, 1)
   extern __shared__ uint8_t smem_raw[];
   MmShared<NT, AHEAD>& S = *reinterpret_cast<MmShared<NT, AHEAD>*>(align1024(smem_raw));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  // arrivals: the boxes' bytes, each lane's scale (or two), two of the weights
+  // arrivals: the boxes' bytes, 16 NT scales of the rows, two of the weights
   if (tid == 0) {
     for (int i = 0; i < kMmWarps * AHEAD; ++i)
       tc::mbar_init(&S.landed[0][0] + i, few_arrivals(3 + 16 * NT, i, a.stall));
@@ -787,7 +789,7 @@ __global__ void __launch_bounds__(kMmWarps * 32, 1)
   const int stride = (int)gridDim.x * teams, rounds = (items + stride - 1) / stride;
   const int first = team * (int)gridDim.x + (int)blockIdx.x;
   const uint32_t get = get_at(g, t);
-  // lane's scales: row lane % 8 NT, blocks lane / 8 NT (and, for two tiles, + 2)
+  // the lane's scale: row lane % (8 NT), block lane / (8 NT) of the two
   const float* xsc = a.a_scale + (size_t)min(lane & (8 * NT - 1), a.M - 1) * KB;
   uint8_t* ring = S.ring[warp][0];
   int li = first, lp = w;  // the loads' item and pair of blocks

@@ -326,7 +326,8 @@ inline cudaError_t ensure_smem_limit(K kernel, int bytes, int* limits) {
 // Launches `kernel` with programmatic stream serialization: its CTAs may be
 // scheduled (and run their set-up) while the previous kernel on the stream
 // is still finishing. Every kernel of this library calls pdl_wait() before
-// its first global memory access, so only launch latency and set-up overlap.
+// its first global memory access, so only launch latency and set-up overlap
+// (but f8_few_down, which reads before it what its predecessor does not write).
 template <typename... P, typename... A>
 inline cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
                               cudaStream_t st, A&&... args) {

@@ -314,3 +314,68 @@ def test_experts_hold_their_configuration_themselves():
         with pytest.raises(ValueError):
             layer.forward(x[:3], ids[:3], alpha[:3], s_shared=gate[:3])
         assert torch.equal(layer.forward(x, ids, alpha, s_shared=gate), want)
+
+
+# ---------------------------------------------------------------------------
+# sizes at which a block or a CTA takes more than one turn
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("rows,cols", [(4097, 1001), (4097, 1024), (2500, 1100)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_quantize_many_blocks(rows, cols, dtype):
+    x = torch.randn(rows, cols, generator=gen(rows + cols), device="cuda")
+    x = (x * torch.exp(3 * torch.randn(rows, 1, generator=gen(7), device="cuda"))).to(dtype)
+    codes, scales = smr.fp8_empty(rows, cols)
+    smr.fp8_quantize(x, codes, scales)
+    p = torch.nn.functional.pad(x.double(), (0, -cols % 128)).view(rows, -1, 128)
+    m, e = torch.frexp(p.abs().amax(-1))
+    s = torch.exp2(torch.where(m > 0.875, e - 8, e - 9).clamp(min=-126).double())
+    assert torch.equal(scales.double(), s)
+    assert torch.equal(codes.double(), round_e4m3(p / s[..., None]).view(rows, -1)[:, :cols])
+    assert torch.equal(values(codes, scales, 1), quantize64(x.double()))
+
+
+@pytest.mark.parametrize("M,N,K", [(1700, 3000, 400), (1300, 300, 2048), (1025, 520, 1100)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_matmul_many_tiles(M, N, K, dtype):
+    """More tiles than SMs (a CTA's second tile), and split k over more than one
+    band of row blocks; bound of the sums as for the smaller products."""
+    g = gen(M + N + K)
+    (a, sa), (b, sb) = random_matrix(g, M, K, 1), random_matrix(g, N, K, 128)
+    out = torch.full((M, N), 7.0, dtype=dtype, device="cuda")
+    smr.fp8_matmul(a, sa, b, sb, out, smr.fp8_matmul_workspace(M, N, K))
+    A, B = values(a, sa, 1), values(b, sb, 128)
+    ref = A @ B.T
+    tol = (128 + blocks(K) + 2) * 2.0 ** -23 * (A.abs() @ B.abs().T) + 1e-30
+    if dtype == torch.bfloat16:
+        tol = tol + 2.0 ** -8 * (ref.abs() + tol)
+    err = (out.double() - ref).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+
+
+# ---------------------------------------------------------------------------
+# the sigmoid-group rule with 8-bit banks
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("T", [1, 16, 40])
+def test_layer_with_the_sigmoid_group_rule(T):
+    """ids and weights are bit for bit those of the routing call; the result is
+    that of the experts for them."""
+    d, E, k, width, shared = SHAPES["tiny"]
+    x, _, _, w, _ = make_exact("tiny", T)
+    g = gen(T)
+    w["W_router"] = (torch.randn(E, d, generator=g, device="cuda") * 0.1).to(torch.bfloat16)
+    w["w_shared"] = (torch.randn(d, generator=g, device="cuda") * 0.1).to(torch.bfloat16)
+    w["expert_bias"] = torch.randn(E, generator=g, device="cuda") * 0.1
+    rule = dict(router=smr.SIGMOID_GROUP_TOPK, n_group=4, topk_group=2, routed_scaling=2.5)
+    layer = smr.Fp8Experts(config("tiny", T, **rule), w)
+    ids, alpha = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+    out = layer.layer(x, ids, alpha, out=torch.empty(T, d, device="cuda"))
+    base = smr.MoEConfig(T=T, d_model=d, n_experts=E, top_k=k, d_ff=width, d_ff_shared=shared,
+                         path=smr.PATH_GEMV, **rule)  # the separate routing kernels
+    ids16, alpha16 = torch.empty_like(ids), torch.empty_like(alpha)
+    smr.route(base, smr.alloc_workspace(base), x, w["W_router"], ids16, alpha16, expert_bias=w["expert_bias"])
+    assert torch.equal(ids, ids16) and torch.equal(alpha, alpha16)
+    gate = torch.sigmoid(x.double() @ w["w_shared"].double())
+    half = layer.forward(x, ids, alpha, s_shared=gate.float(), out=torch.empty(T, d, device="cuda"))
+    banks = {n: b for n, b in w.items() if isinstance(b, tuple)}
+    check_sums(half, x, ids, alpha, banks, gate.float())
+    assert float((out - half).abs().max()) <= 1e-5 * float(half.abs().max())

@@ -76,10 +76,12 @@ moe_cfg_t route_cfg(const moe_cfg_t& c) {
 
 // The two kernels for a few tokens, unless wide experts average three pairs or
 // more each: mma.sync then meets every weight with several chunks' worth of
-// columns, and the tensor-core products are faster. us, few / tensor cores: 256
-// experts T=8 48.6 / 62, T=16 78.5 / 85; 60 experts T=16 102 / 121; 64 experts
-// T=16 105 / 98; 8 wide experts T=4 182 / 220, T=8 253 / 265, T=16 313 / 236;
-// the tiny shape T=16 (4 pairs each) 12.5 / 20.
+// columns, and the tensor-core products are faster. us, few / tensor cores (one
+// call, L2 flushed before it): 256 experts T=8 58 / 75, T=16 92 / 100; 60 experts
+// T=16 121 / 139; 8 wide experts T=4 189 / 194, T=8 253 / 251, T=12 287 / 251, T=16
+// 329 / 253; the tiny shape T=16 (4 pairs each) 17 / 26. Between them the rule
+// takes the slower side at one measured place: 64 experts of width 1408, T=12
+// 104 / 112 but T=16 (1.5 pairs each) 122 / 114.
 bool use_few(const moe_cfg_t& c) {
   if (c.path == MOE_PATH_TC || !f8_few_ok(c.T, c.d_model, c.top_k)) return false;
   if (c.path == MOE_PATH_GEMV) return true;

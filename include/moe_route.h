@@ -373,7 +373,9 @@ MOE_API size_t moe_fp8_matmul_workspace_bytes(const moe_fp8_matmul_t* mm);
 MOE_API moe_status_t moe_fp8_matmul_init(const moe_fp8_matmul_t* mm, void* stream);
 
 /* Workspace of the two calls below for this cfg (0 if invalid), and its
- * initialisation, once before its first use. Status is read with
+ * initialisation, once before its first use. One workspace serves any T that it
+ * is large enough for; another top_k or expert width needs the initialisation
+ * again. Status is read with
  * moe_read_device_status for the same cfg, which after a timeout also clears
  * the counts of finished items that a kernel that gave up can leave behind. */
 MOE_API size_t moe_fp8_workspace_bytes(const moe_cfg_t* cfg);

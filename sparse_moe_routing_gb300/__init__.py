@@ -547,7 +547,7 @@ def fp8_workspace_bytes(cfg: MoEConfig) -> int:
 
 def fp8_alloc_workspace(cfg: MoEConfig, device=None, stream=None):
     """Allocates (with torch) and initialises a workspace of the 8-bit layer on
-    `stream`."""
+    `stream`. It serves other T of the same layer too, where it is large enough."""
     import torch
     ws = _empty(fp8_workspace_bytes(cfg), torch.uint8, device, stream)
     _check(lib().moe_fp8_workspace_init(ctypes.byref(cfg._c(ws)), _stream(stream)),

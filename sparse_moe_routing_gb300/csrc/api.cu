@@ -20,7 +20,7 @@ constexpr int kTcBm = 128;  // token rows per tensor-core tile
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 struct Plan {
-  size_t ctrl, logits, s_shared, counts, offsets, active, perm, pos, rowblocks, cta_hist;
+  size_t ctrl, f8_counters, f8_counters_bytes, logits, s_shared, counts, offsets, active, perm, pos, rowblocks, cta_hist;
   size_t H, Hs, Y, Ys, Xperm, Gs, total;
 };
 
@@ -146,6 +146,9 @@ Plan make_plan(const moe_cfg_t& c) {
   const size_t T = c.T, E = c.n_experts, P = (size_t)c.T * c.top_k;
   const size_t d = c.d_model, I = c.d_ff, Is = c.d_ff_shared;
   p.ctrl = take(sizeof(Ctrl));
+  // (where every T of a shape has them, as kernels.h says)
+  p.f8_counters_bytes = c.expert_dtype == MOE_F8_E4M3_B128 ? f8_counter_bytes(c) : 0;
+  p.f8_counters = take(p.f8_counters_bytes);
   const bool small = T <= (size_t)kDecodeMaxTokens;
   p.logits = take(T * (E + 1) * 4 * (small ? kDecodeKSplit : 1));
   p.s_shared = take(T * 4);
@@ -720,8 +723,8 @@ uint64_t launch_wait_limit(int kid, int* stall) { return take_stall(kid, stall);
 
 RoutePlan route_plan(const moe_cfg_t& c) {
   const Plan p = make_plan(c);
-  return RoutePlan{p.s_shared, p.counts, p.offsets, p.active, p.perm, p.pos, p.rowblocks, p.cta_hist,
-                   p.H};
+  return RoutePlan{p.f8_counters, p.f8_counters_bytes, p.s_shared, p.counts, p.offsets, p.active, p.perm,
+                   p.pos, p.rowblocks, p.cta_hist, p.H};
 }
 
 moe_status_t route_chain(const void* x, const void* W_router, const float* bias,

@@ -66,7 +66,7 @@ MmPlan mm_plan(const moe_fp8_matmul_t& m) {
 // ---------------------------------------------------------------------------
 // layer
 // ---------------------------------------------------------------------------
-// The routing half's view of an 8-bit layer: bf16, the separate kernels.
+// The checks' view of an 8-bit layer's routing half: bf16, the separate kernels.
 moe_cfg_t route_cfg(const moe_cfg_t& c) {
   moe_cfg_t r = c;
   r.expert_dtype = MOE_BF16;
@@ -106,15 +106,17 @@ moe_status_t validate_f8(const moe_cfg_t* c) {
   return MOE_OK;
 }
 
+// Scales of a row of h, routed or shared.
+int h_blocks(const moe_cfg_t& c) { return f8_blocks(c.d_ff > c.d_ff_shared ? c.d_ff : c.d_ff_shared); }
+
 struct F8Plan {
   RoutePlan r;
   int hblocks;
-  size_t counters, counters_bytes, xq, xs, Hf, Hq, Hs, Y, total;
+  size_t xq, xs, Hf, Hq, Hs, Y, total;
 };
 F8Plan f8_plan(const moe_cfg_t& c) {
   F8Plan p{};
-  const moe_cfg_t rc = route_cfg(c);
-  p.r = route_plan(rc);
+  p.r = route_plan(c);
   size_t off = p.r.end;
   auto take = [&](size_t bytes) {
     const size_t o = off;
@@ -122,12 +124,9 @@ F8Plan f8_plan(const moe_cfg_t& c) {
     return o;
   };
   const size_t T = c.T, P = T * c.top_k, d = c.d_model;
-  const int wide = c.d_ff > c.d_ff_shared ? c.d_ff : c.d_ff_shared;
-  p.hblocks = f8_blocks(wide);
+  p.hblocks = h_blocks(c);
   const size_t ldh = (size_t)p.hblocks * kF8Block;
   const bool few = c.T <= kF8FewTokens;
-  p.counters_bytes = few ? (P + 2) * p.hblocks * sizeof(unsigned) : 0;
-  p.counters = take(p.counters_bytes);
   p.xq = take((P + T) * d);
   p.xs = take((P + T) * f8_blocks(c.d_model) * 4);
   p.Hf = take(few ? (P + T) * ldh * 4 : 0);
@@ -190,7 +189,7 @@ moe_status_t enqueue_few(const void* x, const float* r_attn, const int32_t* ids,
   a.Hf = at<float>(c, p.Hf);
   a.Hq = at<uint8_t>(c, p.Hq);
   a.Hs = at<float>(c, p.Hs);
-  a.counters = at<unsigned>(c, p.counters);
+  a.counters = at<unsigned>(c, p.r.f8_counters);
   a.out = out;
   a.ctrl = at<Ctrl>(c, 0);
   a.T = c->T; a.d = c->d_model; a.E = c->n_experts; a.k = c->top_k;
@@ -373,12 +372,17 @@ moe_status_t enqueue_experts(const void* x, const float* r_attn, const int32_t* 
 
 }  // namespace
 
+// A count for every chunk (at most one a pair, and two of the shared expert's)
+// and block of h that a call of the few-token kernels can have.
+size_t f8_counter_bytes(const moe_cfg_t& c) {
+  return ((size_t)kF8FewTokens * c.top_k + 2) * h_blocks(c) * sizeof(unsigned);
+}
+
 cudaError_t f8_reset_counters(const moe_cfg_t& c, cudaStream_t st) {
   if (c.expert_dtype != MOE_F8_E4M3_B128 || validate_f8(&c) != MOE_OK || check_workspace(&c) != MOE_OK)
     return cudaSuccess;
-  const F8Plan p = f8_plan(c);
-  if (!p.counters_bytes) return cudaSuccess;
-  return cudaMemsetAsync(at<char>(&c, p.counters), 0, p.counters_bytes, st);
+  const RoutePlan r = route_plan(c);
+  return cudaMemsetAsync(at<char>(&c, r.f8_counters), 0, r.f8_counters_bytes, st);
 }
 
 }  // namespace moe
@@ -536,8 +540,7 @@ moe_status_t moe_fp8_layer_forward(const void* x, const float* r_attn, const voi
   if (shared && (!w_shared || !aligned(w_shared, 16))) return MOE_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   float* gate = shared ? at<float>(cfg, f8_plan(*cfg).r.s_shared) : nullptr;
-  const moe_cfg_t rc = route_cfg(*cfg);
-  s = route_chain(x, W_router, expert_bias, shared ? w_shared : nullptr, &rc, topk_ids, weights, gate,
+  s = route_chain(x, W_router, expert_bias, shared ? w_shared : nullptr, cfg, topk_ids, weights, gate,
                   st);
   if (s != MOE_OK) return s;
   return enqueue_experts(x, r_attn, topk_ids, weights, gate, b, cfg, out, out_dtype, st);

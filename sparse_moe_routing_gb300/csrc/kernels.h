@@ -363,9 +363,11 @@ cudaError_t run_kernel(int kid, cudaStream_t st, F f) {
 // stall flag of the launch.
 uint64_t launch_wait_limit(int kid, int* stall);
 // Workspace offsets that every layer workspace starts with (routing and
-// bucketing), and their end.
+// bucketing), and their end. The 8-bit layer's item counters, which are zero
+// between calls, come first and are as large for every number of tokens, so that
+// calls of other T that share a workspace neither move nor overwrite them.
 struct RoutePlan {
-  size_t s_shared, counts, offsets, active, perm, pos, rowblocks, cta_hist, end;
+  size_t f8_counters, f8_counters_bytes, s_shared, counts, offsets, active, perm, pos, rowblocks, cta_hist, end;
 };
 RoutePlan route_plan(const moe_cfg_t& c);
 // Routing into ids, weights and s_shared (or null) with the separate routing
@@ -374,6 +376,7 @@ moe_status_t route_chain(const void* x, const void* W_router, const float* bias,
                          const void* w_shared, const moe_cfg_t* c, int32_t* ids, float* w,
                          float* s_shared, cudaStream_t st);
 
+size_t f8_counter_bytes(const moe_cfg_t& c);
 // Zeroes the counters that the 8-bit layer's workspace holds outside its control
 // block; nothing for a workspace of other calls.
 cudaError_t f8_reset_counters(const moe_cfg_t& c, cudaStream_t st);

@@ -240,6 +240,26 @@ def test_linear_reports_a_timeout():
 
 
 # ---------------------------------------------------------------------------
+# one workspace, batches of several sizes
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("shape", ["tiny", "apart", "wide"])
+def test_one_workspace_serves_every_number_of_tokens(shape):
+    """Initialised once for the largest batch, then used for others in turn: bit
+    for bit what a workspace of their own gives."""
+    sizes = (64, 5, 200, 16, 1, 64, 9)
+    ws = smr.fp8_alloc_workspace(config(shape, max(sizes)))
+    for T in sizes:
+        x, ids, alpha, w, gate = make_exact(shape, T)
+        want = smr.Fp8Experts(config(shape, T), w).forward(x, ids, alpha, s_shared=gate)
+        out = torch.empty_like(want)
+        smr.fp8_experts_forward(config(shape, T), ws, x, ids, alpha, w["W_gate"], w["W_up"], w["W_down"], out,
+                                s_shared=gate, Ws_gate=w.get("Ws_gate"), Ws_up=w.get("Ws_up"),
+                                Ws_down=w.get("Ws_down"))
+        assert torch.equal(out, want)
+        assert smr.read_device_status(config(shape, T), ws)[0] == 0
+
+
+# ---------------------------------------------------------------------------
 # after a timeout
 # ---------------------------------------------------------------------------
 @pytest.mark.parametrize("shape,T", [("tiny", 5), ("apart", 16), ("tiny", 40)])

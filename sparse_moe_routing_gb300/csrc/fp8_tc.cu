@@ -55,7 +55,8 @@ constexpr int kPartCols = BN / kParts;    // 64
 // sixteen took 668 on the 8192 x 14336 x 4096 product). Launched with 96
 // registers a thread (61,440 in all); the first warpgroup hands some to the
 // epilogue, which holds 64 fp32 sums and 32 values in flight a thread:
-// 128 x 64 + 512 x 104 = 61,440.
+// 128 x 64 + 512 x 104 = 61,440. (gate/up, at 96, spills one register: 4 bytes
+// stored, 20 loaded.)
 constexpr int kEpiWarp0 = 4;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 

@@ -104,7 +104,10 @@ typedef enum {
    * w = scale * code, scales [E][ceil(N/128)][ceil(K/128)], codes uint8
    * [E][N][K]. Banks of the moe_fp8_* calls only; the other calls answer it
    * with MOE_ERR_INVALID_ARG. */
-  MOE_F8_E4M3_B128 = 3
+  MOE_F8_E4M3_B128 = 3,
+  /* 8-bit integers with one f32 scale per row: w = scale * code. Codes of
+   * moe_add_rmsnorm; no bank or value type. */
+  MOE_I8_ROW = 4
 } moe_dtype_t;
 
 /* Expert-path selection for moe_layer_forward / moe_experts_forward. */
@@ -187,7 +190,10 @@ typedef enum {
   MOE_KERNEL_F8_FEW_DOWN = 15,  /* fp8 down + combine for a few tokens */
   MOE_KERNEL_F8_TC_GATEUP = 16, /* fp8 grouped gate/up + SwiGLU on tcgen05 */
   MOE_KERNEL_F8_TC_DOWN = 17,   /* fp8 grouped down on tcgen05 */
-  MOE_KERNEL_F8_MATMUL = 18     /* fp8 product (few rows, or tcgen05) */
+  MOE_KERNEL_F8_MATMUL = 18,    /* fp8 product (few rows, or tcgen05) */
+  MOE_KERNEL_ADD_RMSNORM = 19,  /* residual add, norm and 8-bit output of rows */
+  MOE_KERNEL_I8_QUANT = 20,     /* int8 quantiser of rows */
+  MOE_KERNEL_I8_MATMUL = 21     /* int8 product, plain or gated (few rows, or tcgen05) */
 } moe_kernel_t;
 
 /* Returns the ABI version (MOE_ROUTE_ABI_VERSION). */
@@ -217,7 +223,8 @@ MOE_API moe_status_t moe_trace_kernel(int kernel, void* const* starts, void* con
 
 /* Failure-detection self-test: the next launch of kernel family `kernel`
  * (MOE_KERNEL_TC_GATEUP, MOE_KERNEL_TC_DOWN, MOE_KERNEL_DECODE,
- * MOE_KERNEL_F8_TC_GATEUP, MOE_KERNEL_F8_TC_DOWN or MOE_KERNEL_F8_MATMUL; the
+ * MOE_KERNEL_F8_TC_GATEUP, MOE_KERNEL_F8_TC_DOWN, MOE_KERNEL_F8_MATMUL or
+ * MOE_KERNEL_I8_MATMUL with more than 8 rows, which up to 8 waits for nothing; the
  * few-token gate/up and down take the stall of the tensor-core ones in whose
  * place they run) waits on a flag that nothing sets, and every bounded wait of that launch gives up
  * after wait_us microseconds instead of about one second. The launch then
@@ -406,6 +413,93 @@ MOE_API moe_status_t moe_fp8_layer_forward(
     moe_bank_t W_gate, moe_bank_t W_up, moe_bank_t W_down, moe_bank_t Ws_gate, moe_bank_t Ws_up,
     moe_bank_t Ws_down, const void* w_shared, const moe_cfg_t* cfg, void* out, int32_t out_dtype,
     int32_t* topk_ids, float* weights, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The norm in front of a layer, and 8-bit integer products: the dense
+ * projections next to the expert layers.
+ *
+ * A matrix in 8-bit integers is codes (int8) and f32 scales, one per row: a
+ * token of activations, an output channel of weights. It stands for
+ * code * scale.
+ * ------------------------------------------------------------------------ */
+
+typedef struct {
+  int32_t T, d;            /* rows >= 0; columns 1..32768 */
+  int32_t x_dtype, residual_dtype, gain_dtype, sum_dtype, out_dtype; /* F32 or BF16 */
+  int32_t codes_dtype;     /* MOE_I8_ROW or MOE_F8_E4M3_B128 */
+  int64_t ldx, ldr, lds, ldo, ldq; /* values between rows of x, residual,
+                                      sum_out, out and codes: >= d */
+  float eps;               /* >= 0 */
+} moe_rmsnorm_t;
+
+/* Residual add and root-mean-square norm of T rows:
+ *   s = x + residual;  t = s * gain;  f = 1 / sqrt(mean(s^2) + eps)
+ *   sum_out = s;  out = t * f;  codes and scales: t * f in 8 bits.
+ * residual, gain [d], sum_out, out and codes with scales may each be NULL (then
+ * their fields of n are ignored), but one output is wanted; the norm is of the
+ * f32 sum, not of its rounding to sum_out's type. 8 bits: the codes are those
+ * of t, and f goes into the scales, so that no code depends on the order in
+ * which the squares are summed:
+ *   MOE_I8_ROW        as moe_i8_quantize's of t; scales [T], each times f;
+ *   MOE_F8_E4M3_B128  as moe_fp8_quantize's of t with block_rows 1; scales
+ *                     [T][ceil(d/128)], each times f.
+ * s, t and the sum of squares are f32 (rows with |s| above 1e19 overflow it: f
+ * is 0). A row that holds an infinity or a NaN is NaN or 0 throughout; its int8
+ * scale is NaN and its codes 0. sum_out and out may each be x or residual with
+ * the same type and row pitch; nothing else may overlap. Tensors need the
+ * alignment of their element; 16-byte aligned rows are read and written in wide
+ * pieces. Deterministic. */
+MOE_API moe_status_t moe_add_rmsnorm(const moe_rmsnorm_t* n, const void* x, const void* residual,
+                                     const void* gain, void* sum_out, void* out, void* codes,
+                                     float* scales, void* stream);
+
+/* Quantises rows of x (F32 or BF16, the first `cols` of every ldx values) into
+ * int8 codes in [-127, 127] and a scale per row: with m = max(max |x|,
+ * 127 * 2^-126), code = rint(x * (127 / m)) to nearest even and scale = m / 127,
+ * each step in f32 (code * scale is within 0.5000001 scales of x). A row with
+ * a value that is not finite gets the scale NaN and codes 0. Codes past a row's
+ * last column are not written. cols 1..32768. */
+MOE_API moe_status_t moe_i8_quantize(const void* x, int32_t x_dtype, int64_t ldx, int32_t rows,
+                                     int32_t cols, void* codes, int64_t ldq, float* scales,
+                                     void* stream);
+
+typedef struct {
+  int32_t M, N, K;       /* M, N >= 0; K 1..131071 */
+  int32_t out_dtype;     /* MOE_BF16 or MOE_F32 */
+  int32_t gated;         /* 0: moe_i8_matmul, 1: moe_i8_gated_matmul */
+  int64_t lda, ldb;      /* codes between rows of a and of b (or gate and up):
+                            >= K, multiples of 16 */
+  int64_t ldo;           /* values between rows of out: >= N */
+  void* workspace;       /* device scratch, >= moe_i8_matmul_workspace_bytes */
+  size_t workspace_bytes;
+} moe_i8_matmul_t;
+
+/* out [M][N] = (a b^T) * a_scale[m] * b_scale[n], int8 codes a [M][K] (any in
+ * -128..127) with scales [M], b [N][K] with scales [N]. The sum of products is
+ * exact; it is rounded to f32, multiplied by a_scale, then by b_scale, and
+ * rounded once to out_dtype. a and b 16-byte aligned, out aligned to its
+ * element; the bytes between a row's K codes and the next row are not read as
+ * codes. Up to 8 rows stream b on mma.sync; more run on tcgen05, widened
+ * to fp16, which holds codes and their sums over 1024 exactly. M or N of 0
+ * enqueues nothing. Deterministic, and the same for a row whatever M is. */
+MOE_API moe_status_t moe_i8_matmul(const void* a, const float* a_scale, const void* b,
+                                   const float* b_scale, const moe_i8_matmul_t* mm, void* out,
+                                   void* stream);
+
+/* out [M][N] = SiLU(g) * u, g and u the products of a with gate and with up
+ * [N][K] as above, both in f32; ldb is both matrices' pitch. */
+MOE_API moe_status_t moe_i8_gated_matmul(const void* a, const float* a_scale, const void* gate,
+                                         const float* gate_scale, const void* up,
+                                         const float* up_scale, const moe_i8_matmul_t* mm, void* out,
+                                         void* stream);
+
+/* Workspace bytes of a product (0 if mm is invalid; mm's workspace fields are
+ * ignored) and its initialisation, as for moe_fp8_matmul: one workspace serves
+ * any product, plain or gated, that it is large enough for; its status is
+ * read with moe_read_device_status for a moe_cfg_t with these workspace
+ * fields. */
+MOE_API size_t moe_i8_matmul_workspace_bytes(const moe_i8_matmul_t* mm);
+MOE_API moe_status_t moe_i8_matmul_init(const moe_i8_matmul_t* mm, void* stream);
 
 #ifdef __cplusplus
 }

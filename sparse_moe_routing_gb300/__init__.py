@@ -20,14 +20,16 @@ __all__ = [
     "F32", "BF16", "Q4_AFFINE_G64", "PATH_AUTO", "PATH_GEMV", "PATH_TC", "PATH_FUSED",
     "inject_stall", "F8_E4M3_B128", "fp8_empty", "fp8_quantize", "fp8_matmul",
     "fp8_matmul_workspace", "fp8_workspace_bytes", "fp8_alloc_workspace", "fp8_experts_forward",
-    "fp8_layer_forward", "Fp8Experts", "Fp8Linear",
+    "fp8_layer_forward", "Fp8Experts", "Fp8Linear", "I8_ROW", "add_rmsnorm", "int8_empty",
+    "int8_quantize", "int8_matmul_workspace", "int8_matmul", "int8_gated_matmul", "Int8Linear",
+    "Int8FeedForward",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_PKG, "libmoe_route.so")
 
 SOFTMAX_TOPK, SIGMOID_GROUP_TOPK = 0, 1
-F32, BF16, Q4_AFFINE_G64, F8_E4M3_B128 = 0, 1, 2, 3
+F32, BF16, Q4_AFFINE_G64, F8_E4M3_B128, I8_ROW = 0, 1, 2, 3, 4
 PATH_AUTO, PATH_GEMV, PATH_TC, PATH_FUSED = 0, 1, 2, 3
 _STATUS = ["MOE_OK", "MOE_ERR_INVALID_ARG", "MOE_ERR_UNSUPPORTED", "MOE_ERR_WORKSPACE",
            "MOE_ERR_CUDA", "MOE_ERR_DEVICE_TIMEOUT", "MOE_ERR_DEVICE_CHECK"]
@@ -67,6 +69,19 @@ class _Fp8Matmul(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
+class _RmsNorm(ctypes.Structure):
+    _fields_ = ([(f, ctypes.c_int32) for f in ("T", "d", "x_dtype", "residual_dtype", "gain_dtype", "sum_dtype",
+                                               "out_dtype", "codes_dtype")]
+                + [(f, ctypes.c_int64) for f in ("ldx", "ldr", "lds", "ldo", "ldq")] + [("eps", ctypes.c_float)])
+
+
+class _I8Matmul(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("gated", ctypes.c_int32), ("lda", ctypes.c_int64),
+                ("ldb", ctypes.c_int64), ("ldo", ctypes.c_int64), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
 _P = ctypes.c_void_p
 _SIGS = {
     "moe_abi_version": (ctypes.c_int, []),
@@ -97,6 +112,13 @@ _SIGS = {
         _P, ctypes.POINTER(_Cfg), _P, ctypes.c_int32, _P]),
     "moe_fp8_layer_forward": (ctypes.c_int, [_P] * 4 + [_Bank] * 6 + [
         _P, ctypes.POINTER(_Cfg), _P, ctypes.c_int32, _P, _P, _P]),
+    "moe_add_rmsnorm": (ctypes.c_int, [ctypes.POINTER(_RmsNorm)] + [_P] * 8),
+    "moe_i8_quantize": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _P,
+                                       ctypes.c_int64, _P, _P]),
+    "moe_i8_matmul_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(_I8Matmul)]),
+    "moe_i8_matmul_init": (ctypes.c_int, [ctypes.POINTER(_I8Matmul), _P]),
+    "moe_i8_matmul": (ctypes.c_int, [_P] * 4 + [ctypes.POINTER(_I8Matmul), _P, _P]),
+    "moe_i8_gated_matmul": (ctypes.c_int, [_P] * 6 + [ctypes.POINTER(_I8Matmul), _P, _P]),
 }
 
 # kernel families (moe_kernel_t)
@@ -104,7 +126,7 @@ KERNELS = {"router_logits": 1, "router_topk": 2, "shared_gate": 3, "bucket": 4,
            "gemv_gateup": 5, "gemv_down": 6, "combine": 7, "tc_gateup": 8, "tc_down": 9,
            "gather": 10, "tc_router": 11, "decode_fused": 12, "f8_quant": 13,
            "f8_few_gateup": 14, "f8_few_down": 15, "f8_tc_gateup": 16, "f8_tc_down": 17,
-           "f8_matmul": 18}
+           "f8_matmul": 18, "add_rmsnorm": 19, "i8_quant": 20, "i8_matmul": 21}
 
 _lib = None
 
@@ -279,8 +301,8 @@ def layer_forward(cfg, workspace, x, r_attn, W_router, W_gate, W_up, W_down, out
 
 def inject_stall(kernel: str, wait_us: int):
     """Failure self-test (moe_inject_stall): the next launch of `kernel`
-    ("tc_gateup", "tc_down", "decode_fused", "f8_tc_gateup", "f8_tc_down" or
-    "f8_matmul") waits on a flag nothing sets and gives up after wait_us; None
+    ("tc_gateup", "tc_down", "decode_fused", "f8_tc_gateup", "f8_tc_down",
+    "f8_matmul" or "i8_matmul") waits on a flag nothing sets and gives up after wait_us; None
     disarms."""
     _check(lib().moe_inject_stall(0 if kernel is None else KERNELS[kernel], int(wait_us)),
            "moe_inject_stall")
@@ -704,3 +726,280 @@ class Fp8Experts:
 
     def device_status(self, stream=None):
         return read_device_status(self.cfg, self.ws, stream)
+
+
+# ---------------------------------------------------------------------------
+# the norm in front of a layer, and 8-bit integers: codes and one fp32 scale per row
+# ---------------------------------------------------------------------------
+_current_device = None
+
+
+def _on_device(*tensors):
+    """All tensors (None: not given) on the current CUDA device."""
+    global _current_device
+    if _current_device is None:
+        import torch
+        torch.cuda.init()
+        _current_device = torch.cuda.current_device
+    want = _current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != want:
+            raise ValueError("tensors must be on the current CUDA device (%d), got one on %s" % (want, t.device))
+
+
+def _rows_of(t, name):
+    """Values between the rows of a matrix with contiguous rows; the row length where there is one row."""
+    r, c = t.shape
+    s0, s1 = t.stride()
+    if s1 != 1 and c > 1:
+        raise ValueError("%s must have contiguous rows" % name)
+    return s0 if r > 1 else max(s0, c)
+
+
+def _vector(t, n, name):
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError("%s must be a contiguous vector of %d values, got shape %s" % (name, n, tuple(t.shape)))
+
+
+_int8 = None
+
+
+def _i8_type(t):
+    global _int8
+    if _int8 is None:
+        import torch
+        _int8 = torch.int8
+    return t.dtype == _int8
+
+
+def _i8_codes(t, name):
+    if t.dim() != 2 or not _i8_type(t):
+        raise ValueError("%s must be an int8 matrix" % name)
+
+
+def add_rmsnorm(x, residual=None, gain=None, eps=1e-6, out=None, sum_out=None, codes=None, scales=None, stream=None):
+    """moe_add_rmsnorm: s = x + residual, out = s * gain / sqrt(mean(s^2) + eps) of rows x [T, d].
+
+    Writes what is given: sum_out (s) and out, float32 or bfloat16 [T, d], and the result in 8 bits: codes int8 [T, d]
+    with scales [T], or codes float8_e4m3fn with scales [T, ceil(d / 128)] (int8_empty, fp8_empty make either). sum_out
+    and out may be x or residual themselves."""
+    if x.dim() != 2:
+        raise ValueError("x must have two dimensions")
+    T, d = shape = x.shape
+    n = _RmsNorm(T, d, _dtype_of(x))
+    n.ldx = _rows_of(x, "x")
+    n.eps = eps
+    pr = pg = ps = po = pq = pc = None
+    if residual is not None:
+        _shape_is(residual, shape, "residual")
+        n.residual_dtype, n.ldr, pr = _dtype_of(residual), _rows_of(residual, "residual"), residual.data_ptr()
+    if gain is not None:
+        _vector(gain, d, "gain")
+        n.gain_dtype, pg = _dtype_of(gain), gain.data_ptr()
+    if sum_out is not None:
+        _shape_is(sum_out, shape, "sum_out")
+        n.sum_dtype, n.lds, ps = _dtype_of(sum_out), _rows_of(sum_out, "sum_out"), sum_out.data_ptr()
+    if out is not None:
+        _shape_is(out, shape, "out")
+        n.out_dtype, n.ldo, po = _dtype_of(out), _rows_of(out, "out"), out.data_ptr()
+    if (codes is None) != (scales is None):
+        raise ValueError("codes and scales belong together")
+    if codes is not None:
+        _shape_is(codes, shape, "codes")
+        if _i8_type(codes):
+            n.codes_dtype = I8_ROW
+            _scales_ok(scales, (T,), "scales")
+        else:
+            _codes_dtype(codes, "codes")
+            n.codes_dtype = F8_E4M3_B128
+            _scales_ok(scales, (T, -(-d // 128)), "scales")
+        if not scales.is_contiguous():
+            raise ValueError("scales must be contiguous")
+        n.ldq, pq, pc = _rows_of(codes, "codes"), codes.data_ptr(), scales.data_ptr()
+    _on_device(x, residual, gain, sum_out, out, codes, scales)
+    _check(lib().moe_add_rmsnorm(n, x.data_ptr(), pr, pg, ps, po, pq, pc, _stream(stream)), "moe_add_rmsnorm")
+
+
+def int8_empty(rows, cols, device=None):
+    """(codes, scales) tensors for a rows x cols matrix: codes' rows are padded to 16 bytes, as the products take
+    them."""
+    import torch
+    codes = torch.empty((rows, -(-cols // 16) * 16), dtype=torch.int8, device=device or "cuda")
+    return codes[:, :cols], torch.empty(rows, dtype=torch.float32, device=device or "cuda")
+
+
+def int8_quantize(x, codes, scales, stream=None):
+    """moe_i8_quantize: rows of x [rows, cols] (float32 or bfloat16) into int8 codes and scales [rows]."""
+    if x.dim() != 2:
+        raise ValueError("x must have two dimensions")
+    rows, cols = x.shape
+    _i8_codes(codes, "codes")
+    _shape_is(codes, x.shape, "codes")
+    _scales_ok(scales, (rows,), "scales")
+    _vector(scales, rows, "scales")
+    dtype, ldx, ldq = _dtype_of(x), _rows_of(x, "x"), _rows_of(codes, "codes")
+    _on_device(x, codes, scales)
+    _check(lib().moe_i8_quantize(x.data_ptr(), dtype, ldx, rows, cols, codes.data_ptr(), ldq, scales.data_ptr(),
+                                 _stream(stream)), "moe_i8_quantize")
+
+
+def _i8_args(M, N, K, gated=False, out_dtype=BF16, lda=0, ldb=0, ldo=0, workspace=None):
+    p = -(-max(K, 1) // 16) * 16
+    m = _I8Matmul(M, N, K, out_dtype, 1 if gated else 0, lda or p, ldb or p, ldo or N, None, 0)
+    if workspace is not None:
+        m.workspace = workspace.data_ptr()
+        m.workspace_bytes = workspace.numel() * workspace.element_size()
+    return m
+
+
+def _i8_workspace_bytes(M, N, K, gated):
+    n = lib().moe_i8_matmul_workspace_bytes(ctypes.byref(_i8_args(M, N, K, gated)))
+    if n == 0:
+        raise MoEError(1, "moe_i8_matmul_workspace_bytes")
+    return n
+
+
+def int8_matmul_workspace(M, N, K, gated=False, device=None, stream=None):
+    """Allocates (with torch) and initialises the workspace of an M x N x K product (gated: of int8_gated_matmul) on
+    `stream`. It serves other products too, where it is large enough."""
+    import torch
+    ws = _empty(_i8_workspace_bytes(M, N, K, gated), torch.uint8, device, stream)
+    _check(lib().moe_i8_matmul_init(ctypes.byref(_i8_args(M, N, K, gated, workspace=ws)), _stream(stream)),
+           "moe_i8_matmul_init")
+    return ws
+
+
+def _i8_product(a, a_scale, weights, out, workspace, stream):
+    """(arguments, structure, result, stream) of a product with one or two (codes, scale) weights."""
+    _i8_codes(a, "a")
+    M, K = a.shape
+    pitches = []
+    args = [a.data_ptr(), a_scale.data_ptr()]
+    for name, b, b_scale in weights:
+        _i8_codes(b, name)
+        N = weights[0][1].shape[0]
+        _shape_is(b, (N, K), name)
+        _scales_ok(b_scale, (N,), name + "_scale")
+        _vector(b_scale, N, name + "_scale")
+        pitches.append(_rows_of(b, name))
+        args += [b.data_ptr(), b_scale.data_ptr()]
+    if pitches[-1] != pitches[0]:
+        raise ValueError("gate and up must have the same row pitch")
+    _scales_ok(a_scale, (M,), "a_scale")
+    _vector(a_scale, M, "a_scale")
+    _shape_is(out, (M, N), "out")
+    m = _I8Matmul(M, N, K, _dtype_of(out), len(weights) - 1, _rows_of(a, "a"), pitches[0], _rows_of(out, "out"),
+                  workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _on_device(a, a_scale, out, workspace, *(t for w in weights for t in w[1:]))
+    return args, m, out.data_ptr(), _stream(stream)
+
+
+def int8_matmul(a, a_scale, b, b_scale, out, workspace, stream=None):
+    """moe_i8_matmul: out [M, N] = (a [M, K] b [N, K]^T) a_scale [M] b_scale [N], int8 codes, the sum exact; out float32
+    or bfloat16. K at most 131071."""
+    args, m, p, st = _i8_product(a, a_scale, [("b", b, b_scale)], out, workspace, stream)
+    _check(lib().moe_i8_matmul(*args, m, p, st), "moe_i8_matmul")
+
+
+def int8_gated_matmul(a, a_scale, gate, gate_scale, up, up_scale, out, workspace, stream=None):
+    """moe_i8_gated_matmul: out [M, N] = SiLU(g) * u, g and u the products of a with gate and up [N, K] as by
+    int8_matmul, in fp32."""
+    args, m, p, st = _i8_product(a, a_scale, [("gate", gate, gate_scale), ("up", up, up_scale)], out, workspace, stream)
+    _check(lib().moe_i8_gated_matmul(*args, m, p, st), "moe_i8_gated_matmul")
+
+
+def _i8_most(max_rows, N, K, gated):
+    """Rows, at most max_rows, whose product needs the most workspace. What it needs grows with the rows but for the
+    split's sums, which fewer tiles need more of, and which end with 76 tiles of 128 rows."""
+    some = {max_rows, *(r for r in (16, 32, 64) if r < max_rows), *range(128, min(max_rows, 76 * 128) + 1, 128)}
+    return max(some, key=lambda M: _i8_workspace_bytes(M, N, K, gated))
+
+
+class _Int8Weight:
+    """A weight [N, K] (float32 or bfloat16) in 8-bit integers with a scale per row."""
+
+    def __init__(self, weight):
+        self.N, self.K = weight.shape
+        self.codes, self.scale = int8_empty(self.N, self.K, weight.device)
+        int8_quantize(weight, self.codes, self.scale)
+
+
+class Int8Linear:
+    """y = x W^T with W [N, K] held in 8-bit integers, for up to max_rows rows: x quantised on the way, or given as
+    (codes, scales), as add_rmsnorm and int8_quantize write them. The quantised x and the workspace belong to the
+    object: calls on several streams are ordered by the caller."""
+
+    def __init__(self, weight, max_rows, device=None):
+        if device is not None:
+            weight = weight.to(device)
+        self.w = _Int8Weight(weight)
+        self.N, self.K, self.max_rows = self.w.N, self.w.K, max_rows
+        self.x, self.x_scales = int8_empty(max_rows, self.K, weight.device)
+        self.ws = int8_matmul_workspace(_i8_most(max_rows, self.N, self.K, False), self.N, self.K, device=weight.device)
+
+    def __call__(self, x, out, stream=None):
+        quantised = isinstance(x, tuple)
+        M = (x[0] if quantised else x).shape[0]
+        if M > self.max_rows:
+            raise ValueError("x has %d rows, made for %d" % (M, self.max_rows))
+        if quantised:
+            codes, scales = x
+        else:
+            codes, scales = self.x[:M], self.x_scales[:M]
+            int8_quantize(x, codes, scales, stream)
+        int8_matmul(codes, scales, self.w.codes, self.w.scale, out, self.ws, stream)
+        return out
+
+    def device_status(self, stream=None):
+        """(status, raw word) of the products since the last call, as read_device_status."""
+        return read_device_status(MoEConfig(T=1, d_model=128, n_experts=1, top_k=1, d_ff=128), self.ws, stream)
+
+
+class Int8FeedForward:
+    """The dense feed-forward block of a layer without experts, in 8-bit integers: y = W_down h,
+    h = SiLU(W_gate x) * (W_up x), for up to max_rows rows. W_gate, W_up [I, d] and W_down [d, I] float32 or bfloat16.
+
+    x is quantised on the way, or given as (codes, scales), as add_rmsnorm writes them; h is rounded to bfloat16 and
+    then to 8 bits with a scale per row (the bfloat16 rounding is 1/2^9 of a value, a step of the codes 1/127 of the
+    row's largest). The workspace and what lies between the products belong to the object: calls on several streams
+    are ordered by the caller."""
+
+    def __init__(self, W_gate, W_up, W_down, max_rows, device=None):
+        import torch
+        if device is not None:
+            W_gate, W_up, W_down = W_gate.to(device), W_up.to(device), W_down.to(device)
+        self.I, self.d = W_gate.shape
+        _shape_is(W_up, (self.I, self.d), "W_up")
+        _shape_is(W_down, (self.d, self.I), "W_down")
+        at = W_gate.device
+        self.max_rows = max_rows
+        self.gate, self.up, self.down = _Int8Weight(W_gate), _Int8Weight(W_up), _Int8Weight(W_down)
+        self.x, self.x_scales = int8_empty(max_rows, self.d, at)
+        self.h = torch.empty((max_rows, self.I), dtype=torch.bfloat16, device=at)
+        self.hq, self.h_scales = int8_empty(max_rows, self.I, at)
+        shapes = [(_i8_most(max_rows, N, K, g), N, K, g) for N, K, g in ((self.I, self.d, True), (self.d, self.I, False))]
+        M, N, K, g = max(shapes, key=lambda s: _i8_workspace_bytes(*s))
+        self.ws = int8_matmul_workspace(M, N, K, gated=g, device=at)
+
+    def __call__(self, x, out, stream=None):
+        quantised = isinstance(x, tuple)
+        M = (x[0] if quantised else x).shape[0]
+        if M > self.max_rows:
+            raise ValueError("x has %d rows, made for %d" % (M, self.max_rows))
+        if quantised:
+            codes, scales = x
+        else:
+            codes, scales = self.x[:M], self.x_scales[:M]
+            int8_quantize(x, codes, scales, stream)
+        h, hq, hs = self.h[:M], self.hq[:M], self.h_scales[:M]
+        int8_gated_matmul(codes, scales, self.gate.codes, self.gate.scale, self.up.codes, self.up.scale, h, self.ws,
+                          stream)
+        int8_quantize(h, hq, hs, stream)
+        int8_matmul(hq, hs, self.down.codes, self.down.scale, out, self.ws, stream)
+        return out
+
+    def device_status(self, stream=None):
+        """(status, raw word) of the products since the last call, as read_device_status."""
+        return read_device_status(MoEConfig(T=1, d_model=128, n_experts=1, top_k=1, d_ff=128), self.ws, stream)

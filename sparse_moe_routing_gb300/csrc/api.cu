@@ -295,6 +295,9 @@ const char* kernel_name(int kid) {
     case MOE_KERNEL_F8_TC_GATEUP: return "moe:f8_tc_gateup";
     case MOE_KERNEL_F8_TC_DOWN: return "moe:f8_tc_down";
     case MOE_KERNEL_F8_MATMUL: return "moe:f8_matmul";
+    case MOE_KERNEL_ADD_RMSNORM: return "moe:add_rmsnorm";
+    case MOE_KERNEL_I8_QUANT: return "moe:i8_quant";
+    case MOE_KERNEL_I8_MATMUL: return "moe:i8_matmul";
   }
   return "moe:kernel";
 }
@@ -764,7 +767,7 @@ moe_status_t moe_trace_kernel(int kernel, void* const* starts, void* const* stop
     g_trace = TraceState{};
     return MOE_OK;
   }
-  if (kernel < MOE_KERNEL_ROUTER_LOGITS || kernel > MOE_KERNEL_F8_MATMUL || n <= 0 || !starts ||
+  if (kernel < MOE_KERNEL_ROUTER_LOGITS || kernel > MOE_KERNEL_I8_MATMUL || n <= 0 || !starts ||
       !stops || !count)
     return MOE_ERR_INVALID_ARG;
   g_trace.kernel = kernel;
@@ -783,7 +786,8 @@ moe_status_t moe_inject_stall(int kernel, uint32_t wait_us) {
   }
   if (kernel != MOE_KERNEL_TC_GATEUP && kernel != MOE_KERNEL_TC_DOWN &&
       kernel != MOE_KERNEL_DECODE && kernel != MOE_KERNEL_F8_TC_GATEUP &&
-      kernel != MOE_KERNEL_F8_TC_DOWN && kernel != MOE_KERNEL_F8_MATMUL)
+      kernel != MOE_KERNEL_F8_TC_DOWN && kernel != MOE_KERNEL_F8_MATMUL &&
+      kernel != MOE_KERNEL_I8_MATMUL)
     return MOE_ERR_INVALID_ARG;
   g_stall_wait_ns.store((uint64_t)(wait_us ? wait_us : 1) * 1000ull);
   g_stall_kernel.store(kernel);

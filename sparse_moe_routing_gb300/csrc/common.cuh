@@ -29,6 +29,7 @@ enum : uint32_t {
   kSiteDecode = 9,
   kSiteFewFp8 = 10,
   kSiteTcFp8 = 11,
+  kSiteTcI8 = 12,
 };
 
 struct Ctrl {

@@ -308,6 +308,73 @@ cudaError_t launch_f8_tc(int mode, const F8TcMaps& m, const F8TcArgs& a, int max
 // Adds a dense product's partial sums (ksplit > 1) into its output.
 cudaError_t launch_f8_split_sum(const F8TcArgs& a, cudaStream_t st);
 
+// Rows: norm with the residual's addition, and 8-bit output (norm_quant.cu).
+enum RowsCodes { kRowsNone = 0, kRowsInt8 = 1, kRowsE4m3 = 2 };
+constexpr int kRowsMaxCols = 32768;  // 512 threads of 64 values
+struct RowsArgs {
+  const void* x;         // [rows][ldx]
+  const void* residual;  // [rows][ldr] or null
+  const void* gain;      // [cols] or null
+  void* sum;             // [rows][lds] or null
+  void* out;             // [rows][ldo] or null
+  uint8_t* codes;        // [rows][ldq] or null
+  float* scales;         // int8: [rows]; e4m3: [rows][column blocks]
+  long long ldx, ldr, lds, ldo, ldq;
+  int rows, cols;
+  int norm, kind;        // kind: RowsCodes; e4m3 with norm only
+  int x_bf16, res_bf16, gain_bf16, sum_bf16, out_bf16;
+  int warp_rows;         // set by the launcher
+  float eps;
+};
+cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st);
+
+// 8-bit integer products (i8_few.cu, i8_tc.cu).
+constexpr int kI8FewRows = 8;
+constexpr int kI8MaxK = 131071;  // 2^14 a product: the sums stay below 2^31
+struct I8FewArgs {
+  const uint8_t* a;                  // [M][lda]
+  const uint8_t *b0, *b1;            // [N][ldb]; b1: up (gated)
+  const float *a_scale, *b_scale0, *b_scale1;
+  void* out;                         // [M][ldo]
+  int M, N, K, out_bf16;
+  long long lda, ldb, ldo;
+  int ks;                            // set by the launcher
+};
+cudaError_t launch_i8_few(I8FewArgs a, bool gated, cudaStream_t st);
+
+// Rows of codes as fp16 values [rows][pitch], pitch = cols rounded up to 16.
+struct I8WidenArgs {
+  const uint8_t* a;  // [rows][lda]
+  void* out;
+  int rows, cols, pitch;
+  long long lda;
+};
+cudaError_t launch_i8_widen(const I8WidenArgs& a, cudaStream_t st);
+
+// Forms of the tensor-core product: a tile is 128 columns of the result by one
+// or two blocks of `half` rows, or the gate and up products of one block.
+enum I8Kind { kI8One = 0, kI8Two = 1, kI8Gated = 2 };
+struct I8TcArgs {
+  const float *a_scale, *b_scale0, *b_scale1;
+  void* out;
+  int* partial;        // ksplit > 1: [ksplit][tiles][accumulators][half][128]
+  Ctrl* ctrl;
+  int M, N, steps;     // steps: blocks of 128 k
+  int m_tiles, n_tiles, ksplit, out_bf16;
+  long long ldo;
+  uint64_t wait_ns;
+  int stall;
+};
+struct I8TcMaps {
+  CUtensorMap A, B0, B1;
+};
+// Map of fp16 rows [rows][cols], `pitch` values apart, box 64 x box_rows.
+bool i8_make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t pitch,
+                 uint32_t box_rows);
+cudaError_t launch_i8_tc(I8Kind kind, int half, const I8TcMaps& m, const I8TcArgs& a, cudaStream_t st);
+// Adds the splits' sums of a product (ksplit > 1) and finishes them.
+cudaError_t launch_i8_split_sum(I8Kind kind, int half, const I8TcArgs& a, cudaStream_t st);
+
 // Raises `kernel`'s dynamic shared-memory opt-in limit to at least `bytes`
 // on the current device; `limits` holds the value set so far per device
 // ordinal (< 64), so the attribute is only set when a launch needs more.

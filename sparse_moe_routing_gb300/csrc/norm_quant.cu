@@ -1,0 +1,330 @@
+// Rows: root-mean-square norm with the residual's addition, and 8-bit output.
+//
+//   s = x + r,  t = s * gain,  f = 1 / sqrt(mean(s^2) + eps),  out = t * f
+//
+// and, in 8 bits, codes of t with a scale that takes the factor f:
+//   integers  m = max(max |t|, 127 * 2^-126): code = rint(t * (127 / m)), scale = (m / 127) * f, one per row;
+//   e4m3      p = the smallest power of two >= 2^-126 with max |t| / p <= 448: code = e4m3(t / p),
+//             scale = p * f, one per 1 x 128 block.
+// A row's factor is the same for all of its values, so that taking it into the
+// scale changes nothing but the roundings: s, t and t * (127 / m) are rounded
+// once each whatever order the squares are summed in (codes do not depend on
+// it), and the largest magnitude needs no second pass behind the sum: one
+// reduction serves both. The integer quantiser of plain rows is the same kernel
+// without norm (f = 1, t = x).
+//
+// A row belongs to a group of threads (a warp where it has at most 1024
+// columns, a CTA else) and stays in its registers: x and the residual are read
+// once, everything is written once. Bound by HBM for many rows, by latency for
+// few (a load, one reduction, a store).
+//
+// Rows that are not finite: the norm of a row with an infinity or a NaN is NaN
+// there and 0 or NaN elsewhere; an integer row gets the scale NaN and codes 0, an
+// e4m3 block the scale NaN and NaN codes.
+#include "fp8_common.cuh"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+// Threads of a CTA at most: as many as keep a row's values in registers.
+constexpr int max_threads(int ch) { return ch <= 2 ? 1024 : 512; }
+constexpr int kWarpRows = 8;  // rows per CTA where a warp has one
+
+// Plain loads: the residual may be the sum's own place.
+__device__ __forceinline__ uint4 ld16(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
+// The eight values of a lane in piece `piece` of its row. VEC: eight
+// consecutive columns, 16 lanes a block of 128. Otherwise lane + 32 j of a
+// warp's 256 columns: accesses of a warp stay side by side whatever the row's
+// start and length, and a block of 128 is the whole warp's four values.
+template <bool VEC>
+__device__ __forceinline__ int col_of(int unit, int lane, int j) {
+  return VEC ? (unit * 32 + lane) * 8 + j : unit * 256 + j * 32 + lane;
+}
+
+template <typename T>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = ld16(p); }
+  __device__ __forceinline__ void values(float (&o)[8]) const { Chunk<__nv_bfloat16>::unpack(v, o); }
+};
+template <>
+struct Raw<float> {
+  uint4 v[2];
+  __device__ __forceinline__ void load(const float* p) {
+    v[0] = ld16(p);
+    v[1] = ld16(p + 4);
+  }
+  __device__ __forceinline__ void values(float (&o)[8]) const {
+    Chunk<float>::unpack(v[0], o);
+    Chunk<float>::unpack(v[1], o + 4);
+  }
+};
+
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// Loads the CH pieces of a row into v (zeros past its end).
+template <typename T, bool VEC, int CH>
+__device__ __forceinline__ void load_row(const T* row, int unit0, int units, int lane, int cols,
+                                         float (&v)[CH][8]) {
+  if (VEC) {
+    Raw<T> raw[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int col = col_of<true>(unit0 + c * units, lane, 0);
+      if (col < cols) raw[c].load(row + col);
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      if (col_of<true>(unit0 + c * units, lane, 0) < cols) {
+        raw[c].values(v[c]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[c][j] = 0.f;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int col = col_of<false>(unit0 + c * units, lane, j);
+        v[c][j] = col < cols ? widen(row[col]) : 0.f;
+      }
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store_values(void* base, long long at, bool bf16, int unit, int lane,
+                                             int cols, const float (&v)[8]) {
+  if (VEC) {
+    const int col = col_of<true>(unit, lane, 0);
+    if (col >= cols) return;
+    if (bf16) {
+      tc::st_global_v4(static_cast<__nv_bfloat16*>(base) + at + col, pack_bf16x2(v[0], v[1]),
+                       pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    } else {
+      float* p = static_cast<float*>(base) + at + col;
+      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = col_of<false>(unit, lane, j);
+      if (col >= cols) continue;
+      if (bf16)
+        static_cast<__nv_bfloat16*>(base)[at + col] = __float2bfloat16_rn(v[j]);
+      else
+        static_cast<float*>(base)[at + col] = v[j];
+    }
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store_codes(uint8_t* row, int unit, int lane, int cols, uint2 q) {
+  if (VEC) {
+    const int col = col_of<true>(unit, lane, 0);
+    if (col < cols) *reinterpret_cast<uint2*>(row + col) = q;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = col_of<false>(unit, lane, j);
+      if (col < cols) row[col] = (uint8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+    }
+  }
+}
+
+// rint(v * inv) of four values as bytes, |v * inv| <= 127 (1 + 2^-23): adding
+// 1.5 * 2^23 rounds to a whole number, to nearest even, and leaves it in the low
+// bits. The product is rounded by itself (no fma).
+__device__ __forceinline__ uint32_t int8x4(const float* v, float inv) {
+  uint32_t b[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) b[j] = __float_as_uint(__fadd_rn(__fmul_rn(v[j], inv), 12582912.f));
+  return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+}
+
+constexpr float kLeastMax = 127.f * 1.17549435e-38f;  // 127 * 2^-126, an fp32 number
+
+// TX: x's type. RES: 0 no residual, 1 fp32, 2 bf16. NORM: with the factor f (and
+// gain, sum, values); else the integer quantiser alone. CH pieces of eight
+// values a thread. A CTA has one row, or one per warp where a.warp_rows.
+template <typename TX, int RES, bool NORM, bool VEC, int CH>
+__global__ void __launch_bounds__(max_threads(CH)) rows_kernel(RowsArgs a) {
+  __shared__ float s_sum[32];
+  __shared__ uint32_t s_max[32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int units = a.warp_rows ? 1 : blockDim.x >> 5;  // warps of a row
+  const int unit0 = a.warp_rows ? 0 : warp;
+  const long long row = a.warp_rows ? (long long)blockIdx.x * kWarpRows + warp : blockIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  if (row >= a.rows) return;  // (whole warps, and only where no barrier follows)
+
+  float t[CH][8];
+  load_row<TX, VEC, CH>(static_cast<const TX*>(a.x) + row * a.ldx, unit0, units, lane, a.cols, t);
+  if (NORM && RES != 0) {
+    float r[CH][8];
+    if (RES == 1)
+      load_row<float, VEC, CH>(static_cast<const float*>(a.residual) + row * a.ldr, unit0, units, lane, a.cols, r);
+    else
+      load_row<__nv_bfloat16, VEC, CH>(static_cast<const __nv_bfloat16*>(a.residual) + row * a.ldr, unit0, units,
+                                       lane, a.cols, r);
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[c][j] += r[c][j];
+  }
+  float sum = 0.f;
+  if (NORM) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      if (a.sum) store_values<VEC>(a.sum, row * a.lds, a.sum_bf16, unit0 + c * units, lane, a.cols, t[c]);
+      float q = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q = fmaf(t[c][j], t[c][j], q);
+      sum += q;
+    }
+    if (a.gain) {
+      float g[CH][8];
+      if (a.gain_bf16)
+        load_row<__nv_bfloat16, VEC, CH>(static_cast<const __nv_bfloat16*>(a.gain), unit0, units, lane, a.cols, g);
+      else
+        load_row<float, VEC, CH>(static_cast<const float*>(a.gain), unit0, units, lane, a.cols, g);
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[c][j] = __fmul_rn(t[c][j], g[c][j]);
+    }
+    sum = warp_sum(sum);
+  }
+  uint32_t mx = 0;
+  if (a.kind == kRowsInt8) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mx = max(mx, f8_mag(t[c][j]));
+    mx = __reduce_max_sync(0xffffffffu, mx);
+  }
+  if (!a.warp_rows) {
+    if (lane == 0) {
+      s_sum[warp] = sum;
+      s_max[warp] = mx;
+    }
+    __syncthreads();
+    // warps' sums in warp order in every lane
+    float ws = lane < units ? s_sum[lane] : 0.f;
+    const uint32_t wm = lane < units ? s_max[lane] : 0u;
+    if (NORM) sum = warp_sum(ws);
+    mx = __reduce_max_sync(0xffffffffu, wm);
+  }
+  float f = 1.f;
+  if (NORM) f = 1.f / sqrtf(sum / (float)a.cols + a.eps);
+
+  if (NORM && a.out) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = t[c][j] * f;
+      store_values<VEC>(a.out, row * a.ldo, a.out_bf16, unit0 + c * units, lane, a.cols, y);
+    }
+  }
+  if (a.kind == kRowsInt8) {
+    const bool finite = mx < 0x7F800000u;
+    const float m = fmaxf(__uint_as_float(mx), kLeastMax);
+    const float inv = finite ? 127.f / m : 0.f;
+    uint8_t* codes = a.codes + row * a.ldq;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const uint2 q = make_uint2(int8x4(t[c], inv), int8x4(t[c] + 4, inv));
+      store_codes<VEC>(codes, unit0 + c * units, lane, a.cols, finite ? q : make_uint2(0u, 0u));
+    }
+    if (unit0 == 0 && lane == 0) a.scales[row] = finite ? (m / 127.f) * f : __uint_as_float(kF8NanScale);
+  } else if (NORM && a.kind == kRowsE4m3) {
+    const int nb = f8_blocks(a.cols);
+    float* scales = a.scales + row * nb;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int unit = unit0 + c * units;
+      // the largest magnitudes of the warp's two blocks: VEC by half warps,
+      // else of values 0-3 and 4-7 over the warp
+      uint32_t m[2] = {0u, 0u};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m[VEC ? 0 : j >> 2] = max(m[VEC ? 0 : j >> 2], f8_mag(t[c][j]));
+      if (VEC) {
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m[0] = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+        m[1] = m[0];
+      } else {
+        m[0] = __reduce_max_sync(0xffffffffu, m[0]);
+        m[1] = __reduce_max_sync(0xffffffffu, m[1]);
+      }
+      const uint32_t sb[2] = {f8_scale_bits(m[0]), f8_scale_bits(m[1])};
+      const float i0 = f8_inverse(sb[0]), i1 = f8_inverse(sb[1]);
+      store_codes<VEC>(a.codes + row * a.ldq, unit, lane, a.cols,
+                       make_uint2(f8_pack4(t[c][0] * i0, t[c][1] * i0, t[c][2] * i0, t[c][3] * i0),
+                                  f8_pack4(t[c][4] * i1, t[c][5] * i1, t[c][6] * i1, t[c][7] * i1)));
+      // one lane a block: lanes 0 and 16 (VEC), else lanes 0 and 1
+      const int blk = 2 * unit + (VEC ? lane >> 4 : lane);
+      if ((VEC ? (lane & 15) == 0 : lane < 2) && blk < nb)
+        scales[blk] = __uint_as_float(VEC || lane == 0 ? sb[0] : sb[1]) * f;
+    }
+  }
+}
+
+template <typename TX, int RES, bool NORM, bool VEC>
+cudaError_t launch_ch(RowsArgs a, cudaStream_t st) {
+  const int units = (a.cols + 255) / 256;
+  if (units <= 4) {
+    a.warp_rows = 1;
+    const dim3 grid((unsigned)((a.rows + kWarpRows - 1) / kWarpRows));
+    if (units == 1) return launch_pdl(rows_kernel<TX, RES, NORM, VEC, 1>, grid, 32 * kWarpRows, 0, st, a);
+    if (units == 2) return launch_pdl(rows_kernel<TX, RES, NORM, VEC, 2>, grid, 32 * kWarpRows, 0, st, a);
+    return launch_pdl(rows_kernel<TX, RES, NORM, VEC, 4>, grid, 32 * kWarpRows, 0, st, a);
+  }
+  a.warp_rows = 0;
+  const dim3 grid((unsigned)a.rows);
+  const bool few = a.rows <= 2 * tc_sm_count();
+  // pieces a thread: one where rows are few (latency), else two while a row
+  // fits a CTA that way
+  const int ch = few && units <= 32 ? 1 : units <= 64 ? 2 : 8;
+  const int threads = 32 * ((units + ch - 1) / ch);
+  if (ch == 1) return launch_pdl(rows_kernel<TX, RES, NORM, VEC, 1>, grid, threads, 0, st, a);
+  if (ch == 2) return launch_pdl(rows_kernel<TX, RES, NORM, VEC, 2>, grid, threads, 0, st, a);
+  return launch_pdl(rows_kernel<TX, RES, NORM, VEC, 8>, grid, threads, 0, st, a);
+}
+
+template <typename TX, bool VEC>
+cudaError_t launch_rows_t(const RowsArgs& a, cudaStream_t st) {
+  if (!a.norm) return launch_ch<TX, 0, false, VEC>(a, st);
+  if (!a.residual) return launch_ch<TX, 0, true, VEC>(a, st);
+  return a.res_bf16 ? launch_ch<TX, 2, true, VEC>(a, st) : launch_ch<TX, 1, true, VEC>(a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st) {
+  const auto wide = [&](const void* p, long long ld, int bytes, int align) {
+    return !p || (((uintptr_t)p & (align - 1)) == 0 && ld * bytes % align == 0);
+  };
+  const bool vec = a.cols % 8 == 0 && wide(a.x, a.ldx, a.x_bf16 ? 2 : 4, 16) &&
+                   wide(a.residual, a.ldr, a.res_bf16 ? 2 : 4, 16) && wide(a.gain, 0, 1, 16) &&
+                   wide(a.sum, a.lds, a.sum_bf16 ? 2 : 4, 16) && wide(a.out, a.ldo, a.out_bf16 ? 2 : 4, 16) &&
+                   wide(a.codes, a.ldq, 1, 8);
+  if (a.x_bf16) return vec ? launch_rows_t<__nv_bfloat16, true>(a, st) : launch_rows_t<__nv_bfloat16, false>(a, st);
+  return vec ? launch_rows_t<float, true>(a, st) : launch_rows_t<float, false>(a, st);
+}
+
+}  // namespace moe

@@ -12,7 +12,7 @@
 namespace moe {
 namespace {
 
-constexpr int kTileCols = 128;  // columns of the result in a tile
+constexpr int kTileRows = 128;  // weight rows of a tile
 constexpr int kStepK = 128;
 constexpr int kSms = 152;       // SMs that a product is laid out for
 
@@ -38,7 +38,7 @@ moe_status_t validate_mm(const moe_i8_matmul_t* m) {
   if (m->lda >= (1ll << 40) || m->ldb >= (1ll << 40) || m->ldo >= (1ll << 40)) return MOE_ERR_UNSUPPORTED;
   // the kernels count tiles and their splits in 32 bits
   if (m->N > (1 << 30) || m->M > (1 << 30) ||
-      ((long long)m->M / 16 + 1) * ((long long)m->N / kTileCols + 1) > (1ll << 24))
+      ((long long)m->M / 16 + 1) * ((long long)m->N / 64 + 1) > (1ll << 24))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -54,11 +54,12 @@ MmPlan mm_plan(const moe_i8_matmul_t& m) {
   p.wide = p.total = align256(sizeof(Ctrl));
   if (m.M <= kI8FewRows) return p;
   p.half = m.M <= 16 ? 16 : m.M <= 32 ? 32 : m.M <= 64 ? 64 : 128;
-  p.kind = m.gated ? kI8Gated : kI8One;
-  p.n_tiles = (m.N + kTileCols - 1) / kTileCols;
+  p.kind = kI8One;
+  const int cols = m.gated ? kTileRows / 2 : kTileRows;
+  p.n_tiles = (m.N + cols - 1) / cols;
   const auto tiles_of = [&](int rows) { return (long long)((m.M + rows - 1) / rows) * p.n_tiles; };
   // two blocks a tile where that leaves a tile for every SM
-  if (!m.gated && m.M > 128 && tiles_of(256) >= kSms) p.kind = kI8Two;
+  if (m.M > 128 && tiles_of(256) >= kSms) p.kind = kI8Two;
   const int rows = p.half * (p.kind == kI8Two ? 2 : 1);
   p.m_tiles = (m.M + rows - 1) / rows;
   const int steps = (m.K + kStepK - 1) / kStepK;
@@ -73,8 +74,7 @@ MmPlan mm_plan(const moe_i8_matmul_t& m) {
   p.pitch = (m.K + 15) / 16 * 16;
   p.partial = p.wide + align256((size_t)m.M * p.pitch * 2);
   p.total = p.partial;
-  const int sums = p.kind == kI8One ? 1 : 2;
-  if (p.ksplit > 1) p.total += (size_t)p.ksplit * tiles * sums * p.half * kTileCols * 4;
+  if (p.ksplit > 1) p.total += (size_t)p.ksplit * tiles * rows * kTileRows * 4;
   return p;
 }
 
@@ -108,8 +108,8 @@ moe_status_t product(const void* a, const float* a_scale, const void* b0, const 
   char* ws = static_cast<char*>(mm->workspace);
   I8TcMaps m{};
   if (!i8_make_map(&m.A, ws + p.wide, mm->M, mm->K, p.pitch, p.half) ||
-      !f8_make_map(&m.B0, b0, mm->N, mm->K, mm->ldb, kTileCols) ||
-      !f8_make_map(&m.B1, gated ? b1 : b0, mm->N, mm->K, mm->ldb, kTileCols))
+      !f8_make_map(&m.B0, b0, mm->N, mm->K, mm->ldb, gated ? kTileRows / 2 : kTileRows) ||
+      !f8_make_map(&m.B1, gated ? b1 : b0, mm->N, mm->K, mm->ldb, kTileRows / 2))
     return MOE_ERR_CUDA;
   const I8WidenArgs w{static_cast<const uint8_t*>(a), ws + p.wide, mm->M, mm->K, p.pitch, mm->lda};
   cudaError_t e = run_kernel(MOE_KERNEL_I8_MATMUL, st, [&] { return launch_i8_widen(w, st); });
@@ -130,11 +130,11 @@ moe_status_t product(const void* a, const float* a_scale, const void* b0, const 
   g.out_bf16 = bf16 ? 1 : 0;
   g.ldo = mm->ldo;
   g.wait_ns = launch_wait_limit(MOE_KERNEL_I8_MATMUL, &g.stall);
-  e = run_kernel(MOE_KERNEL_I8_MATMUL, st, [&] { return launch_i8_tc(p.kind, p.half, m, g, st); });
+  e = run_kernel(MOE_KERNEL_I8_MATMUL, st, [&] { return launch_i8_tc(p.kind, p.half, gated != 0, m, g, st); });
   if (e != cudaSuccess) return MOE_ERR_CUDA;
   if (p.ksplit == 1) return MOE_OK;
   return cuda_status(
-      run_kernel(MOE_KERNEL_I8_MATMUL, st, [&] { return launch_i8_split_sum(p.kind, p.half, g, st); }));
+      run_kernel(MOE_KERNEL_I8_MATMUL, st, [&] { return launch_i8_split_sum(p.kind, p.half, gated != 0, g, st); }));
 }
 
 }  // namespace

@@ -8,21 +8,25 @@
 // into int32 registers: the result is the integers' exact sum, whatever the
 // codes and whatever the order.
 //
-// The weights are the m side of the products (128 columns of the result), the
-// tokens the n side. Weights come by TMA as 8-bit codes, 128 x 128 a step; four
-// warps widen them, a thread one row, and write them to TMEM, from where
-// tcgen05.mma takes its first operand: the widened weights cost no shared
-// memory traffic. The tokens are few bytes and are widened once, by a launch
-// before this one, into the workspace, and come by TMA as fp16.
+// The weights are the m side of the products (128 rows a tile; gated: 64 rows of
+// gate and the same 64 of up), the tokens the n side. Weights come by TMA as
+// 8-bit codes, 128 x 128 a step; eight warps widen them, a thread half a row,
+// and write them to TMEM, from where tcgen05.mma takes its first operand: the
+// widened weights cost no shared memory traffic. The tokens are few bytes and
+// are widened once, by a launch before this one, into the workspace, and come by
+// TMA as fp16.
 //
-// TMEM: columns 0-255 two accumulators of up to 128 columns, 256-511 four slots of
-// widened weights (64 columns: 128 k of fp16 pairs). Accumulators:
-//  * kI8Two   two blocks of `half` rows of A; one drains while the other fills;
-//  * kI8Gated the gate and the up product of one block; the same;
-//  * kI8One   one block; the accumulators take turns by 1024 k.
+// Two threads issue the MMAs: what an issuer does between two steps (two waits,
+// two commits) takes longer than the step's MMAs leave. With one block of tokens
+// (kI8One) they take the steps in turn, with two (kI8Two) a block each, and each
+// sums on its own. Their sums rotate through three accumulators, so that one is
+// read back while two fill (two accumulators left the tensor core idle for the
+// read-back, 1400 cycles every 1024 k: the conversion to integers runs at 16 a
+// cycle).
 //
-// Warps: 0 brings weights, 3 tokens, 1 and 2 issue the MMAs (an accumulator each;
-// kI8One has one issuer), 4-7 widen, 8-15 read back, scale and store.
+// Warps: 0 brings weights, 3 tokens, 1 and 2 issue, 4-11 widen, 12-19 read back,
+// scale and store. Gated, the warps that hold a column's gate and its up sums
+// swap half of them through shared memory.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -38,23 +42,33 @@ using namespace tc;
 constexpr int kRows = 128;    // weight rows of a tile
 constexpr int kStep = 128;    // k of a step
 constexpr int kChunk = 8;     // steps whose sums fp32 holds exactly
-constexpr int kSlots = 4;     // widened weights in TMEM
-constexpr uint32_t kAccCols = 128, kSlotCol0 = 256, kSlotCols = 64, kTmemCols = 512;
+constexpr int kAccs = 3;      // accumulators
+constexpr uint32_t kSlotCols = 64, kTmemCols = 512;
 constexpr int kStageW = kRows * kStep;
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 32 * (8 + kEpiWarps);
+constexpr int kConvWarp0 = 4, kConvWarps = 8, kEpiWarp0 = 12, kEpiWarps = 8;
+constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 static_assert(kChunk * kStep * 128 * 128 <= 1 << 24, "a chunk's sums are exact in fp32");
 
-// Stages of the two rings: about 208 KB whatever the tokens' block.
 template <int HALF>
 struct Plan {
+  // TMEM: accumulators, then widened weights (64 columns: 128 k of fp16 pairs)
+  static constexpr uint32_t kAccCols = HALF == 128 ? 128 : 64;
+  static constexpr uint32_t kSlotCol0 = HALF == 128 ? 384 : 256;
+  static constexpr int kSlots = HALF == 128 ? 2 : 4;
+  // stages of the two rings, up to about 200 KB
   static constexpr int kStageT = HALF * kStep * 2;
   static constexpr int kT = HALF == 128 ? 4 : HALF == 64 ? 6 : 8;
-  static constexpr int kW = HALF == 128 ? 5 : HALF == 64 ? 7 : HALF == 32 ? 9 : 11;
+  static constexpr int kW = HALF == 128 ? 4 : HALF == 64 ? 6 : HALF == 32 ? 8 : 10;
+  // columns of an accumulator that an epilogue warp reads, and swaps at a time
+  static constexpr int kCols = HALF / 2;
+  static constexpr int kSwap = kCols < 16 ? kCols / 2 : 8;
   static constexpr size_t kToken = 0;
   static constexpr size_t kWeight = kToken + (size_t)kT * kStageT;
-  static constexpr size_t kBars = kWeight + (size_t)kW * kStageW;
-  static constexpr size_t kBytes = 1024 + kBars + (2 * kT + 2 * kW + 2 * kSlots + 4) * 8 + 16;
+  static constexpr size_t kScale = kWeight + (size_t)kW * kStageW;  // [epilogue warp][128] scales of rows of A
+  static constexpr size_t kXchg = kScale + kEpiWarps * 128 * 4;     // [epilogue warp][2][kSwap][32] sums
+  static constexpr size_t kBars = kXchg + kEpiWarps * 2 * kSwap * 32 * 4;
+  static constexpr size_t kBytes = 1024 + kBars + (2 * kT + 2 * kW + 2 * kSlots + 2 * kAccs + 4) * 8 + 16;
+  static_assert(kAccs * kAccCols <= kSlotCol0 && kSlotCol0 + kSlots * kSlotCols <= kTmemCols, "TMEM plan");
   static_assert(kBytes <= 227 * 1024, "shared memory plan exceeds 227 KB");
 };
 
@@ -89,8 +103,17 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
                : "r"(taddr));
 }
 
+// Asynchronous copy of one fp32 value to shared memory, or of zero; and the wait
+// for this thread's copies.
+__device__ __forceinline__ void copy4_async(float* dst, const float* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(valid ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 struct Item {
-  int mt, nt;     // block of rows of A, tile of columns
+  int mt, nt;     // tile of rows of A, tile of weight rows
   int kb0, kb1;   // steps
   int tile, split;
 };
@@ -111,6 +134,16 @@ __device__ __forceinline__ Item item_at(const I8TcArgs& a, int t) {
   it.kb1 = (it.split + 1) * a.steps / a.ksplit;
   tile_at(it.tile, a.m_tiles, a.n_tiles, it.mt, it.nt);
   return it;
+}
+
+// Accumulators that an item of n steps fills: eight steps each, the two issuers'
+// in turn (kI8One: every second step each, so that a lone last step is the
+// first issuer's).
+template <int KIND>
+__device__ __forceinline__ int accs_of(int n) {
+  if (KIND == kI8Two) return 2 * ((n + kChunk - 1) / kChunk);
+  const int rest = n % (2 * kChunk);
+  return 2 * (n / (2 * kChunk)) + (rest < 2 ? rest : 2);
 }
 
 __device__ __forceinline__ void give_up(const I8TcArgs& a, volatile int* abort_flag) {
@@ -141,14 +174,13 @@ struct Place {
   }
 };
 
-template <int KIND, int HALF>
+template <int KIND, int HALF, bool GATED>
 __global__ void __launch_bounds__(kThreads, 1)
     i8_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
                  const __grid_constant__ CUtensorMap tmB1, const I8TcArgs a) {
   using P = Plan<HALF>;
-  constexpr int kBlocks = KIND == kI8Two ? 2 : 1;    // token blocks of a tile
-  constexpr int kWeights = KIND == kI8Gated ? 2 : 1; // weight matrices
-  constexpr int kSums = KIND == kI8One ? 1 : 2;      // accumulators that an item ends with
+  constexpr int kBlocks = KIND == kI8Two ? 2 : 1;  // token blocks of a tile
+  constexpr int kOuts = GATED ? kRows / 2 : kRows;  // columns of the result of a tile
   constexpr uint32_t kIdesc = idesc_f16(HALF);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -159,30 +191,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* tempty = tfull + P::kT;
   uint64_t* wfull = tempty + P::kT;
   uint64_t* wempty = wfull + P::kW;
-  uint64_t* sfull = wempty + P::kW;   // slots of widened weights
-  uint64_t* sempty = sfull + kSlots;
-  uint64_t* dfull = sempty + kSlots;  // accumulators
-  uint64_t* dempty = dfull + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dempty + 2);
+  uint64_t* sfull = wempty + P::kW;      // slots of widened weights
+  uint64_t* sempty = sfull + P::kSlots;
+  uint64_t* dfull = sempty + P::kSlots;  // accumulators
+  uint64_t* dempty = dfull + kAccs;
+  uint64_t* xbar = dempty + kAccs;       // pairs of epilogue warps that swap sums
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(xbar + 4);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < P::kT; ++s) {
       mbar_init(&tfull[s], 1);
-      mbar_init(&tempty[s], kWeights);  // one commit per issuer that reads the stage
+      mbar_init(&tempty[s], 1);
     }
     for (int s = 0; s < P::kW; ++s) {
       mbar_init(&wfull[s], 1);
-      mbar_init(&wempty[s], 4);
+      mbar_init(&wempty[s], kConvWarps);
     }
-    for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&sfull[s], 4);
-      mbar_init(&sempty[s], kBlocks);
+    for (int s = 0; s < P::kSlots; ++s) {
+      mbar_init(&sfull[s], kConvWarps);
+      mbar_init(&sempty[s], kBlocks);  // one commit per issuer that reads the slot
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kAccs; ++b) {
       mbar_init(&dfull[b], 1);
       mbar_init(&dempty[b], kEpiWarps);
     }
+    for (int b = 0; b < 4; ++b) mbar_init(&xbar[b], 2);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -196,32 +230,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  pdl_wait();
-  pdl_trigger();
   const int total = a.m_tiles * a.n_tiles * a.ksplit;
 
-  if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  if (warp < kConvWarp0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp == 0) {
       // --------------------------------------------------------------- weights
+      // Before the wait for the kernel before this one: that is the same call's
+      // widening of the tokens, and what is older has completed.
       if (lane == 0) {
         Place p;
         bool alive = true;
         for (int t = blockIdx.x; t < total && alive; t += gridDim.x) {
           const Item it = item_at(a, t);
-          for (int kb = it.kb0; kb < it.kb1 && alive; ++kb) {
-#pragma unroll
-            for (int w = 0; w < kWeights; ++w) {
-              if (!(alive = lane_wait(&wempty[p.at], p.ph ^ 1u, a, abort_flag))) break;
-              mbar_expect_tx(&wfull[p.at], kStageW);
-              tma_load_2d(sW + p.at * kStageW, w ? &tmB1 : &tmB0, &wfull[p.at], kb * kStep, it.nt * kRows);
-              p.next(P::kW);
-            }
+          for (int kb = it.kb0; kb < it.kb1; ++kb) {
+            if (!(alive = lane_wait(&wempty[p.at], p.ph ^ 1u, a, abort_flag))) break;
+            uint8_t* dst = sW + p.at * kStageW;
+            mbar_expect_tx(&wfull[p.at], kStageW);
+            tma_load_2d(dst, &tmB0, &wfull[p.at], kb * kStep, it.nt * kOuts);
+            if (GATED) tma_load_2d(dst + kStageW / 2, &tmB1, &wfull[p.at], kb * kStep, it.nt * kOuts);
+            p.next(P::kW);
           }
         }
       }
     } else if (warp == 3) {
       // ---------------------------------------------------------------- tokens
+      pdl_wait();
+      pdl_trigger();
       if (lane == 0) {
         Place p;
         bool alive = true;
@@ -241,28 +276,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-    } else if (warp - 1 < kSums) {
+    } else if (lane == 0) {
       // --------------------------------------------------------------- issuers
-      if (lane == 0) {
-        const int me = warp - 1;
-        Place tp, sp;         // this issuer's next token stage and weight slot
-        if (KIND == kI8Two && me) tp.next(P::kT);
-        if (KIND == kI8Gated && me) sp.next(kSlots);
-        uint32_t used[2] = {0, 0};  // chunks that an accumulator has had
-        int acc = me;
-        // failure self-test: wait on a barrier that only this warp completes
-        bool alive = !a.stall || lane_wait(&dfull[me], 0u, a, abort_flag);
-        for (int t = blockIdx.x; t < total && alive; t += gridDim.x) {
-          const Item it = item_at(a, t);
-          for (int kb = it.kb0; kb < it.kb1; ++kb) {
-            const int in_chunk = (kb - it.kb0) % kChunk;
-            if (in_chunk == 0 && !(alive = lane_wait(&dempty[acc], (used[acc] & 1u) ^ 1u, a, abort_flag))) break;
+      const int me = warp - 1;
+      Place tp, sp;  // token stage and weight slot
+      if (KIND == kI8Two && me) tp.next(P::kT);
+      int base = 0;  // accumulators filled before this item
+      // failure self-test: wait on a barrier that only this warp completes
+      bool alive = !a.stall || lane_wait(&dfull[me], 0u, a, abort_flag);
+      for (int t = blockIdx.x; t < total && alive; t += gridDim.x) {
+        const Item it = item_at(a, t);
+        const int n = it.kb1 - it.kb0;
+        int in_chunk = 0, use = base + me;
+        for (int i = 0; i < n; ++i) {
+          if (KIND == kI8Two || (i & 1) == me) {
+            const int acc = use % kAccs;
+            if (in_chunk == 0 &&
+                !(alive = lane_wait(&dempty[acc], ((use / kAccs) & 1u) ^ 1u, a, abort_flag)))
+              break;
             if (!(alive = lane_wait(&sfull[sp.at], sp.ph, a, abort_flag) &&
                           lane_wait(&tfull[tp.at], tp.ph, a, abort_flag)))
               break;
             tc_fence_after();
-            const uint32_t d = tmem_base + acc * kAccCols;
-            const uint32_t w = tmem_base + kSlotCol0 + sp.at * kSlotCols;
+            const uint32_t d = tmem_base + acc * P::kAccCols;
+            const uint32_t w = tmem_base + P::kSlotCol0 + sp.at * kSlotCols;
             const uint64_t b = sw128_desc(smem_u32(sT + tp.at * P::kStageT));
             constexpr uint64_t kHalfStage = (P::kStageT / 2) >> 4;
 #pragma unroll
@@ -271,89 +308,103 @@ __global__ void __launch_bounds__(kThreads, 1)
                          in_chunk != 0 || k != 0 ? 1u : 0u);
             mma_commit(&tempty[tp.at]);
             mma_commit(&sempty[sp.at]);
-            if (in_chunk == kChunk - 1 || kb == it.kb1 - 1) {
+            if (++in_chunk == kChunk || i + (KIND == kI8Two ? 1 : 2) >= n) {
               mma_commit(&dfull[acc]);
-              ++used[acc];
-              if (KIND == kI8One) acc ^= 1;
+              in_chunk = 0;
+              use += 2;
             }
-            for (int i = 0; i < kBlocks; ++i) tp.next(P::kT);
-            for (int i = 0; i < kWeights; ++i) sp.next(kSlots);
           }
+          tp.next(P::kT);
+          if (KIND == kI8Two) tp.next(P::kT);
+          sp.next(P::kSlots);
         }
+        base += accs_of<KIND>(n);
       }
     }
     __syncwarp();
-  } else if (warp < 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  } else if (warp < kEpiWarp0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     // ------------------------------------------------------------------- widen
-    const int r = (warp & 3) * 32 + lane;  // this thread's weight row, and TMEM lane
-    const uint32_t tq = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + kSlotCol0;
+    const int r = (warp & 3) * 32 + lane;        // this thread's weight row, and TMEM lane
+    const int h = (warp - kConvWarp0) >> 2;      // its half of the step's k
+    const uint32_t tq = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + P::kSlotCol0 + h * (kSlotCols / 2);
     Place wp, sp;
     bool alive = true;
     for (int t = blockIdx.x; t < total && alive; t += gridDim.x) {
       const int split = t % a.ksplit;
-      const int tiles = ((split + 1) * a.steps / a.ksplit - split * a.steps / a.ksplit) * kWeights;
-      for (int i = 0; i < tiles; ++i) {
-        if (!(alive = warp_wait(&wfull[wp.at], wp.ph, a, abort_flag) &&
-                      warp_wait(&sempty[sp.at], sp.ph ^ 1u, a, abort_flag)))
-          break;
-        tc_fence_after();
+      const int n = (split + 1) * a.steps / a.ksplit - split * a.steps / a.ksplit;
+      for (int i = 0; i < n; ++i) {
+        if (!(alive = warp_wait(&wfull[wp.at], wp.ph, a, abort_flag))) break;
         const uint8_t* row = sW + wp.at * kStageW + r * kStep;
+        uint32_t v[32];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t v[32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {  // 16-byte pieces, swizzled by the row
-            const uint4 w = ld_shared_v4(row + (((h * 4 + c) ^ (r & 7)) << 4));
-            i8_to_f16(w.x, v[8 * c], v[8 * c + 1]);
-            i8_to_f16(w.y, v[8 * c + 2], v[8 * c + 3]);
-            i8_to_f16(w.z, v[8 * c + 4], v[8 * c + 5]);
-            i8_to_f16(w.w, v[8 * c + 6], v[8 * c + 7]);
-          }
-          tmem_st32(tq + sp.at * kSlotCols + h * 32, v);
+        for (int c = 0; c < 4; ++c) {  // 16-byte pieces, swizzled by the row
+          const uint4 w = ld_shared_v4(row + (((h * 4 + c) ^ (r & 7)) << 4));
+          i8_to_f16(w.x, v[8 * c], v[8 * c + 1]);
+          i8_to_f16(w.y, v[8 * c + 2], v[8 * c + 3]);
+          i8_to_f16(w.z, v[8 * c + 4], v[8 * c + 5]);
+          i8_to_f16(w.w, v[8 * c + 6], v[8 * c + 7]);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&wempty[wp.at]);
+        if (!(alive = warp_wait(&sempty[sp.at], sp.ph ^ 1u, a, abort_flag))) break;
+        tc_fence_after();
+        tmem_st32(tq + sp.at * kSlotCols, v);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sfull[sp.at]);
         wp.next(P::kW);
-        sp.next(kSlots);
+        sp.next(P::kSlots);
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     // ---------------------------------------------------------------- epilogue
-    constexpr int kCols = HALF / 2;  // columns of an accumulator that a warp reads
+    constexpr int kCols = P::kCols, kSwap = P::kSwap;
     constexpr int kPiece = kCols < 16 ? 8 : 16;
-    const int part = (warp - 8) >> 2;
+    const int mine = warp - kEpiWarp0, part = mine >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t tq = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + part * kCols;
-    int acc = 0;
-    uint32_t ph[2] = {0, 0};
+    float* scale = reinterpret_cast<float*>(smem + P::kScale) + mine * 128;
+    const bool up = GATED && (warp & 2) != 0;  // this warp's rows are up's
+    int* swap_out = reinterpret_cast<int*>(smem + P::kXchg) + mine * (2 * kSwap * 32) + lane;
+    const int* swap_in = reinterpret_cast<int*>(smem + P::kXchg) + (mine ^ 2) * (2 * kSwap * 32) + lane;
+    uint64_t* swap_bar = &xbar[part * 2 + (warp & 1)];
+    uint32_t swaps = 0;
+    int use = 0;
     bool alive = true;
     for (int t = blockIdx.x; t < total && alive; t += gridDim.x) {
       const Item it = item_at(a, t);
-      int sum[kSums][kCols];
+      // the scales of this warp's rows of A, in flight during the steps
+      constexpr int kMine = kBlocks * kCols;
 #pragma unroll
-      for (int s = 0; s < kSums; ++s)
+      for (int i = 0; i < (kMine + 31) / 32; ++i) {
+        const int j = i * 32 + lane, m = (it.mt * kBlocks + j / kCols) * HALF + part * kCols + j % kCols;
+        if (j < kMine) copy4_async(scale + j, a.a_scale + (m < a.M ? m : 0), m < a.M);
+      }
+      const int n = it.nt * kOuts + r % kOuts;
+      const bool in = n < a.N;
+      const float b0 = in ? a.b_scale0[n] : 0.f;
+      const float b1 = GATED && in ? a.b_scale1[n] : 0.f;
+      int sum[kBlocks][kCols];
+#pragma unroll
+      for (int s = 0; s < kBlocks; ++s)
 #pragma unroll
         for (int j = 0; j < kCols; ++j) sum[s][j] = 0;
-      for (int kb = it.kb0; kb < it.kb1 && alive; kb += kChunk) {
+      for (int left = accs_of<KIND>(it.kb1 - it.kb0); left > 0 && alive; left -= kBlocks) {
 #pragma unroll
-        for (int s = 0; s < kSums; ++s) {
-          const int at = KIND == kI8One ? acc : s;
-          if (!(alive = warp_wait(&dfull[at], ph[at], a, abort_flag))) break;
-          ph[at] ^= 1u;
+        for (int s = 0; s < kBlocks; ++s) {
+          const int acc = use % kAccs;
+          if (!(alive = warp_wait(&dfull[acc], (use / kAccs) & 1u, a, abort_flag))) break;
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < kCols / kPiece; ++c) {
             uint32_t v[kPiece];
             if (kPiece == 8)
-              tmem_ld8(tq + at * kAccCols + c * kPiece, v);
+              tmem_ld8(tq + acc * P::kAccCols + c * kPiece, v);
             else
-              tmem_ld16(tq + at * kAccCols + c * kPiece, v);
+              tmem_ld16(tq + acc * P::kAccCols + c * kPiece, v);
             tmem_ld_wait();
             // the read's registers hold their values from here on: the compiler
             // moves no use above the wait
@@ -365,40 +416,72 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&dempty[at]);
-          if (KIND == kI8One) acc ^= 1;
+          if (lane == 0) mbar_arrive(&dempty[acc]);
+          ++use;
         }
       }
       if (!alive) break;
       if (a.ksplit > 1) {
         int* p = a.partial +
-                 (((size_t)it.split * a.m_tiles * a.n_tiles + it.tile) * kSums * HALF + part * kCols) * kRows + r;
+                 (((size_t)it.split * a.m_tiles * a.n_tiles + it.tile) * kBlocks * HALF + part * kCols) * kRows + r;
 #pragma unroll
-        for (int s = 0; s < kSums; ++s)
+        for (int s = 0; s < kBlocks; ++s)
 #pragma unroll
           for (int j = 0; j < kCols; ++j) p[(s * HALF + j) * kRows] = sum[s][j];
         continue;
       }
-      const int n = it.nt * kRows + r;
-      const bool in = n < a.N;
-      const float b0 = in ? a.b_scale0[n] : 0.f;
-      const float b1 = KIND == kI8Gated && in ? a.b_scale1[n] : 0.f;
+      copies_wait();
+      __syncwarp();
+      const auto finish = [&](auto* out) {
 #pragma unroll
-      for (int s = 0; s < (KIND == kI8Two ? 2 : 1); ++s) {
-        const int m0 = (it.mt * kBlocks + s) * HALF + part * kCols;
+        for (int s = 0; s < kBlocks; ++s) {
+          const int m0 = (it.mt * kBlocks + s) * HALF + part * kCols, rows = in ? a.M - m0 : 0;
+          if (!GATED) {
+            auto* dst = out + (long long)m0 * a.ldo + n;
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) {
-          const int m = m0 + j;
-          if (m >= a.M) break;
-          const float sa = __ldg(a.a_scale + m);
-          float y = i8_value(sum[s][j], sa, b0);
-          if (KIND == kI8Gated) y = siluf_(y) * i8_value(sum[kSums - 1][j], sa, b1);
-          if (in) i8_store(a.out, (size_t)m * a.ldo + n, a.out_bf16, y);
+            for (int j = 0; j < kCols; j += 4) {
+              const float4 sa = *reinterpret_cast<const float4*>(scale + s * kCols + j);
+              const float f[4] = {sa.x, sa.y, sa.z, sa.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (j + i < rows) store_act(dst, 0, i8_value(sum[s][j + i], f[i], b0));
+                dst += a.ldo;
+              }
+            }
+          } else {
+            // This warp finishes the first half of its columns (gate) or the second
+            // (up): it hands on its sums of the other half, kSwap columns at a time.
+            const int c0 = up ? kCols / 2 : 0;
+            auto* dst = out + (long long)(m0 + c0) * a.ldo + n;
+#pragma unroll
+            for (int p = 0; p < kCols / 2; p += kSwap) {
+              const uint32_t buf = (swaps & 1u) * (kSwap * 32);
+#pragma unroll
+              for (int j = 0; j < kSwap; ++j)
+                swap_out[buf + j * 32] = up ? sum[s][p + j] : sum[s][kCols / 2 + p + j];
+              __syncwarp();
+              if (lane == 0) mbar_arrive(swap_bar);
+              if (!warp_wait(swap_bar, swaps & 1u, a, abort_flag)) return false;
+              ++swaps;
+#pragma unroll
+              for (int j = 0; j < kSwap; ++j) {
+                const int own = up ? sum[s][kCols / 2 + p + j] : sum[s][p + j], other = swap_in[buf + j * 32];
+                const float sa = scale[s * kCols + c0 + p + j];
+                const float g = i8_value(up ? other : own, sa, b0), u = i8_value(up ? own : other, sa, b1);
+                if (c0 + p + j < rows) store_act(dst, 0, siluf_(g) * u);
+                dst += a.ldo;
+              }
+            }
+          }
         }
-      }
+        return true;
+      };
+      alive = a.out_bf16 ? finish(static_cast<__nv_bfloat16*>(a.out)) : finish(static_cast<float*>(a.out));
+      __syncwarp();  // the scales are read before the next item's come
     }
   }
 
+  copies_wait();
   tc_fence_before();
   __syncthreads();
   if (*abort_flag && threadIdx.x == 0) {
@@ -435,49 +518,49 @@ __global__ void __launch_bounds__(256) i8_widen_kernel(I8WidenArgs a) {
 }
 
 // The splits' sums of one output (two, gated) added and finished; a thread an
-// output, a block 128 columns of two rows.
-template <int KIND>
-__global__ void __launch_bounds__(256) i8_split_sum_kernel(I8TcArgs a, int half) {
+// output, a block the columns of a tile and two (gated: four) of its rows.
+template <bool GATED>
+__global__ void __launch_bounds__(256) i8_split_sum_kernel(I8TcArgs a, int rows) {
   pdl_wait();
   pdl_trigger();
-  const int per = half * (KIND == kI8Two ? 2 : 1);  // rows of a tile
-  const int r = threadIdx.x & (kRows - 1);
-  const int groups = (per + 1) / 2;
-  const int tile = blockIdx.x / groups, j = (blockIdx.x % groups) * 2 + (threadIdx.x >> 7);
+  constexpr int kOuts = GATED ? kRows / 2 : kRows, kPer = 256 / kOuts;
+  const int r = threadIdx.x % kOuts;
+  const int groups = (rows + kPer - 1) / kPer;
+  const int tile = blockIdx.x / groups, j = (blockIdx.x % groups) * kPer + threadIdx.x / kOuts;
   int mt, nt;
   tile_at(tile, a.m_tiles, a.n_tiles, mt, nt);
-  const int m = mt * per + j, n = nt * kRows + r;
+  const int m = mt * rows + j, n = nt * kOuts + r;
   if (m >= a.M || n >= a.N) return;
-  const int sums = KIND == kI8One ? 1 : 2;
-  const size_t plane = (size_t)a.m_tiles * a.n_tiles * sums * half * kRows;
-  const int* p = a.partial + ((size_t)tile * sums * half + j) * kRows + r;
+  const size_t plane = (size_t)a.m_tiles * a.n_tiles * rows * kRows;
+  const int* p = a.partial + ((size_t)tile * rows + j) * kRows + r;
   int s0 = 0, s1 = 0;
 #pragma unroll 8
   for (int z = 0; z < a.ksplit; ++z) {
     s0 += __ldcg(p + z * plane);
-    if (KIND == kI8Gated) s1 += __ldcg(p + z * plane + (size_t)half * kRows);
+    if (GATED) s1 += __ldcg(p + z * plane + kOuts);
   }
   const float sa = a.a_scale[m];
   float y = i8_value(s0, sa, a.b_scale0[n]);
-  if (KIND == kI8Gated) y = siluf_(y) * i8_value(s1, sa, a.b_scale1[n]);
+  if (GATED) y = siluf_(y) * i8_value(s1, sa, a.b_scale1[n]);
   i8_store(a.out, (size_t)m * a.ldo + n, a.out_bf16, y);
 }
 
-template <int KIND, int HALF>
+template <int KIND, int HALF, bool GATED>
 cudaError_t launch_t(const I8TcMaps& m, const I8TcArgs& a, cudaStream_t st) {
   static int attr[64] = {};
-  cudaError_t e = ensure_smem_limit(i8_tc_kernel<KIND, HALF>, (int)Plan<HALF>::kBytes, attr);
+  cudaError_t e = ensure_smem_limit(i8_tc_kernel<KIND, HALF, GATED>, (int)Plan<HALF>::kBytes, attr);
   if (e != cudaSuccess) return e;
   const int items = a.m_tiles * a.n_tiles * a.ksplit, sms = tc_sm_count();
-  return launch_pdl(i8_tc_kernel<KIND, HALF>, dim3(items < sms ? items : sms), kThreads, Plan<HALF>::kBytes, st,
-                    m.A, m.B0, m.B1, a);
+  return launch_pdl(i8_tc_kernel<KIND, HALF, GATED>, dim3(items < sms ? items : sms), kThreads, Plan<HALF>::kBytes,
+                    st, m.A, m.B0, m.B1, a);
 }
-template <int KIND>
-cudaError_t launch_half(int half, const I8TcMaps& m, const I8TcArgs& a, cudaStream_t st) {
-  if (half == 16) return launch_t<KIND, 16>(m, a, st);
-  if (half == 32) return launch_t<KIND, 32>(m, a, st);
-  if (half == 64) return launch_t<KIND, 64>(m, a, st);
-  return half == 128 ? launch_t<KIND, 128>(m, a, st) : cudaErrorInvalidValue;
+template <bool GATED>
+cudaError_t launch_half(I8Kind kind, int half, const I8TcMaps& m, const I8TcArgs& a, cudaStream_t st) {
+  if (kind == kI8Two) return half == 128 ? launch_t<kI8Two, 128, GATED>(m, a, st) : cudaErrorInvalidValue;
+  if (half == 16) return launch_t<kI8One, 16, GATED>(m, a, st);
+  if (half == 32) return launch_t<kI8One, 32, GATED>(m, a, st);
+  if (half == 64) return launch_t<kI8One, 64, GATED>(m, a, st);
+  return half == 128 ? launch_t<kI8One, 128, GATED>(m, a, st) : cudaErrorInvalidValue;
 }
 
 }  // namespace
@@ -495,10 +578,9 @@ bool i8_make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t launch_i8_tc(I8Kind kind, int half, const I8TcMaps& m, const I8TcArgs& a, cudaStream_t st) {
-  if (kind == kI8One) return launch_half<kI8One>(half, m, a, st);
-  if (kind == kI8Gated) return launch_half<kI8Gated>(half, m, a, st);
-  return half == 128 ? launch_t<kI8Two, 128>(m, a, st) : cudaErrorInvalidValue;
+cudaError_t launch_i8_tc(I8Kind kind, int half, bool gated, const I8TcMaps& m, const I8TcArgs& a,
+                         cudaStream_t st) {
+  return gated ? launch_half<true>(kind, half, m, a, st) : launch_half<false>(kind, half, m, a, st);
 }
 
 cudaError_t launch_i8_widen(const I8WidenArgs& a, cudaStream_t st) {
@@ -506,12 +588,11 @@ cudaError_t launch_i8_widen(const I8WidenArgs& a, cudaStream_t st) {
   return launch_pdl(i8_widen_kernel, dim3((unsigned)((n + 255) / 256)), 256, 0, st, a);
 }
 
-cudaError_t launch_i8_split_sum(I8Kind kind, int half, const I8TcArgs& a, cudaStream_t st) {
-  const int per = half * (kind == kI8Two ? 2 : 1);
-  const dim3 grid((unsigned)(a.m_tiles * a.n_tiles * ((per + 1) / 2)));
-  if (kind == kI8One) return launch_pdl(i8_split_sum_kernel<kI8One>, grid, 256, 0, st, a, half);
-  if (kind == kI8Two) return launch_pdl(i8_split_sum_kernel<kI8Two>, grid, 256, 0, st, a, half);
-  return launch_pdl(i8_split_sum_kernel<kI8Gated>, grid, 256, 0, st, a, half);
+cudaError_t launch_i8_split_sum(I8Kind kind, int half, bool gated, const I8TcArgs& a, cudaStream_t st) {
+  const int rows = half * (kind == kI8Two ? 2 : 1), per = gated ? 4 : 2;
+  const dim3 grid((unsigned)(a.m_tiles * a.n_tiles * ((rows + per - 1) / per)));
+  return gated ? launch_pdl(i8_split_sum_kernel<true>, grid, 256, 0, st, a, rows)
+               : launch_pdl(i8_split_sum_kernel<false>, grid, 256, 0, st, a, rows);
 }
 
 }  // namespace moe

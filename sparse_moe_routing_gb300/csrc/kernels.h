@@ -351,13 +351,13 @@ struct I8WidenArgs {
 };
 cudaError_t launch_i8_widen(const I8WidenArgs& a, cudaStream_t st);
 
-// Forms of the tensor-core product: a tile is 128 columns of the result by one
-// or two blocks of `half` rows, or the gate and up products of one block.
-enum I8Kind { kI8One = 0, kI8Two = 1, kI8Gated = 2 };
+// Forms of the tensor-core product: a tile is 128 rows of weights (gated: 64 of
+// gate and of up) by one or two blocks of `half` rows of A.
+enum I8Kind { kI8One = 0, kI8Two = 1 };
 struct I8TcArgs {
   const float *a_scale, *b_scale0, *b_scale1;
   void* out;
-  int* partial;        // ksplit > 1: [ksplit][tiles][accumulators][half][128]
+  int* partial;        // ksplit > 1: [ksplit][tiles][rows of A in a tile][128]
   Ctrl* ctrl;
   int M, N, steps;     // steps: blocks of 128 k
   int m_tiles, n_tiles, ksplit, out_bf16;
@@ -371,9 +371,10 @@ struct I8TcMaps {
 // Map of fp16 rows [rows][cols], `pitch` values apart, box 64 x box_rows.
 bool i8_make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t pitch,
                  uint32_t box_rows);
-cudaError_t launch_i8_tc(I8Kind kind, int half, const I8TcMaps& m, const I8TcArgs& a, cudaStream_t st);
+cudaError_t launch_i8_tc(I8Kind kind, int half, bool gated, const I8TcMaps& m, const I8TcArgs& a,
+                         cudaStream_t st);
 // Adds the splits' sums of a product (ksplit > 1) and finishes them.
-cudaError_t launch_i8_split_sum(I8Kind kind, int half, const I8TcArgs& a, cudaStream_t st);
+cudaError_t launch_i8_split_sum(I8Kind kind, int half, bool gated, const I8TcArgs& a, cudaStream_t st);
 
 // Raises `kernel`'s dynamic shared-memory opt-in limit to at least `bytes`
 // on the current device; `limits` holds the value set so far per device

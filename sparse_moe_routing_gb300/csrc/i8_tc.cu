@@ -9,7 +9,7 @@
 // codes and whatever the order.
 //
 // The weights are the m side of the products (128 rows a tile; gated: 64 rows of
-// gate and the same 64 of up), the tokens the n side. Weights come by TMA as
+// gate and the same 64 of up, 16 and 16 in turn), the tokens the n side. Weights come by TMA as
 // 8-bit codes, 128 x 128 a step; eight warps widen them, a thread half a row,
 // and write them to TMEM, from where tcgen05.mma takes its first operand: the
 // widened weights cost no shared memory traffic. The tokens are few bytes and
@@ -25,10 +25,12 @@
 // cycle).
 //
 // Warps: 0 brings weights, 3 tokens, 1 and 2 issue, 4-11 widen, 12-19 read back,
-// scale and store. Gated, the warps that hold a column's gate and its up sums
-// swap half of them through shared memory.
+// scale and store. Gated, the two lanes of a warp that hold a column's gate and
+// its up sums give each other half of them.
 #include <cuda.h>
 #include <cudaTypedefs.h>
+
+#include <type_traits>
 
 #include "fp8_common.cuh"
 #include "i8_common.cuh"
@@ -59,15 +61,12 @@ struct Plan {
   static constexpr int kStageT = HALF * kStep * 2;
   static constexpr int kT = HALF == 128 ? 4 : HALF == 64 ? 6 : 8;
   static constexpr int kW = HALF == 128 ? 4 : HALF == 64 ? 6 : HALF == 32 ? 8 : 10;
-  // columns of an accumulator that an epilogue warp reads, and swaps at a time
-  static constexpr int kCols = HALF / 2;
-  static constexpr int kSwap = kCols < 16 ? kCols / 2 : 8;
+  static constexpr int kCols = HALF / 2;  // columns of an accumulator that an epilogue warp reads
   static constexpr size_t kToken = 0;
   static constexpr size_t kWeight = kToken + (size_t)kT * kStageT;
   static constexpr size_t kScale = kWeight + (size_t)kW * kStageW;  // [epilogue warp][128] scales of rows of A
-  static constexpr size_t kXchg = kScale + kEpiWarps * 128 * 4;     // [epilogue warp][2][kSwap][32] sums
-  static constexpr size_t kBars = kXchg + kEpiWarps * 2 * kSwap * 32 * 4;
-  static constexpr size_t kBytes = 1024 + kBars + (2 * kT + 2 * kW + 2 * kSlots + 2 * kAccs + 4) * 8 + 16;
+  static constexpr size_t kBars = kScale + kEpiWarps * 128 * 4;
+  static constexpr size_t kBytes = 1024 + kBars + (2 * kT + 2 * kW + 2 * kSlots + 2 * kAccs) * 8 + 16;
   static_assert(kAccs * kAccCols <= kSlotCol0 && kSlotCol0 + kSlots * kSlotCols <= kTmemCols, "TMEM plan");
   static_assert(kBytes <= 227 * 1024, "shared memory plan exceeds 227 KB");
 };
@@ -136,6 +135,11 @@ __device__ __forceinline__ Item item_at(const I8TcArgs& a, int t) {
   return it;
 }
 
+// Gated: the output that row r of a tile holds the gate or the up sum of, and the
+// row of output c's gate sum (up's is 16 rows on).
+__device__ __forceinline__ int out_of_row(int r) { return (r >> 5) * 16 + (r & 15); }
+__device__ __forceinline__ int row_of_out(int c) { return (c >> 4) * 32 + (c & 15); }
+
 // Accumulators that an item of n steps fills: eight steps each, the two issuers'
 // in turn (kI8One: every second step each, so that a lone last step is the
 // first issuer's).
@@ -195,8 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* sempty = sfull + P::kSlots;
   uint64_t* dfull = sempty + P::kSlots;  // accumulators
   uint64_t* dempty = dfull + kAccs;
-  uint64_t* xbar = dempty + kAccs;       // pairs of epilogue warps that swap sums
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(xbar + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dempty + kAccs);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -216,7 +219,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&dfull[b], 1);
       mbar_init(&dempty[b], kEpiWarps);
     }
-    for (int b = 0; b < 4; ++b) mbar_init(&xbar[b], 2);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -247,8 +249,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(alive = lane_wait(&wempty[p.at], p.ph ^ 1u, a, abort_flag))) break;
             uint8_t* dst = sW + p.at * kStageW;
             mbar_expect_tx(&wfull[p.at], kStageW);
-            tma_load_2d(dst, &tmB0, &wfull[p.at], kb * kStep, it.nt * kOuts);
-            if (GATED) tma_load_2d(dst + kStageW / 2, &tmB1, &wfull[p.at], kb * kStep, it.nt * kOuts);
+            if (GATED) {
+#pragma unroll
+              for (int i = 0; i < kRows / 32; ++i) {
+                tma_load_2d(dst + i * 32 * kStep, &tmB0, &wfull[p.at], kb * kStep, it.nt * kOuts + i * 16);
+                tma_load_2d(dst + (i * 32 + 16) * kStep, &tmB1, &wfull[p.at], kb * kStep, it.nt * kOuts + i * 16);
+              }
+            } else {
+              tma_load_2d(dst, &tmB0, &wfull[p.at], kb * kStep, it.nt * kOuts);
+            }
             p.next(P::kW);
           }
         }
@@ -361,17 +370,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     // ---------------------------------------------------------------- epilogue
-    constexpr int kCols = P::kCols, kSwap = P::kSwap;
+    constexpr int kCols = P::kCols;
     constexpr int kPiece = kCols < 16 ? 8 : 16;
     const int mine = warp - kEpiWarp0, part = mine >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t tq = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + part * kCols;
     float* scale = reinterpret_cast<float*>(smem + P::kScale) + mine * 128;
-    const bool up = GATED && (warp & 2) != 0;  // this warp's rows are up's
-    int* swap_out = reinterpret_cast<int*>(smem + P::kXchg) + mine * (2 * kSwap * 32) + lane;
-    const int* swap_in = reinterpret_cast<int*>(smem + P::kXchg) + (mine ^ 2) * (2 * kSwap * 32) + lane;
-    uint64_t* swap_bar = &xbar[part * 2 + (warp & 1)];
-    uint32_t swaps = 0;
+    const bool up = GATED && (lane & 16) != 0;  // this lane's row is up's
     int use = 0;
     bool alive = true;
     for (int t = blockIdx.x; t < total && alive; t += gridDim.x) {
@@ -383,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int j = i * 32 + lane, m = (it.mt * kBlocks + j / kCols) * HALF + part * kCols + j % kCols;
         if (j < kMine) copy4_async(scale + j, a.a_scale + (m < a.M ? m : 0), m < a.M);
       }
-      const int n = it.nt * kOuts + r % kOuts;
+      const int n = it.nt * kOuts + (GATED ? out_of_row(r) : r);
       const bool in = n < a.N;
       const float b0 = in ? a.b_scale0[n] : 0.f;
       const float b1 = GATED && in ? a.b_scale1[n] : 0.f;
@@ -432,51 +437,70 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       copies_wait();
       __syncwarp();
-      const auto finish = [&](auto* out) {
+      // WHOLE: every row of this warp's blocks exists.
+      const auto finish = [&](auto* out, auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
 #pragma unroll
         for (int s = 0; s < kBlocks; ++s) {
-          const int m0 = (it.mt * kBlocks + s) * HALF + part * kCols, rows = in ? a.M - m0 : 0;
+          const int m0 = (it.mt * kBlocks + s) * HALF + part * kCols;
           if (!GATED) {
             auto* dst = out + (long long)m0 * a.ldo + n;
+            if (in) {
 #pragma unroll
-            for (int j = 0; j < kCols; j += 4) {
-              const float4 sa = *reinterpret_cast<const float4*>(scale + s * kCols + j);
-              const float f[4] = {sa.x, sa.y, sa.z, sa.w};
+              for (int j = 0; j < kCols; j += 8) {
+                float y[8];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if (j + i < rows) store_act(dst, 0, i8_value(sum[s][j + i], f[i], b0));
-                dst += a.ldo;
+                for (int i = 0; i < 8; i += 4) {
+                  const float4 sa = *reinterpret_cast<const float4*>(scale + s * kCols + j + i);
+                  y[i] = i8_value(sum[s][j + i], sa.x, b0);
+                  y[i + 1] = i8_value(sum[s][j + i + 1], sa.y, b0);
+                  y[i + 2] = i8_value(sum[s][j + i + 2], sa.z, b0);
+                  y[i + 3] = i8_value(sum[s][j + i + 3], sa.w, b0);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  if (WHOLE || m0 + j + i < a.M) store_act(dst, 0, y[i]);
+                  dst += a.ldo;
+                }
               }
             }
           } else {
-            // This warp finishes the first half of its columns (gate) or the second
-            // (up): it hands on its sums of the other half, kSwap columns at a time.
+            // A gate lane finishes the first half of its columns, its up lane the
+            // second: each hands on its sums of the other half.
             const int c0 = up ? kCols / 2 : 0;
             auto* dst = out + (long long)(m0 + c0) * a.ldo + n;
+            constexpr int kGroup = kCols / 2 < 8 ? kCols / 2 : 8;
 #pragma unroll
-            for (int p = 0; p < kCols / 2; p += kSwap) {
-              const uint32_t buf = (swaps & 1u) * (kSwap * 32);
+            for (int p = 0; p < kCols / 2; p += kGroup) {
+              float y[kGroup];
 #pragma unroll
-              for (int j = 0; j < kSwap; ++j)
-                swap_out[buf + j * 32] = up ? sum[s][p + j] : sum[s][kCols / 2 + p + j];
-              __syncwarp();
-              if (lane == 0) mbar_arrive(swap_bar);
-              if (!warp_wait(swap_bar, swaps & 1u, a, abort_flag)) return false;
-              ++swaps;
-#pragma unroll
-              for (int j = 0; j < kSwap; ++j) {
-                const int own = up ? sum[s][kCols / 2 + p + j] : sum[s][p + j], other = swap_in[buf + j * 32];
+              for (int j = 0; j < kGroup; ++j) {
+                const int lo = sum[s][p + j], hi = sum[s][kCols / 2 + p + j];
+                const int own = up ? hi : lo, other = __shfl_xor_sync(0xffffffffu, up ? lo : hi, 16);
                 const float sa = scale[s * kCols + c0 + p + j];
-                const float g = i8_value(up ? other : own, sa, b0), u = i8_value(up ? own : other, sa, b1);
-                if (c0 + p + j < rows) store_act(dst, 0, siluf_(g) * u);
+                const float g = i8_value(up ? other : own, sa, b0);
+                y[j] = siluf_(g) * i8_value(up ? own : other, sa, b1);
+              }
+#pragma unroll
+              for (int j = 0; j < kGroup; ++j) {
+                if (in && (WHOLE || m0 + c0 + p + j < a.M)) store_act(dst, 0, y[j]);
                 dst += a.ldo;
               }
             }
           }
         }
-        return true;
       };
-      alive = a.out_bf16 ? finish(static_cast<__nv_bfloat16*>(a.out)) : finish(static_cast<float*>(a.out));
+      const bool whole = (it.mt + 1) * kBlocks * HALF <= a.M;
+      const auto finish_as = [&](auto* out) {
+        if (whole)
+          finish(out, std::true_type{});
+        else
+          finish(out, std::false_type{});
+      };
+      if (a.out_bf16)
+        finish_as(static_cast<__nv_bfloat16*>(a.out));
+      else
+        finish_as(static_cast<float*>(a.out));
       __syncwarp();  // the scales are read before the next item's come
     }
   }
@@ -532,12 +556,12 @@ __global__ void __launch_bounds__(256) i8_split_sum_kernel(I8TcArgs a, int rows)
   const int m = mt * rows + j, n = nt * kOuts + r;
   if (m >= a.M || n >= a.N) return;
   const size_t plane = (size_t)a.m_tiles * a.n_tiles * rows * kRows;
-  const int* p = a.partial + ((size_t)tile * rows + j) * kRows + r;
+  const int* p = a.partial + ((size_t)tile * rows + j) * kRows + (GATED ? row_of_out(r) : r);
   int s0 = 0, s1 = 0;
 #pragma unroll 8
   for (int z = 0; z < a.ksplit; ++z) {
     s0 += __ldcg(p + z * plane);
-    if (GATED) s1 += __ldcg(p + z * plane + kOuts);
+    if (GATED) s1 += __ldcg(p + z * plane + 16);
   }
   const float sa = a.a_scale[m];
   float y = i8_value(s0, sa, a.b_scale0[n]);

@@ -910,13 +910,6 @@ def int8_gated_matmul(a, a_scale, gate, gate_scale, up, up_scale, out, workspace
     _check(lib().moe_i8_gated_matmul(*args, m, p, st), "moe_i8_gated_matmul")
 
 
-def _i8_most(max_rows, N, K, gated):
-    """Rows, at most max_rows, whose product needs the most workspace. What it needs grows with the rows but for the
-    split's sums, which fewer tiles need more of, and which end with 76 tiles of 128 rows."""
-    some = {max_rows, *(r for r in (16, 32, 64) if r < max_rows), *range(128, min(max_rows, 76 * 128) + 1, 128)}
-    return max(some, key=lambda M: _i8_workspace_bytes(M, N, K, gated))
-
-
 class _Int8Weight:
     """A weight [N, K] (float32 or bfloat16) in 8-bit integers with a scale per row."""
 
@@ -937,7 +930,7 @@ class Int8Linear:
         self.w = _Int8Weight(weight)
         self.N, self.K, self.max_rows = self.w.N, self.w.K, max_rows
         self.x, self.x_scales = int8_empty(max_rows, self.K, weight.device)
-        self.ws = int8_matmul_workspace(_i8_most(max_rows, self.N, self.K, False), self.N, self.K, device=weight.device)
+        self.ws = int8_matmul_workspace(max_rows, self.N, self.K, device=weight.device)
 
     def __call__(self, x, out, stream=None):
         quantised = isinstance(x, tuple)
@@ -979,9 +972,8 @@ class Int8FeedForward:
         self.x, self.x_scales = int8_empty(max_rows, self.d, at)
         self.h = torch.empty((max_rows, self.I), dtype=torch.bfloat16, device=at)
         self.hq, self.h_scales = int8_empty(max_rows, self.I, at)
-        shapes = [(_i8_most(max_rows, N, K, g), N, K, g) for N, K, g in ((self.I, self.d, True), (self.d, self.I, False))]
-        M, N, K, g = max(shapes, key=lambda s: _i8_workspace_bytes(*s))
-        self.ws = int8_matmul_workspace(M, N, K, gated=g, device=at)
+        # (what a product needs grows with its rows and the length of its sums)
+        self.ws = int8_matmul_workspace(max_rows, self.I, max(self.d, self.I), device=at)
 
     def __call__(self, x, out, stream=None):
         quantised = isinstance(x, tuple)

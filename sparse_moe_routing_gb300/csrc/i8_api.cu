@@ -36,7 +36,7 @@ moe_status_t validate_mm(const moe_i8_matmul_t* m) {
   if (m->K > kI8MaxK) return MOE_ERR_UNSUPPORTED;
   // a tensor map's row pitch is below 2^40 bytes
   if (m->lda >= (1ll << 40) || m->ldb >= (1ll << 40) || m->ldo >= (1ll << 40)) return MOE_ERR_UNSUPPORTED;
-  // the kernels count tiles and their splits in 32 bits
+  // the kernels count tiles in 32 bits
   if (m->N > (1 << 30) || m->M > (1 << 30) ||
       ((long long)m->M / 16 + 1) * ((long long)m->N / 64 + 1) > (1ll << 24))
     return MOE_ERR_UNSUPPORTED;
@@ -45,36 +45,25 @@ moe_status_t validate_mm(const moe_i8_matmul_t* m) {
 
 struct MmPlan {
   I8Kind kind;
-  int half, m_tiles, n_tiles, ksplit;
+  int half, m_tiles, n_tiles;
   int pitch;  // of the widened rows
-  size_t wide, partial, total;
+  size_t wide, total;
 };
 MmPlan mm_plan(const moe_i8_matmul_t& m) {
   MmPlan p{};
   p.wide = p.total = align256(sizeof(Ctrl));
-  if (m.M <= kI8FewRows) return p;
+  if (m.M <= kI8FewRows || m.N == 0) return p;
   p.half = m.M <= 16 ? 16 : m.M <= 32 ? 32 : m.M <= 64 ? 64 : 128;
   p.kind = kI8One;
   const int cols = m.gated ? kTileRows / 2 : kTileRows;
   p.n_tiles = (m.N + cols - 1) / cols;
   const auto tiles_of = [&](int rows) { return (long long)((m.M + rows - 1) / rows) * p.n_tiles; };
-  // two blocks a tile where that leaves a tile for every SM
-  if (m.M > 128 && tiles_of(256) >= kSms) p.kind = kI8Two;
+  // two blocks a tile where that leaves a tile for every second SM
+  if (m.M > 128 && 2 * tiles_of(256) >= kSms) p.kind = kI8Two;
   const int rows = p.half * (p.kind == kI8Two ? 2 : 1);
   p.m_tiles = (m.M + rows - 1) / rows;
-  const int steps = (m.K + kStepK - 1) / kStepK;
-  const long long tiles = (long long)p.m_tiles * p.n_tiles;
-  p.ksplit = 1;
-  // fewer tiles than half the SMs: k is split over CTAs, four steps each at least
-  if (tiles > 0 && 2 * tiles <= kSms) {
-    int s = (int)(kSms / tiles);
-    if (s > steps / 4) s = steps / 4;
-    if (s > 1) p.ksplit = s;
-  }
   p.pitch = (m.K + 15) / 16 * 16;
-  p.partial = p.wide + align256((size_t)m.M * p.pitch * 2);
-  p.total = p.partial;
-  if (p.ksplit > 1) p.total += (size_t)p.ksplit * tiles * rows * kTileRows * 4;
+  p.total = p.wide + align256((size_t)m.M * p.pitch * 2);
   return p;
 }
 
@@ -119,22 +108,17 @@ moe_status_t product(const void* a, const float* a_scale, const void* b0, const 
   g.b_scale0 = s0;
   g.b_scale1 = s1;
   g.out = out;
-  g.partial = reinterpret_cast<int*>(ws + p.partial);
   g.ctrl = reinterpret_cast<Ctrl*>(ws);
   g.M = mm->M;
   g.N = mm->N;
   g.steps = (mm->K + kStepK - 1) / kStepK;
   g.m_tiles = p.m_tiles;
   g.n_tiles = p.n_tiles;
-  g.ksplit = p.ksplit;
   g.out_bf16 = bf16 ? 1 : 0;
   g.ldo = mm->ldo;
   g.wait_ns = launch_wait_limit(MOE_KERNEL_I8_MATMUL, &g.stall);
-  e = run_kernel(MOE_KERNEL_I8_MATMUL, st, [&] { return launch_i8_tc(p.kind, p.half, gated != 0, m, g, st); });
-  if (e != cudaSuccess) return MOE_ERR_CUDA;
-  if (p.ksplit == 1) return MOE_OK;
-  return cuda_status(
-      run_kernel(MOE_KERNEL_I8_MATMUL, st, [&] { return launch_i8_split_sum(p.kind, p.half, gated != 0, g, st); }));
+  return cuda_status(run_kernel(MOE_KERNEL_I8_MATMUL, st,
+                                [&] { return launch_i8_tc(p.kind, p.half, gated != 0, m, g, st); }));
 }
 
 }  // namespace

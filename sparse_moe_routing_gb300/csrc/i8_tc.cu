@@ -49,6 +49,9 @@ constexpr uint32_t kSlotCols = 64, kTmemCols = 512;
 constexpr int kStageW = kRows * kStep;
 constexpr int kConvWarp0 = 4, kConvWarps = 8, kEpiWarp0 = 12, kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+// Launched with 96 registers a thread, 61,440 in all, which the warps share out
+// anew: kI8Two 128 x 48 + 256 x 56 + 256 x 160 (128 sums a thread of the
+// epilogue) = 61,440, kI8One 128 x 64 + 256 x 80 + 256 x 120 = 59,392.
 static_assert(kChunk * kStep * 128 * 128 <= 1 << 24, "a chunk's sums are exact in fp32");
 
 template <int HALF>
@@ -68,6 +71,7 @@ struct Plan {
   static constexpr size_t kBars = kScale + kEpiWarps * 128 * 4;
   static constexpr size_t kBytes = 1024 + kBars + (2 * kT + 2 * kW + 2 * kSlots + 2 * kAccs) * 8 + 16;
   static_assert(kAccs * kAccCols <= kSlotCol0 && kSlotCol0 + kSlots * kSlotCols <= kTmemCols, "TMEM plan");
+  static_assert(kT % 2 == 0 && kW % 2 == 0 && kSlots % 2 == 0, "every second stage is one issuer's, one widening group's");
   static_assert(kBytes <= 227 * 1024, "shared memory plan exceeds 227 KB");
 };
 
@@ -111,38 +115,66 @@ __device__ __forceinline__ void copy4_async(float* dst, const float* src, bool v
 }
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// What a CTA works off: a.waves whole tiles; then, of the a.cut tiles that are
+// left, a cluster one, whose CTAs share its steps evenly.
 struct Item {
   int mt, nt;     // tile of rows of A, tile of weight rows
   int kb0, kb1;   // steps
-  int tile, split;
+  bool part;      // of a tile
 };
-// Items walk bands of 8 token tiles, column tile by column tile, so that the
+// Tiles go in bands of 8 token tiles, weight tile by weight tile, so that the
 // CTAs in flight share both operands through L2.
 constexpr int kBand = 8;
-__host__ __device__ __forceinline__ void tile_at(int t, int m_tiles, int n_tiles, int& mt, int& nt) {
-  const int span = kBand * n_tiles, band = t / span, w = t - band * span;
-  const int left = m_tiles - band * kBand, width = left < kBand ? left : kBand;
-  mt = band * kBand + w % width;
-  nt = w / width;
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
 }
-__device__ __forceinline__ Item item_at(const I8TcArgs& a, int t) {
-  Item it;
-  it.split = t % a.ksplit;
-  it.tile = t / a.ksplit;
-  it.kb0 = it.split * a.steps / a.ksplit;
-  it.kb1 = (it.split + 1) * a.steps / a.ksplit;
-  tile_at(it.tile, a.m_tiles, a.n_tiles, it.mt, it.nt);
-  return it;
+struct Walk {
+  int i = 0;
+  __device__ __forceinline__ bool next(const I8TcArgs& a, Item& it) {
+    int tile = i * gridDim.x + blockIdx.x;
+    it.kb0 = 0;
+    it.kb1 = a.steps;
+    it.part = false;
+    if (i >= a.waves) {
+      const int mine = blockIdx.x / a.ks;
+      if (i > a.waves || mine >= a.cut) return false;
+      tile = i * gridDim.x + mine;
+      const int rank = cluster_rank();
+      it.kb0 = rank * a.steps / a.ks;
+      it.kb1 = (rank + 1) * a.steps / a.ks;
+      it.part = true;
+    }
+    ++i;
+    if (tile >= a.m_tiles * a.n_tiles) return false;  // (the last wave need not be full)
+    const int span = kBand * a.n_tiles, band = tile / span, w = tile - band * span;
+    const int width = min(kBand, a.m_tiles - band * kBand);
+    it.mt = band * kBand + w % width;
+    it.nt = w / width;
+    return true;
+  }
+};
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A 32-bit value at this CTA's shared address `addr` in the cluster's CTA `rank`.
+__device__ __forceinline__ int ld_cluster(uint32_t addr, int rank) {
+  int v;
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.s32 %0, [a];\n}"
+      : "=r"(v)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
 }
 
-// Gated: the output that row r of a tile holds the gate or the up sum of, and the
-// row of output c's gate sum (up's is 16 rows on).
+// Gated: the output that row r of a tile holds the gate or the up sum of.
 __device__ __forceinline__ int out_of_row(int r) { return (r >> 5) * 16 + (r & 15); }
-__device__ __forceinline__ int row_of_out(int c) { return (c >> 4) * 32 + (c & 15); }
 
 // Accumulators that an item of n steps fills: eight steps each, the two issuers'
-// in turn (kI8One: every second step each, so that a lone last step is the
-// first issuer's).
+// in turn (kI8One: every second step each, so that a lone last step is that of
+// the issuer with the item's first).
 template <int KIND>
 __device__ __forceinline__ int accs_of(int n) {
   if (KIND == kI8Two) return 2 * ((n + kChunk - 1) / kChunk);
@@ -184,6 +216,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                  const __grid_constant__ CUtensorMap tmB1, const I8TcArgs a) {
   using P = Plan<HALF>;
   constexpr int kBlocks = KIND == kI8Two ? 2 : 1;  // token blocks of a tile
+  // The eight widening warps share every step where the MMAs of a step take long
+  // and a slot has to be filled soon after it came free; else four take every
+  // second step, whose waits then overlap.
+  constexpr bool kHalves = KIND == kI8Two;
+  constexpr int kWideners = kHalves ? kConvWarps : kConvWarps / 2;
   constexpr int kOuts = GATED ? kRows / 2 : kRows;  // columns of the result of a tile
   constexpr uint32_t kIdesc = idesc_f16(HALF);
   extern __shared__ uint8_t smem_raw[];
@@ -209,10 +246,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < P::kW; ++s) {
       mbar_init(&wfull[s], 1);
-      mbar_init(&wempty[s], kConvWarps);
+      mbar_init(&wempty[s], kWideners);
     }
     for (int s = 0; s < P::kSlots; ++s) {
-      mbar_init(&sfull[s], kConvWarps);
+      mbar_init(&sfull[s], kWideners);
       mbar_init(&sempty[s], kBlocks);  // one commit per issuer that reads the slot
     }
     for (int b = 0; b < kAccs; ++b) {
@@ -232,10 +269,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int total = a.m_tiles * a.n_tiles * a.ksplit;
-
   if (warp < kConvWarp0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (KIND == kI8Two)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 0) {
       // --------------------------------------------------------------- weights
       // Before the wait for the kernel before this one: that is the same call's
@@ -243,8 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         Place p;
         bool alive = true;
-        for (int t = blockIdx.x; t < total && alive; t += gridDim.x) {
-          const Item it = item_at(a, t);
+        Item it;
+        for (Walk walk; alive && walk.next(a, it);) {
           for (int kb = it.kb0; kb < it.kb1; ++kb) {
             if (!(alive = lane_wait(&wempty[p.at], p.ph ^ 1u, a, abort_flag))) break;
             uint8_t* dst = sW + p.at * kStageW;
@@ -269,8 +307,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         Place p;
         bool alive = true;
-        for (int t = blockIdx.x; t < total && alive; t += gridDim.x) {
-          const Item it = item_at(a, t);
+        Item it;
+        for (Walk walk; alive && walk.next(a, it);) {
           for (int kb = it.kb0; kb < it.kb1 && alive; ++kb) {
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) {
@@ -290,15 +328,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int me = warp - 1;
       Place tp, sp;  // token stage and weight slot
       if (KIND == kI8Two && me) tp.next(P::kT);
-      int base = 0;  // accumulators filled before this item
+      // kI8One: an issuer has the even or the odd steps of all items together, and so
+      // every second stage and slot. (Their barriers tell two phases apart: an
+      // issuer that came to a stage whose last use was the other's could take the
+      // phase before that use for its own.) The issuer with an item's first step
+      // has the item's first accumulator.
+      int base = 0, done = 0;  // accumulators filled and steps made before this item
       // failure self-test: wait on a barrier that only this warp completes
       bool alive = !a.stall || lane_wait(&dfull[me], 0u, a, abort_flag);
-      for (int t = blockIdx.x; t < total && alive; t += gridDim.x) {
-        const Item it = item_at(a, t);
+      Item it;
+      for (Walk walk; alive && walk.next(a, it);) {
         const int n = it.kb1 - it.kb0;
-        int in_chunk = 0, use = base + me;
+        const int second = KIND == kI8Two ? me : (me + done) & 1;
+        int in_chunk = 0, use = base + second;
         for (int i = 0; i < n; ++i) {
-          if (KIND == kI8Two || (i & 1) == me) {
+          if (KIND == kI8Two || (i & 1) == second) {
             const int acc = use % kAccs;
             if (in_chunk == 0 &&
                 !(alive = lane_wait(&dempty[acc], ((use / kAccs) & 1u) ^ 1u, a, abort_flag)))
@@ -328,47 +372,66 @@ __global__ void __launch_bounds__(kThreads, 1)
           sp.next(P::kSlots);
         }
         base += accs_of<KIND>(n);
+        done += n;
       }
     }
     __syncwarp();
   } else if (warp < kEpiWarp0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (KIND == kI8Two)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     // ------------------------------------------------------------------- widen
-    const int r = (warp & 3) * 32 + lane;        // this thread's weight row, and TMEM lane
-    const int h = (warp - kConvWarp0) >> 2;      // its half of the step's k
-    const uint32_t tq = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + P::kSlotCol0 + h * (kSlotCols / 2);
+    const int r = (warp & 3) * 32 + lane;         // this thread's weight row, and TMEM lane
+    const int group = (warp - kConvWarp0) >> 2;   // its half of every step's k, or of the steps
+    const uint32_t tq = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + P::kSlotCol0;
+    int steps = 0;
     Place wp, sp;
     bool alive = true;
-    for (int t = blockIdx.x; t < total && alive; t += gridDim.x) {
-      const int split = t % a.ksplit;
-      const int n = (split + 1) * a.steps / a.ksplit - split * a.steps / a.ksplit;
-      for (int i = 0; i < n; ++i) {
-        if (!(alive = warp_wait(&wfull[wp.at], wp.ph, a, abort_flag))) break;
-        const uint8_t* row = sW + wp.at * kStageW + r * kStep;
-        uint32_t v[32];
+    Item it;
+    for (Walk walk; alive && walk.next(a, it);) {
+      const int n = it.kb1 - it.kb0;
+      for (int i = 0; i < n; ++i, ++steps) {
+        if (kHalves || (steps & 1) == group) {
+          if (!(alive = warp_wait(&wfull[wp.at], wp.ph, a, abort_flag))) break;
+          const uint8_t* row = sW + wp.at * kStageW + r * kStep;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {  // 16-byte pieces, swizzled by the row
-          const uint4 w = ld_shared_v4(row + (((h * 4 + c) ^ (r & 7)) << 4));
-          i8_to_f16(w.x, v[8 * c], v[8 * c + 1]);
-          i8_to_f16(w.y, v[8 * c + 2], v[8 * c + 3]);
-          i8_to_f16(w.z, v[8 * c + 4], v[8 * c + 5]);
-          i8_to_f16(w.w, v[8 * c + 6], v[8 * c + 7]);
+          for (int z = 0; z < (kHalves ? 1 : 2); ++z) {
+            const int h = kHalves ? group : z;
+            uint32_t v[32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {  // 16-byte pieces, swizzled by the row
+              const uint4 w = ld_shared_v4(row + (((h * 4 + c) ^ (r & 7)) << 4));
+              i8_to_f16(w.x, v[8 * c], v[8 * c + 1]);
+              i8_to_f16(w.y, v[8 * c + 2], v[8 * c + 3]);
+              i8_to_f16(w.z, v[8 * c + 4], v[8 * c + 5]);
+              i8_to_f16(w.w, v[8 * c + 6], v[8 * c + 7]);
+            }
+            if (kHalves || z == 1) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&wempty[wp.at]);
+            }
+            if (z == 0) {
+              if (!(alive = warp_wait(&sempty[sp.at], sp.ph ^ 1u, a, abort_flag))) break;
+              tc_fence_after();
+            }
+            tmem_st32(tq + sp.at * kSlotCols + h * (kSlotCols / 2), v);
+          }
+          if (!alive) break;
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sfull[sp.at]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&wempty[wp.at]);
-        if (!(alive = warp_wait(&sempty[sp.at], sp.ph ^ 1u, a, abort_flag))) break;
-        tc_fence_after();
-        tmem_st32(tq + sp.at * kSlotCols, v);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sfull[sp.at]);
         wp.next(P::kW);
         sp.next(P::kSlots);
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+    if (KIND == kI8Two)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
     // ---------------------------------------------------------------- epilogue
     constexpr int kCols = P::kCols;
     constexpr int kPiece = kCols < 16 ? 8 : 16;
@@ -379,8 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool up = GATED && (lane & 16) != 0;  // this lane's row is up's
     int use = 0;
     bool alive = true;
-    for (int t = blockIdx.x; t < total && alive; t += gridDim.x) {
-      const Item it = item_at(a, t);
+    Item it;
+    for (Walk walk; alive && walk.next(a, it);) {
       // the scales of this warp's rows of A, in flight during the steps
       constexpr int kMine = kBlocks * kCols;
 #pragma unroll
@@ -426,14 +489,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!alive) break;
-      if (a.ksplit > 1) {
-        int* p = a.partial +
-                 (((size_t)it.split * a.m_tiles * a.n_tiles + it.tile) * kBlocks * HALF + part * kCols) * kRows + r;
+      if (it.part) {
+        // its sums, for the cluster's CTAs, in the rings' place, which nothing
+        // uses any more: [column][row]
+        int* dst = reinterpret_cast<int*>(smem) + part * kCols * kRows + r;
 #pragma unroll
         for (int s = 0; s < kBlocks; ++s)
 #pragma unroll
-          for (int j = 0; j < kCols; ++j) p[(s * HALF + j) * kRows] = sum[s][j];
-        continue;
+          for (int j = 0; j < kCols; ++j) dst[(s * HALF + j) * kRows] = sum[s][j];
+        break;
       }
       copies_wait();
       __syncwarp();
@@ -506,6 +570,54 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   copies_wait();
+  __syncwarp();
+  // A cut tile: each of the cluster's CTAs adds and finishes its share of the
+  // columns. (Every thread of the cluster comes here, after a wait that ran out
+  // too.)
+  if ((int)(blockIdx.x / a.ks) < a.cut) {
+    cluster_sync();
+    if (warp >= kEpiWarp0) {
+      const int mine = warp - kEpiWarp0, q = mine & 3, r = q * 32 + lane, rank = cluster_rank();
+      const int tile = a.waves * gridDim.x + blockIdx.x / a.ks;
+      const int span = kBand * a.n_tiles, band = tile / span, w = tile - band * span;
+      const int width = min(kBand, a.m_tiles - band * kBand);
+      const int m0 = (band * kBand + w % width) * kBlocks * HALF, n = w / width * kOuts + (GATED ? out_of_row(r) : r);
+      const bool in = n < a.N, up = GATED && (lane & 16) != 0;
+      const float b0 = in ? a.b_scale0[n] : 0.f, b1 = GATED && in ? a.b_scale1[n] : 0.f;
+      const int cols = min(kBlocks * HALF, a.M - m0);  // of the tile that exist
+      const int c0 = rank * cols / a.ks, c1 = (rank + 1) * cols / a.ks;
+      constexpr int kAtOnce = 4;
+      // the two warps of a lane quarter take every second group of columns
+      for (int c = c0 + (mine >> 2) * kAtOnce; c < c1; c += 2 * kAtOnce) {
+        int sum[kAtOnce] = {};
+        float sa[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) sa[j] = a.a_scale[m0 + min(c + j, c1 - 1)];
+        const uint32_t at = smem_u32(smem) + (uint32_t)(c * kRows + r) * 4;
+        for (int z = 0; z < a.ks; ++z)
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j)
+            if (c + j < c1) sum[j] += ld_cluster(at + j * kRows * 4, z);
+        if (!GATED) {
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j)
+            if (in && c + j < c1) i8_store(a.out, (size_t)(m0 + c + j) * a.ldo + n, a.out_bf16, i8_value(sum[j], sa[j], b0));
+        } else {
+          // as above: the gate lane two columns, the up lane two
+#pragma unroll
+          for (int j = 0; j < kAtOnce / 2; ++j) {
+            const int own = up ? sum[j + 2] : sum[j];
+            const int other = __shfl_xor_sync(0xffffffffu, up ? sum[j] : sum[j + 2], 16);
+            const int k = c + j + (up ? 2 : 0);
+            const float f = up ? sa[j + 2] : sa[j];
+            const float y = siluf_(i8_value(up ? other : own, f, b0)) * i8_value(up ? own : other, f, b1);
+            if (in && k < c1) i8_store(a.out, (size_t)(m0 + k) * a.ldo + n, a.out_bf16, y);
+          }
+        }
+      }
+    }
+    cluster_sync();
+  }
   tc_fence_before();
   __syncthreads();
   if (*abort_flag && threadIdx.x == 0) {
@@ -541,42 +653,78 @@ __global__ void __launch_bounds__(256) i8_widen_kernel(I8WidenArgs a) {
   st_global_v4(dst + 8, v[4], v[5], v[6], v[7]);
 }
 
-// The splits' sums of one output (two, gated) added and finished; a thread an
-// output, a block the columns of a tile and two (gated: four) of its rows.
-template <bool GATED>
-__global__ void __launch_bounds__(256) i8_split_sum_kernel(I8TcArgs a, int rows) {
-  pdl_wait();
-  pdl_trigger();
-  constexpr int kOuts = GATED ? kRows / 2 : kRows, kPer = 256 / kOuts;
-  const int r = threadIdx.x % kOuts;
-  const int groups = (rows + kPer - 1) / kPer;
-  const int tile = blockIdx.x / groups, j = (blockIdx.x % groups) * kPer + threadIdx.x / kOuts;
-  int mt, nt;
-  tile_at(tile, a.m_tiles, a.n_tiles, mt, nt);
-  const int m = mt * rows + j, n = nt * kOuts + r;
-  if (m >= a.M || n >= a.N) return;
-  const size_t plane = (size_t)a.m_tiles * a.n_tiles * rows * kRows;
-  const int* p = a.partial + ((size_t)tile * rows + j) * kRows + (GATED ? row_of_out(r) : r);
-  int s0 = 0, s1 = 0;
-#pragma unroll 8
-  for (int z = 0; z < a.ksplit; ++z) {
-    s0 += __ldcg(p + z * plane);
-    if (GATED) s1 += __ldcg(p + z * plane + 16);
+constexpr int kMaxCluster = 8;
+constexpr int kCutCost = 5;  // of a cut tile's end, in steps
+
+// Clusters of ks CTAs that fit the device at a time.
+template <int KIND, int HALF, bool GATED>
+int clusters_of(int ks) {
+  static int known[64][kMaxCluster + 1] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (known[dev][ks] == 0) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = ks;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(tc_sm_count() / ks * ks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Plan<HALF>::kBytes;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, i8_tc_kernel<KIND, HALF, GATED>, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = -1;  // none
+    }
+    known[dev][ks] = n;
   }
-  const float sa = a.a_scale[m];
-  float y = i8_value(s0, sa, a.b_scale0[n]);
-  if (GATED) y = siluf_(y) * i8_value(s1, sa, a.b_scale1[n]);
-  i8_store(a.out, (size_t)m * a.ldo + n, a.out_bf16, y);
+  return known[dev][ks];
 }
 
 template <int KIND, int HALF, bool GATED>
-cudaError_t launch_t(const I8TcMaps& m, const I8TcArgs& a, cudaStream_t st) {
+cudaError_t launch_t(const I8TcMaps& m, I8TcArgs a, cudaStream_t st) {
   static int attr[64] = {};
-  cudaError_t e = ensure_smem_limit(i8_tc_kernel<KIND, HALF, GATED>, (int)Plan<HALF>::kBytes, attr);
+  const auto kernel = i8_tc_kernel<KIND, HALF, GATED>;
+  cudaError_t e = ensure_smem_limit(kernel, (int)Plan<HALF>::kBytes, attr);
   if (e != cudaSuccess) return e;
-  const int items = a.m_tiles * a.n_tiles * a.ksplit, sms = tc_sm_count();
-  return launch_pdl(i8_tc_kernel<KIND, HALF, GATED>, dim3(items < sms ? items : sms), kThreads, Plan<HALF>::kBytes,
-                    st, m.A, m.B0, m.B1, a);
+  // Whole tiles in waves over the SMs; or clusters of ks CTAs, and what is left after
+  // the full waves cut over a cluster each, where that ends sooner.
+  const int tiles = a.m_tiles * a.n_tiles, sms = tc_sm_count();
+  a.ks = 1;
+  a.cut = 0;
+  a.waves = (tiles + sms - 1) / sms;
+  int grid = tiles < sms ? tiles : sms;
+  long long best = (long long)a.waves * a.steps;
+  for (int ks = 2; ks <= kMaxCluster && 2 * ks <= a.steps && a.waves <= 3; ++ks) {
+    const int fit = clusters_of<KIND, HALF, GATED>(ks);
+    if (fit < 1) continue;
+    const int waves = tiles / (fit * ks), rest = tiles - waves * fit * ks;
+    if (rest == 0 || rest > fit) continue;
+    const long long t = (long long)waves * a.steps + (a.steps + ks - 1) / ks + kCutCost;
+    if (t < best) {
+      best = t;
+      a.ks = ks;
+      a.cut = rest;
+      grid = (waves ? fit : rest) * ks;
+    }
+  }
+  if (a.cut) a.waves = (tiles - a.cut) / grid;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = a.ks;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Plan<HALF>::kBytes;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, m.A, m.B0, m.B1, a);
 }
 template <bool GATED>
 cudaError_t launch_half(I8Kind kind, int half, const I8TcMaps& m, const I8TcArgs& a, cudaStream_t st) {
@@ -610,13 +758,6 @@ cudaError_t launch_i8_tc(I8Kind kind, int half, bool gated, const I8TcMaps& m, c
 cudaError_t launch_i8_widen(const I8WidenArgs& a, cudaStream_t st) {
   const long long n = (long long)a.rows * (a.pitch / 16);
   return launch_pdl(i8_widen_kernel, dim3((unsigned)((n + 255) / 256)), 256, 0, st, a);
-}
-
-cudaError_t launch_i8_split_sum(I8Kind kind, int half, bool gated, const I8TcArgs& a, cudaStream_t st) {
-  const int rows = half * (kind == kI8Two ? 2 : 1), per = gated ? 4 : 2;
-  const dim3 grid((unsigned)(a.m_tiles * a.n_tiles * ((rows + per - 1) / per)));
-  return gated ? launch_pdl(i8_split_sum_kernel<true>, grid, 256, 0, st, a, rows)
-               : launch_pdl(i8_split_sum_kernel<false>, grid, 256, 0, st, a, rows);
 }
 
 }  // namespace moe

@@ -357,10 +357,10 @@ enum I8Kind { kI8One = 0, kI8Two = 1 };
 struct I8TcArgs {
   const float *a_scale, *b_scale0, *b_scale1;
   void* out;
-  int* partial;        // ksplit > 1: [ksplit][tiles][rows of A in a tile][128]
   Ctrl* ctrl;
   int M, N, steps;     // steps: blocks of 128 k
-  int m_tiles, n_tiles, ksplit, out_bf16;
+  int m_tiles, n_tiles, out_bf16;
+  int waves, cut, ks;  // set by the launcher: whole tiles per CTA, tiles cut over a cluster of ks CTAs each
   long long ldo;
   uint64_t wait_ns;
   int stall;
@@ -373,8 +373,6 @@ bool i8_make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
                  uint32_t box_rows);
 cudaError_t launch_i8_tc(I8Kind kind, int half, bool gated, const I8TcMaps& m, const I8TcArgs& a,
                          cudaStream_t st);
-// Adds the splits' sums of a product (ksplit > 1) and finishes them.
-cudaError_t launch_i8_split_sum(I8Kind kind, int half, bool gated, const I8TcArgs& a, cudaStream_t st);
 
 // Raises `kernel`'s dynamic shared-memory opt-in limit to at least `bytes`
 // on the current device; `limits` holds the value set so far per device

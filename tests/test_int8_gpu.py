@@ -48,11 +48,13 @@ def check_product(M, N, K, gated, dtype, seed=0, lo=-127, hi=127):
 
 
 # one to eight rows stream, more run on the tensor cores: 16, 32, 64 and 128 rows a block, two blocks a tile
-# where there are tiles enough (257 x 19400), k split where there are few
+# where there are tiles enough (257 x 19400); few tiles are cut along k over clusters, several waves of tiles with
+# steps odd in number share the rings (100 x 30000 x 333), and a last wave may be cut behind whole ones
 SHAPES = [(1, 1, 1), (1, 16, 16), (3, 17, 63), (8, 128, 64), (8, 130, 1000), (7, 4096, 4097), (2, 33, 14336),
           (9, 1, 1), (9, 128, 128), (16, 129, 127), (17, 1000, 1024), (33, 255, 1025), (64, 4096, 2048),
           (65, 300, 300), (128, 128, 4096), (129, 640, 129), (333, 1001, 1400), (257, 19400, 513),
-          (1024, 2561, 1111), (700, 9800, 1100)]
+          (1024, 2561, 1111), (700, 9800, 1100), (100, 30000, 333), (16, 41000, 600), (50, 25000, 4096),
+          (20, 12300, 4200), (200, 2000, 10000), (128, 5632, 2048)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])

@@ -198,15 +198,18 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
   if (!ok && (threadIdx.x & 31) == 0) give_up(a, abort_flag);
   return ok;
 }
-// A ring's place: stage and parity after n uses.
+// A ring's place, of N stages, and its phase's parity, after any number of steps
+// of `by` stages (which divides N).
+template <int N>
 struct Place {
-  int at = 0;
+  int at;
   uint32_t ph = 0;
-  __device__ __forceinline__ void next(int n) {
-    if (++at == n) {
-      at = 0;
-      ph ^= 1u;
-    }
+  __device__ __forceinline__ explicit Place(int first = 0) : at(first) {}
+  __device__ __forceinline__ void next(int by = 1) {
+    at += by;
+    const bool round = at >= N;
+    at -= round ? N : 0;
+    ph ^= round ? 1u : 0u;
   }
 };
 
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Before the wait for the kernel before this one: that is the same call's
       // widening of the tokens, and what is older has completed.
       if (lane == 0) {
-        Place p;
+        Place<P::kW> p;
         bool alive = true;
         Item it;
         for (Walk walk; alive && walk.next(a, it);) {
@@ -296,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               tma_load_2d(dst, &tmB0, &wfull[p.at], kb * kStep, it.nt * kOuts);
             }
-            p.next(P::kW);
+            p.next();
           }
         }
       }
@@ -305,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       pdl_wait();
       pdl_trigger();
       if (lane == 0) {
-        Place p;
+        Place<P::kT> p;
         bool alive = true;
         Item it;
         for (Walk walk; alive && walk.next(a, it);) {
@@ -318,58 +321,60 @@ __global__ void __launch_bounds__(kThreads, 1)
               mbar_expect_tx(&tfull[p.at], P::kStageT);
               tma_load_2d(dst, &tmA, &tfull[p.at], kb * kStep, row);
               tma_load_2d(dst + P::kStageT / 2, &tmA, &tfull[p.at], kb * kStep + kStep / 2, row);
-              p.next(P::kT);
+              p.next();
             }
           }
         }
       }
     } else if (lane == 0) {
       // --------------------------------------------------------------- issuers
+      // An issuer has a block of tokens (kI8Two), or the even or the odd steps of all
+      // items together, and so every second stage and slot. (A barrier's parity tells
+      // two phases apart: an issuer that came to a stage whose last use was the
+      // other's could take the phase before that use for its own.) The issuer
+      // with an item's first step has the item's first accumulator.
       const int me = warp - 1;
-      Place tp, sp;  // token stage and weight slot
-      if (KIND == kI8Two && me) tp.next(P::kT);
-      // kI8One: an issuer has the even or the odd steps of all items together, and so
-      // every second stage and slot. (Their barriers tell two phases apart: an
-      // issuer that came to a stage whose last use was the other's could take the
-      // phase before that use for its own.) The issuer with an item's first step
-      // has the item's first accumulator.
+      constexpr int kBy = KIND == kI8Two ? 1 : 2;  // steps from one of its own to the next
+      Place<P::kT> tp(me);
+      Place<P::kSlots> sp(KIND == kI8Two ? 0 : me);
       int base = 0, done = 0;  // accumulators filled and steps made before this item
       // failure self-test: wait on a barrier that only this warp completes
       bool alive = !a.stall || lane_wait(&dfull[me], 0u, a, abort_flag);
+      const uint64_t b0 = sw128_desc(smem_u32(sT));
       Item it;
       for (Walk walk; alive && walk.next(a, it);) {
         const int n = it.kb1 - it.kb0;
         const int second = KIND == kI8Two ? me : (me + done) & 1;
-        int in_chunk = 0, use = base + second;
-        for (int i = 0; i < n; ++i) {
-          if (KIND == kI8Two || (i & 1) == second) {
-            const int acc = use % kAccs;
-            if (in_chunk == 0 &&
-                !(alive = lane_wait(&dempty[acc], ((use / kAccs) & 1u) ^ 1u, a, abort_flag)))
-              break;
+        int left = KIND == kI8Two ? n : (n + 1 - second) >> 1;  // own steps
+        int acc = (base + second) % kAccs;
+        uint32_t aph = ((base + second) / kAccs) & 1u;
+        while (left > 0) {
+          if (!(alive = lane_wait(&dempty[acc], aph ^ 1u, a, abort_flag))) break;
+          const uint32_t d = tmem_base + acc * P::kAccCols;
+          const int chunk = min(left, kChunk);
+          for (int i = 0; i < chunk; ++i) {
             if (!(alive = lane_wait(&sfull[sp.at], sp.ph, a, abort_flag) &&
                           lane_wait(&tfull[tp.at], tp.ph, a, abort_flag)))
               break;
             tc_fence_after();
-            const uint32_t d = tmem_base + acc * P::kAccCols;
             const uint32_t w = tmem_base + P::kSlotCol0 + sp.at * kSlotCols;
-            const uint64_t b = sw128_desc(smem_u32(sT + tp.at * P::kStageT));
+            const uint64_t b = b0 + tp.at * (P::kStageT >> 4);
             constexpr uint64_t kHalfStage = (P::kStageT / 2) >> 4;
 #pragma unroll
             for (int k = 0; k < kStep / 16; ++k)  // 16 k: 8 columns of A, 32 bytes of B's rows
               mma_f16_ta(d, w + 8 * k, b + (k >> 2) * kHalfStage + 2 * (k & 3), kIdesc,
-                         in_chunk != 0 || k != 0 ? 1u : 0u);
+                         k != 0 ? 1u : (uint32_t)i);
             mma_commit(&tempty[tp.at]);
             mma_commit(&sempty[sp.at]);
-            if (++in_chunk == kChunk || i + (KIND == kI8Two ? 1 : 2) >= n) {
-              mma_commit(&dfull[acc]);
-              in_chunk = 0;
-              use += 2;
-            }
+            tp.next(2);
+            sp.next(kBy);
           }
-          tp.next(P::kT);
-          if (KIND == kI8Two) tp.next(P::kT);
-          sp.next(P::kSlots);
+          if (!alive) break;
+          mma_commit(&dfull[acc]);
+          left -= chunk;
+          // two accumulators on, of three
+          aph ^= acc ? 1u : 0u;
+          acc = acc ? acc - 1 : 2;
         }
         base += accs_of<KIND>(n);
         done += n;
@@ -385,47 +390,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = (warp & 3) * 32 + lane;         // this thread's weight row, and TMEM lane
     const int group = (warp - kConvWarp0) >> 2;   // its half of every step's k, or of the steps
     const uint32_t tq = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + P::kSlotCol0;
-    int steps = 0;
-    Place wp, sp;
+    Place<P::kW> wp(kHalves ? 0 : group);
+    Place<P::kSlots> sp(kHalves ? 0 : group);
+    int done = 0;
     bool alive = true;
     Item it;
     for (Walk walk; alive && walk.next(a, it);) {
       const int n = it.kb1 - it.kb0;
-      for (int i = 0; i < n; ++i, ++steps) {
-        if (kHalves || (steps & 1) == group) {
-          if (!(alive = warp_wait(&wfull[wp.at], wp.ph, a, abort_flag))) break;
-          const uint8_t* row = sW + wp.at * kStageW + r * kStep;
+      for (int left = kHalves ? n : (n + 1 - ((group + done) & 1)) >> 1; left > 0; --left) {
+        if (!(alive = warp_wait(&wfull[wp.at], wp.ph, a, abort_flag))) break;
+        const uint8_t* row = sW + wp.at * kStageW + r * kStep;
 #pragma unroll
-          for (int z = 0; z < (kHalves ? 1 : 2); ++z) {
-            const int h = kHalves ? group : z;
-            uint32_t v[32];
+        for (int z = 0; z < (kHalves ? 1 : 2); ++z) {
+          const int h = kHalves ? group : z;
+          uint32_t v[32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {  // 16-byte pieces, swizzled by the row
-              const uint4 w = ld_shared_v4(row + (((h * 4 + c) ^ (r & 7)) << 4));
-              i8_to_f16(w.x, v[8 * c], v[8 * c + 1]);
-              i8_to_f16(w.y, v[8 * c + 2], v[8 * c + 3]);
-              i8_to_f16(w.z, v[8 * c + 4], v[8 * c + 5]);
-              i8_to_f16(w.w, v[8 * c + 6], v[8 * c + 7]);
-            }
-            if (kHalves || z == 1) {
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&wempty[wp.at]);
-            }
-            if (z == 0) {
-              if (!(alive = warp_wait(&sempty[sp.at], sp.ph ^ 1u, a, abort_flag))) break;
-              tc_fence_after();
-            }
-            tmem_st32(tq + sp.at * kSlotCols + h * (kSlotCols / 2), v);
+          for (int c = 0; c < 4; ++c) {  // 16-byte pieces, swizzled by the row
+            const uint4 w = ld_shared_v4(row + (((h * 4 + c) ^ (r & 7)) << 4));
+            i8_to_f16(w.x, v[8 * c], v[8 * c + 1]);
+            i8_to_f16(w.y, v[8 * c + 2], v[8 * c + 3]);
+            i8_to_f16(w.z, v[8 * c + 4], v[8 * c + 5]);
+            i8_to_f16(w.w, v[8 * c + 6], v[8 * c + 7]);
           }
-          if (!alive) break;
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sfull[sp.at]);
+          if (kHalves || z == 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&wempty[wp.at]);
+          }
+          if (z == 0) {
+            if (!(alive = warp_wait(&sempty[sp.at], sp.ph ^ 1u, a, abort_flag))) break;
+            tc_fence_after();
+          }
+          tmem_st32(tq + sp.at * kSlotCols + h * (kSlotCols / 2), v);
         }
-        wp.next(P::kW);
-        sp.next(P::kSlots);
+        if (!alive) break;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sfull[sp.at]);
+        wp.next(kHalves ? 1 : 2);
+        sp.next(kHalves ? 1 : 2);
       }
+      done += n;
     }
   } else {
     if (KIND == kI8Two)

@@ -97,8 +97,8 @@ moe_status_t product(const void* a, const float* a_scale, const void* b0, const 
   char* ws = static_cast<char*>(mm->workspace);
   I8TcMaps m{};
   if (!i8_make_map(&m.A, ws + p.wide, mm->M, mm->K, p.pitch, p.half) ||
-      !f8_make_map(&m.B0, b0, mm->N, mm->K, mm->ldb, gated ? 16 : kTileRows) ||
-      !f8_make_map(&m.B1, gated ? b1 : b0, mm->N, mm->K, mm->ldb, 16))
+      !f8_make_map(&m.B0, b0, mm->N, mm->K, mm->ldb, gated ? kTileRows / 2 : kTileRows) ||
+      !f8_make_map(&m.B1, gated ? b1 : b0, mm->N, mm->K, mm->ldb, kTileRows / 2))
     return MOE_ERR_CUDA;
   const I8WidenArgs w{static_cast<const uint8_t*>(a), ws + p.wide, mm->M, mm->K, p.pitch, mm->lda};
   cudaError_t e = run_kernel(MOE_KERNEL_I8_MATMUL, st, [&] { return launch_i8_widen(w, st); });

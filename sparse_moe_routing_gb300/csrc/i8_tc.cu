@@ -290,15 +290,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(alive = lane_wait(&wempty[p.at], p.ph ^ 1u, a, abort_flag))) break;
             uint8_t* dst = sW + p.at * kStageW;
             mbar_expect_tx(&wfull[p.at], kStageW);
-            if (GATED) {
-#pragma unroll
-              for (int i = 0; i < kRows / 32; ++i) {
-                tma_load_2d(dst + i * 32 * kStep, &tmB0, &wfull[p.at], kb * kStep, it.nt * kOuts + i * 16);
-                tma_load_2d(dst + (i * 32 + 16) * kStep, &tmB1, &wfull[p.at], kb * kStep, it.nt * kOuts + i * 16);
-              }
-            } else {
-              tma_load_2d(dst, &tmB0, &wfull[p.at], kb * kStep, it.nt * kOuts);
-            }
+            tma_load_2d(dst, &tmB0, &wfull[p.at], kb * kStep, it.nt * kOuts);
+            if (GATED) tma_load_2d(dst + kStageW / 2, &tmB1, &wfull[p.at], kb * kStep, it.nt * kOuts);
             p.next();
           }
         }
@@ -387,7 +380,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     else
       asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     // ------------------------------------------------------------------- widen
-    const int r = (warp & 3) * 32 + lane;         // this thread's weight row, and TMEM lane
+    // this thread's TMEM lane is 32 (warp % 4) + lane, its weight row as it lies in
+    // the stage the same, or gated (gate's rows before up's) as out_of_row says
+    const int r = GATED ? out_of_row((warp & 3) * 32 + lane) + (lane & 16) * 4 : (warp & 3) * 32 + lane;
     const int group = (warp - kConvWarp0) >> 2;   // its half of every step's k, or of the steps
     const uint32_t tq = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + P::kSlotCol0;
     Place<P::kW> wp(kHalves ? 0 : group);
@@ -580,17 +575,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   // columns. (Every thread of the cluster comes here, after a wait that ran out
   // too.)
   if ((int)(blockIdx.x / a.ks) < a.cut) {
+    const int mine = warp - kEpiWarp0, r = (warp & 3) * 32 + lane, rank = cluster_rank();
+    const int tile = a.waves * gridDim.x + blockIdx.x / a.ks;
+    const int span = kBand * a.n_tiles, band = tile / span, w = tile - band * span;
+    const int width = min(kBand, a.m_tiles - band * kBand);
+    const int m0 = (band * kBand + w % width) * kBlocks * HALF, n = w / width * kOuts + (GATED ? out_of_row(r) : r);
+    const bool in = n < a.N, up = GATED && (lane & 16) != 0;
+    const int cols = min(kBlocks * HALF, a.M - m0);  // of the tile that exist
+    const int c0 = rank * cols / a.ks, c1 = (rank + 1) * cols / a.ks;
+    float b0 = 0.f, b1 = 0.f;
+    if (warp >= kEpiWarp0 && in) {
+      b0 = a.b_scale0[n];
+      if (GATED) b1 = a.b_scale1[n];
+    }
     cluster_sync();
     if (warp >= kEpiWarp0) {
-      const int mine = warp - kEpiWarp0, q = mine & 3, r = q * 32 + lane, rank = cluster_rank();
-      const int tile = a.waves * gridDim.x + blockIdx.x / a.ks;
-      const int span = kBand * a.n_tiles, band = tile / span, w = tile - band * span;
-      const int width = min(kBand, a.m_tiles - band * kBand);
-      const int m0 = (band * kBand + w % width) * kBlocks * HALF, n = w / width * kOuts + (GATED ? out_of_row(r) : r);
-      const bool in = n < a.N, up = GATED && (lane & 16) != 0;
-      const float b0 = in ? a.b_scale0[n] : 0.f, b1 = GATED && in ? a.b_scale1[n] : 0.f;
-      const int cols = min(kBlocks * HALF, a.M - m0);  // of the tile that exist
-      const int c0 = rank * cols / a.ks, c1 = (rank + 1) * cols / a.ks;
       constexpr int kAtOnce = 4;
       // the two warps of a lane quarter take every second group of columns
       for (int c = c0 + (mine >> 2) * kAtOnce; c < c1; c += 2 * kAtOnce) {
@@ -599,10 +598,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) sa[j] = a.a_scale[m0 + min(c + j, c1 - 1)];
         const uint32_t at = smem_u32(smem) + (uint32_t)(c * kRows + r) * 4;
-        for (int z = 0; z < a.ks; ++z)
+        // four CTAs' sums of four columns in flight
+        for (int z0 = 0; z0 < a.ks; z0 += 4) {
+          int v[4][kAtOnce];
 #pragma unroll
-          for (int j = 0; j < kAtOnce; ++j)
-            if (c + j < c1) sum[j] += ld_cluster(at + j * kRows * 4, z);
+          for (int z = 0; z < 4; ++z)
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j)
+              v[z][j] = z0 + z < a.ks && c + j < c1 ? ld_cluster(at + j * kRows * 4, z0 + z) : 0;
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) sum[j] += v[z][j];
+        }
         if (!GATED) {
 #pragma unroll
           for (int j = 0; j < kAtOnce; ++j)

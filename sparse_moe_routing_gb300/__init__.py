@@ -731,37 +731,41 @@ class Fp8Experts:
 # ---------------------------------------------------------------------------
 # the norm in front of a layer, and 8-bit integers: codes and one fp32 scale per row
 # ---------------------------------------------------------------------------
-_current_device = None
+_int8 = _device = _raw = None
 
 
-def _on_device(*tensors):
-    """All tensors (None: not given) on the current CUDA device."""
-    global _current_device
-    if _current_device is None:
+def _here(stream):
+    """(current device, handle of the stream: the given one or the current one)."""
+    global _device, _raw
+    if _device is None:
         import torch
         torch.cuda.init()
-        _current_device = torch.cuda.current_device
-    want = _current_device()
+        _device = torch.cuda.current_device
+        _raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
+    device = _device()
+    return device, stream.cuda_stream if stream is not None else _raw(device)
+
+
+def _away(tensors, device):
     for t in tensors:
-        if t is not None and t.get_device() != want:
-            raise ValueError("tensors must be on the current CUDA device (%d), got one on %s" % (want, t.device))
+        if t is not None and t.get_device() != device:
+            raise ValueError("tensors must be on the current CUDA device (%d), got one on %s" % (device, t.device))
 
 
-def _rows_of(t, name):
-    """Values between the rows of a matrix with contiguous rows; the row length where there is one row."""
-    r, c = t.shape
+def _rows_of(t, shape, name):
+    """Values between the rows of a matrix of this shape with contiguous rows; the row length where there is one row."""
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     s0, s1 = t.stride()
-    if s1 != 1 and c > 1:
+    if s1 != 1 and shape[1] > 1:
         raise ValueError("%s must have contiguous rows" % name)
-    return s0 if r > 1 else max(s0, c)
+    return s0 if shape[0] > 1 else max(s0, shape[1])
 
 
 def _vector(t, n, name):
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
         raise ValueError("%s must be a contiguous vector of %d values, got shape %s" % (name, n, tuple(t.shape)))
-
-
-_int8 = None
 
 
 def _i8_type(t):
@@ -785,39 +789,40 @@ def add_rmsnorm(x, residual=None, gain=None, eps=1e-6, out=None, sum_out=None, c
     and out may be x or residual themselves."""
     if x.dim() != 2:
         raise ValueError("x must have two dimensions")
-    T, d = shape = x.shape
-    n = _RmsNorm(T, d, _dtype_of(x))
-    n.ldx = _rows_of(x, "x")
-    n.eps = eps
+    shape = x.shape
+    T, d = shape
+    xt, ldx = _dtype_of(x), _rows_of(x, shape, "x")
+    rt = gt = st = ot = qt = ldr = lds = ldo = ldq = 0
     pr = pg = ps = po = pq = pc = None
     if residual is not None:
-        _shape_is(residual, shape, "residual")
-        n.residual_dtype, n.ldr, pr = _dtype_of(residual), _rows_of(residual, "residual"), residual.data_ptr()
+        ldr, rt, pr = _rows_of(residual, shape, "residual"), _dtype_of(residual), residual.data_ptr()
     if gain is not None:
         _vector(gain, d, "gain")
-        n.gain_dtype, pg = _dtype_of(gain), gain.data_ptr()
+        gt, pg = _dtype_of(gain), gain.data_ptr()
     if sum_out is not None:
-        _shape_is(sum_out, shape, "sum_out")
-        n.sum_dtype, n.lds, ps = _dtype_of(sum_out), _rows_of(sum_out, "sum_out"), sum_out.data_ptr()
+        lds, st, ps = _rows_of(sum_out, shape, "sum_out"), _dtype_of(sum_out), sum_out.data_ptr()
     if out is not None:
-        _shape_is(out, shape, "out")
-        n.out_dtype, n.ldo, po = _dtype_of(out), _rows_of(out, "out"), out.data_ptr()
-    if (codes is None) != (scales is None):
-        raise ValueError("codes and scales belong together")
-    if codes is not None:
-        _shape_is(codes, shape, "codes")
+        ldo, ot, po = _rows_of(out, shape, "out"), _dtype_of(out), out.data_ptr()
+    if codes is not None or scales is not None:
+        if codes is None or scales is None:
+            raise ValueError("codes and scales belong together")
+        ldq = _rows_of(codes, shape, "codes")
         if _i8_type(codes):
-            n.codes_dtype = I8_ROW
+            qt = I8_ROW
             _scales_ok(scales, (T,), "scales")
         else:
             _codes_dtype(codes, "codes")
-            n.codes_dtype = F8_E4M3_B128
+            qt = F8_E4M3_B128
             _scales_ok(scales, (T, -(-d // 128)), "scales")
         if not scales.is_contiguous():
             raise ValueError("scales must be contiguous")
-        n.ldq, pq, pc = _rows_of(codes, "codes"), codes.data_ptr(), scales.data_ptr()
-    _on_device(x, residual, gain, sum_out, out, codes, scales)
-    _check(lib().moe_add_rmsnorm(n, x.data_ptr(), pr, pg, ps, po, pq, pc, _stream(stream)), "moe_add_rmsnorm")
+        pq, pc = codes.data_ptr(), scales.data_ptr()
+    device, handle = _here(stream)
+    _away((x, residual, gain, sum_out, out, codes, scales), device)
+    status = lib().moe_add_rmsnorm(_RmsNorm(T, d, xt, rt, gt, st, ot, qt, ldx, ldr, lds, ldo, ldq, eps), x.data_ptr(),
+                                   pr, pg, ps, po, pq, pc, handle)
+    if status:
+        raise MoEError(status, "moe_add_rmsnorm")
 
 
 def int8_empty(rows, cols, device=None):
@@ -832,15 +837,20 @@ def int8_quantize(x, codes, scales, stream=None):
     """moe_i8_quantize: rows of x [rows, cols] (float32 or bfloat16) into int8 codes and scales [rows]."""
     if x.dim() != 2:
         raise ValueError("x must have two dimensions")
-    rows, cols = x.shape
+    shape = x.shape
+    rows, cols = shape
     _i8_codes(codes, "codes")
-    _shape_is(codes, x.shape, "codes")
+    ldq = _rows_of(codes, shape, "codes")
     _scales_ok(scales, (rows,), "scales")
-    _vector(scales, rows, "scales")
-    dtype, ldx, ldq = _dtype_of(x), _rows_of(x, "x"), _rows_of(codes, "codes")
-    _on_device(x, codes, scales)
-    _check(lib().moe_i8_quantize(x.data_ptr(), dtype, ldx, rows, cols, codes.data_ptr(), ldq, scales.data_ptr(),
-                                 _stream(stream)), "moe_i8_quantize")
+    if not scales.is_contiguous():
+        raise ValueError("scales must be contiguous")
+    ldx = _rows_of(x, shape, "x")
+    dtype = _dtype_of(x)
+    device, handle = _here(stream)
+    _away((x, codes, scales), device)
+    status = lib().moe_i8_quantize(x.data_ptr(), dtype, ldx, rows, cols, codes.data_ptr(), ldq, scales.data_ptr(), handle)
+    if status:
+        raise MoEError(status, "moe_i8_quantize")
 
 
 def _i8_args(M, N, K, gated=False, out_dtype=BF16, lda=0, ldb=0, ldo=0, workspace=None):
@@ -869,45 +879,56 @@ def int8_matmul_workspace(M, N, K, gated=False, device=None, stream=None):
     return ws
 
 
-def _i8_product(a, a_scale, weights, out, workspace, stream):
-    """(arguments, structure, result, stream) of a product with one or two (codes, scale) weights."""
+def _i8_weight(b, b_scale, shape, name):
+    """The row pitch of a product's weight; what does not fit raises."""
+    _i8_codes(b, name)
+    ld = _rows_of(b, shape, name)
+    _scales_ok(b_scale, shape[:1], name + "_scale")
+    if not b_scale.is_contiguous():
+        raise ValueError("%s_scale must be contiguous" % name)
+    return ld
+
+
+def _i8_product(a, a_scale, b, b_scale, up, up_scale, out, workspace, stream):
+    """(structure, stream's handle) of a product with one weight or two; what does not fit raises."""
     _i8_codes(a, "a")
-    M, K = a.shape
-    pitches = []
-    args = [a.data_ptr(), a_scale.data_ptr()]
-    for name, b, b_scale in weights:
-        _i8_codes(b, name)
-        N = weights[0][1].shape[0]
-        _shape_is(b, (N, K), name)
-        _scales_ok(b_scale, (N,), name + "_scale")
-        _vector(b_scale, N, name + "_scale")
-        pitches.append(_rows_of(b, name))
-        args += [b.data_ptr(), b_scale.data_ptr()]
-    if pitches[-1] != pitches[0]:
+    shape = a.shape
+    M, K = shape
+    first = "b" if up is None else "gate"
+    _i8_codes(b, first)
+    N = b.shape[0]
+    ldb = _i8_weight(b, b_scale, (N, K), first)
+    if up is not None and _i8_weight(up, up_scale, (N, K), "up") != ldb:
         raise ValueError("gate and up must have the same row pitch")
-    _scales_ok(a_scale, (M,), "a_scale")
-    _vector(a_scale, M, "a_scale")
-    _shape_is(out, (M, N), "out")
-    m = _I8Matmul(M, N, K, _dtype_of(out), len(weights) - 1, _rows_of(a, "a"), pitches[0], _rows_of(out, "out"),
-                  workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _on_device(a, a_scale, out, workspace, *(t for w in weights for t in w[1:]))
-    return args, m, out.data_ptr(), _stream(stream)
+    _scales_ok(a_scale, shape[:1], "a_scale")
+    lda, ldo = _rows_of(a, shape, "a"), _rows_of(out, (M, N), "out")
+    if not (a_scale.is_contiguous() and workspace.is_contiguous()):
+        raise ValueError("a_scale and workspace must be contiguous")
+    m = _I8Matmul(M, N, K, _dtype_of(out), 0 if up is None else 1, lda, ldb, ldo, workspace.data_ptr(),
+                  workspace.numel() * workspace.element_size())
+    device, handle = _here(stream)
+    _away((a, a_scale, b, b_scale, up, up_scale, out, workspace), device)
+    return m, handle
 
 
 def int8_matmul(a, a_scale, b, b_scale, out, workspace, stream=None):
     """moe_i8_matmul: out [M, N] = (a [M, K] b [N, K]^T) a_scale [M] b_scale [N], int8 codes, the sum exact; out float32
     or bfloat16. K at most 131071."""
-    args, m, p, st = _i8_product(a, a_scale, [("b", b, b_scale)], out, workspace, stream)
-    _check(lib().moe_i8_matmul(*args, m, p, st), "moe_i8_matmul")
+    m, handle = _i8_product(a, a_scale, b, b_scale, None, None, out, workspace, stream)
+    status = lib().moe_i8_matmul(a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), m, out.data_ptr(),
+                                 handle)
+    if status:
+        raise MoEError(status, "moe_i8_matmul")
 
 
 def int8_gated_matmul(a, a_scale, gate, gate_scale, up, up_scale, out, workspace, stream=None):
     """moe_i8_gated_matmul: out [M, N] = SiLU(g) * u, g and u the products of a with gate and up [N, K] as by
-    int8_matmul, in fp32."""
-    args, m, p, st = _i8_product(a, a_scale, [("gate", gate, gate_scale), ("up", up, up_scale)], out, workspace, stream)
-    _check(lib().moe_i8_gated_matmul(*args, m, p, st), "moe_i8_gated_matmul")
+    int8_matmul, in fp32. gate and up have the same row pitch."""
+    m, handle = _i8_product(a, a_scale, gate, gate_scale, up, up_scale, out, workspace, stream)
+    status = lib().moe_i8_gated_matmul(a.data_ptr(), a_scale.data_ptr(), gate.data_ptr(), gate_scale.data_ptr(),
+                                       up.data_ptr(), up_scale.data_ptr(), m, out.data_ptr(), handle)
+    if status:
+        raise MoEError(status, "moe_i8_gated_matmul")
 
 
 class _Int8Weight:

@@ -63,7 +63,7 @@ MmPlan mm_plan(const moe_i8_matmul_t& m) {
   const int rows = p.half * (p.kind == kI8Two ? 2 : 1);
   p.m_tiles = (m.M + rows - 1) / rows;
   p.pitch = (m.K + 15) / 16 * 16;
-  p.total = p.wide + align256((size_t)m.M * p.pitch * 2);
+  if (m.M > kI8FusedRows) p.total += align256((size_t)m.M * p.pitch * 2);
   return p;
 }
 
@@ -95,15 +95,23 @@ moe_status_t product(const void* a, const float* a_scale, const void* b0, const 
     return cuda_status(run_kernel(MOE_KERNEL_I8_MATMUL, st, [&] { return launch_i8_few(f, gated != 0, st); }));
   }
   char* ws = static_cast<char*>(mm->workspace);
+  const bool fused = mm->M <= kI8FusedRows;
   I8TcMaps m{};
-  if (!i8_make_map(&m.A, ws + p.wide, mm->M, mm->K, p.pitch, p.half) ||
+  if ((!fused && !i8_make_map(&m.A, ws + p.wide, mm->M, mm->K, p.pitch, p.half)) ||
       !f8_make_map(&m.B0, b0, mm->N, mm->K, mm->ldb, gated ? kTileRows / 2 : kTileRows) ||
       !f8_make_map(&m.B1, gated ? b1 : b0, mm->N, mm->K, mm->ldb, kTileRows / 2))
     return MOE_ERR_CUDA;
-  const I8WidenArgs w{static_cast<const uint8_t*>(a), ws + p.wide, mm->M, mm->K, p.pitch, mm->lda};
-  cudaError_t e = run_kernel(MOE_KERNEL_I8_MATMUL, st, [&] { return launch_i8_widen(w, st); });
-  if (e != cudaSuccess) return MOE_ERR_CUDA;
+  if (fused) {
+    m.A = m.B0;  // (not read)
+  } else {
+    const I8WidenArgs w{static_cast<const uint8_t*>(a), ws + p.wide, mm->M, mm->K, p.pitch, mm->lda};
+    const cudaError_t e = run_kernel(MOE_KERNEL_I8_MATMUL, st, [&] { return launch_i8_widen(w, st); });
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
+  }
   I8TcArgs g{};
+  g.a = static_cast<const uint8_t*>(a);
+  g.lda = mm->lda;
+  g.K = mm->K;
   g.a_scale = a_scale;
   g.b_scale0 = s0;
   g.b_scale1 = s1;

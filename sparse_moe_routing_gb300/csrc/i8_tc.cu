@@ -12,9 +12,12 @@
 // gate and the same 64 of up, 16 and 16 in turn), the tokens the n side. Weights come by TMA as
 // 8-bit codes, 128 x 128 a step; eight warps widen them, a thread half a row,
 // and write them to TMEM, from where tcgen05.mma takes its first operand: the
-// widened weights cost no shared memory traffic. The tokens are few bytes and
-// are widened once, by a launch before this one, into the workspace, and come by
-// TMA as fp16.
+// widened weights cost no shared memory traffic. Up to 16 tokens are few bytes
+// beside the weights, and the same warps widen them into shared memory on the
+// way; more are widened once, by a launch before this one, into the workspace,
+// and come by TMA as fp16 (us, on the way / before: 16 x 4096 x 4096 9.7 / 10.6,
+// 32 x 2048 x 2048 7.9 / 8.4, but 32 x 4096 x 14336 20.0 / 18.5, 64 x 4096 x 14336
+// 25.4 / 20.6).
 //
 // Two threads issue the MMAs: what an issuer does between two steps (two waits,
 // two commits) takes longer than the step's MMAs leave. With one block of tokens
@@ -62,8 +65,12 @@ struct Plan {
   static constexpr int kSlots = HALF == 128 ? 2 : 4;
   // stages of the two rings, up to about 200 KB
   static constexpr int kStageT = HALF * kStep * 2;
-  static constexpr int kT = HALF == 128 ? 4 : HALF == 64 ? 6 : 8;
+  // Few tokens are widened by this kernel, into stages that go with the slots of
+  // widened weights.
+  static constexpr bool kFused = HALF <= kI8FusedRows;
+  static constexpr int kT = kFused || HALF == 128 ? 4 : HALF == 64 ? 6 : 8;
   static constexpr int kW = HALF == 128 ? 4 : HALF == 64 ? 6 : HALF == 32 ? 8 : 10;
+  static_assert(!kFused || kT == kSlots, "a stage of tokens per slot");
   static constexpr int kCols = HALF / 2;  // columns of an accumulator that an epilogue warp reads
   static constexpr size_t kToken = 0;
   static constexpr size_t kWeight = kToken + (size_t)kT * kStageT;
@@ -213,6 +220,22 @@ struct Place {
   }
 };
 
+// 16 codes at column k of N rows, 16 rows apart, of which `rows` exist (zeros
+// past them and past column K).
+template <int N>
+__device__ __forceinline__ void load_codes(uint4 (&c)[N], const uint8_t* row, long long lda, int rows, int k, int K) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    c[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (16 * i < rows) {
+      if (k + 16 <= K)
+        c[i] = __ldg(reinterpret_cast<const uint4*>(row + 16 * i * lda + k));
+      else
+        c[i] = i8_load16(row + 16 * i * lda, k, K);
+    }
+  }
+}
+
 template <int KIND, int HALF, bool GATED>
 __global__ void __launch_bounds__(kThreads, 1)
     i8_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
@@ -272,6 +295,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  if (P::kFused) {
+    pdl_wait();
+    pdl_trigger();
+  }
+
   if (warp < kConvWarp0) {
     if (KIND == kI8Two)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
@@ -279,8 +307,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 0) {
       // --------------------------------------------------------------- weights
-      // Before the wait for the kernel before this one: that is the same call's
-      // widening of the tokens, and what is older has completed.
+      // (Without kFused before the wait for the kernel before this one: that is the
+      // same call's widening of the tokens, and what is older has completed.)
       if (lane == 0) {
         Place<P::kW> p;
         bool alive = true;
@@ -298,23 +326,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 3) {
       // ---------------------------------------------------------------- tokens
-      pdl_wait();
-      pdl_trigger();
-      if (lane == 0) {
-        Place<P::kT> p;
-        bool alive = true;
-        Item it;
-        for (Walk walk; alive && walk.next(a, it);) {
-          for (int kb = it.kb0; kb < it.kb1 && alive; ++kb) {
+      if (!P::kFused) {
+        pdl_wait();
+        pdl_trigger();
+        if (lane == 0) {
+          Place<P::kT> p;
+          bool alive = true;
+          Item it;
+          for (Walk walk; alive && walk.next(a, it);) {
+            for (int kb = it.kb0; kb < it.kb1 && alive; ++kb) {
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b) {
-              if (!(alive = lane_wait(&tempty[p.at], p.ph ^ 1u, a, abort_flag))) break;
-              uint8_t* dst = sT + p.at * P::kStageT;
-              const int row = (it.mt * kBlocks + b) * HALF;
-              mbar_expect_tx(&tfull[p.at], P::kStageT);
-              tma_load_2d(dst, &tmA, &tfull[p.at], kb * kStep, row);
-              tma_load_2d(dst + P::kStageT / 2, &tmA, &tfull[p.at], kb * kStep + kStep / 2, row);
-              p.next();
+              for (int b = 0; b < kBlocks; ++b) {
+                if (!(alive = lane_wait(&tempty[p.at], p.ph ^ 1u, a, abort_flag))) break;
+                uint8_t* dst = sT + p.at * P::kStageT;
+                const int row = (it.mt * kBlocks + b) * HALF;
+                mbar_expect_tx(&tfull[p.at], P::kStageT);
+                tma_load_2d(dst, &tmA, &tfull[p.at], kb * kStep, row);
+                tma_load_2d(dst + P::kStageT / 2, &tmA, &tfull[p.at], kb * kStep + kStep / 2, row);
+                p.next();
+              }
             }
           }
         }
@@ -347,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int chunk = min(left, kChunk);
           for (int i = 0; i < chunk; ++i) {
             if (!(alive = lane_wait(&sfull[sp.at], sp.ph, a, abort_flag) &&
-                          lane_wait(&tfull[tp.at], tp.ph, a, abort_flag)))
+                          (P::kFused || lane_wait(&tfull[tp.at], tp.ph, a, abort_flag))))
               break;
             tc_fence_after();
             const uint32_t w = tmem_base + P::kSlotCol0 + sp.at * kSlotCols;
@@ -357,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < kStep / 16; ++k)  // 16 k: 8 columns of A, 32 bytes of B's rows
               mma_f16_ta(d, w + 8 * k, b + (k >> 2) * kHalfStage + 2 * (k & 3), kIdesc,
                          k != 0 ? 1u : (uint32_t)i);
-            mma_commit(&tempty[tp.at]);
+            if (!P::kFused) mma_commit(&tempty[tp.at]);
             mma_commit(&sempty[sp.at]);
             tp.next(2);
             sp.next(kBy);
@@ -390,9 +420,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     int done = 0;
     bool alive = true;
     Item it;
+    // kFused: 16 codes of a step of every 16th token, eight lanes a token, so that a
+    // load touches four lines
+    constexpr int kTok = P::kFused ? HALF / 16 : 1;
+    const int tok = (threadIdx.x & 127) >> 3, piece = threadIdx.x & 7;
+    uint4 codes[kTok];
     for (Walk walk; alive && walk.next(a, it);) {
       const int n = it.kb1 - it.kb0;
-      for (int left = kHalves ? n : (n + 1 - ((group + done) & 1)) >> 1; left > 0; --left) {
+      const int first = (group + done) & 1;
+      const uint8_t* tokens = nullptr;
+      int k = 0, rows = 0;
+      if (P::kFused) {
+        rows = a.M - it.mt * HALF - tok;
+        tokens = a.a + (long long)(it.mt * HALF + tok) * a.lda;
+        k = (it.kb0 + first) * kStep + piece * 16;
+        if (first < n) load_codes(codes, tokens, a.lda, rows, k, a.K);
+      }
+      for (int left = kHalves ? n : (n + 1 - first) >> 1; left > 0; --left) {
         if (!(alive = warp_wait(&wfull[wp.at], wp.ph, a, abort_flag))) break;
         const uint8_t* row = sW + wp.at * kStageW + r * kStep;
 #pragma unroll
@@ -418,6 +462,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st32(tq + sp.at * kSlotCols + h * (kSlotCols / 2), v);
         }
         if (!alive) break;
+        if (P::kFused) {
+          // fp16 rows of 128 bytes, their pieces of eight values swizzled by the row;
+          // the second 64 k behind the first. Lanes of the one and of the other write
+          // their two pieces in opposite order, to different banks.
+          const int swap = piece >> 2;
+          uint8_t* stage = sT + sp.at * P::kStageT + swap * (P::kStageT / 2) + tok * 128;
+          const int at = (piece & 3) * 2;
+#pragma unroll
+          for (int i = 0; i < kTok; ++i) {
+            const uint4 w = codes[i];
+            uint32_t v[8];
+            i8_to_f16(w.x, v[0], v[1]);
+            i8_to_f16(w.y, v[2], v[3]);
+            i8_to_f16(w.z, v[4], v[5]);
+            i8_to_f16(w.w, v[6], v[7]);
+            uint8_t* box = stage + i * 16 * 128;  // (16 rows on the swizzle is the same)
+            uint8_t* p0 = box + ((at ^ (tok & 7)) << 4);
+            uint8_t* p1 = box + (((at + 1) ^ (tok & 7)) << 4);
+            st_shared_v4(swap ? p1 : p0, swap ? v[4] : v[0], swap ? v[5] : v[1], swap ? v[6] : v[2],
+                         swap ? v[7] : v[3]);
+            st_shared_v4(swap ? p0 : p1, swap ? v[0] : v[4], swap ? v[1] : v[5], swap ? v[2] : v[6],
+                         swap ? v[3] : v[7]);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          k += 2 * kStep;
+          if (left > 1) load_codes(codes, tokens, a.lda, rows, k, a.K);
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();

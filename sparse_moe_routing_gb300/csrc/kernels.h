@@ -330,6 +330,7 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st);
 
 // 8-bit integer products (i8_few.cu, i8_tc.cu).
 constexpr int kI8FewRows = 8;
+constexpr int kI8FusedRows = 16;  // rows up to which the tensor-core kernel widens them itself
 constexpr int kI8MaxK = 131071;  // 2^14 a product: the sums stay below 2^31
 struct I8FewArgs {
   const uint8_t* a;                  // [M][lda]
@@ -355,10 +356,12 @@ cudaError_t launch_i8_widen(const I8WidenArgs& a, cudaStream_t st);
 // gate and of up) by one or two blocks of `half` rows of A.
 enum I8Kind { kI8One = 0, kI8Two = 1 };
 struct I8TcArgs {
+  const uint8_t* a;    // the codes themselves [M][lda], for up to kI8FusedRows rows
   const float *a_scale, *b_scale0, *b_scale1;
   void* out;
   Ctrl* ctrl;
-  int M, N, steps;     // steps: blocks of 128 k
+  int M, N, K, steps;  // steps: blocks of 128 k
+  long long lda;
   int m_tiles, n_tiles, out_bf16;
   int waves, cut, ks;  // set by the launcher: whole tiles per CTA, tiles cut over a cluster of ks CTAs each
   long long ldo;

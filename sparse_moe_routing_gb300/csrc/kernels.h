@@ -341,7 +341,7 @@ struct I8FewArgs {
   long long lda, ldb, ldo;
   int ks;                            // set by the launcher
 };
-cudaError_t launch_i8_few(I8FewArgs a, bool gated, cudaStream_t st);
+cudaError_t launch_i8_few(const I8FewArgs& a, bool gated, cudaStream_t st);
 
 // Rows of codes as fp16 values [rows][pitch], pitch = cols rounded up to 16.
 struct I8WidenArgs {

@@ -162,15 +162,17 @@ struct Walk {
     return true;
   }
 };
+constexpr int kMaxCluster = 8;
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// A 32-bit value at this CTA's shared address `addr` in the cluster's CTA `rank`.
-__device__ __forceinline__ int ld_cluster(uint32_t addr, int rank) {
-  int v;
+// Four 32-bit values at this CTA's shared address `addr` in the cluster's CTA `rank`.
+__device__ __forceinline__ int4 ld_cluster4(uint32_t addr, int rank) {
+  int4 v;
   asm volatile(
-      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.s32 %0, [a];\n}"
-      : "=r"(v)
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %4, %5;\n"
+      " ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [a];\n}"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
       : "r"(addr), "r"(rank)
       : "memory");
   return v;
@@ -643,61 +645,55 @@ __global__ void __launch_bounds__(kThreads, 1)
   copies_wait();
   __syncwarp();
   // A cut tile: each of the cluster's CTAs adds and finishes its share of the
-  // columns. (Every thread of the cluster comes here, after a wait that ran out
-  // too.)
+  // tokens. (Every thread of the cluster comes here, after a wait that ran out
+  // too.) A warp takes a token at a time, a lane four rows of the tile.
   if ((int)(blockIdx.x / a.ks) < a.cut) {
-    const int mine = warp - kEpiWarp0, r = (warp & 3) * 32 + lane, rank = cluster_rank();
+    const int rank = cluster_rank(), r = lane * 4;
     const int tile = a.waves * gridDim.x + blockIdx.x / a.ks;
     const int span = kBand * a.n_tiles, band = tile / span, w = tile - band * span;
     const int width = min(kBand, a.m_tiles - band * kBand);
-    const int m0 = (band * kBand + w % width) * kBlocks * HALF, n = w / width * kOuts + (GATED ? out_of_row(r) : r);
-    const bool in = n < a.N, up = GATED && (lane & 16) != 0;
-    const int cols = min(kBlocks * HALF, a.M - m0);  // of the tile that exist
+    const int m0 = (band * kBand + w % width) * kBlocks * HALF;
+    // gated, the lane with a column's gate sums finishes the first two of the four,
+    // the lane with its up sums the others
+    const bool up = GATED && (lane & 4) != 0;
+    constexpr int kMine = GATED ? 2 : 4;
+    const int n = w / width * kOuts + (GATED ? out_of_row(r) + (up ? 2 : 0) : r);
+    const int cols = min(kBlocks * HALF, a.M - m0);  // tokens of the tile that exist
     const int c0 = rank * cols / a.ks, c1 = (rank + 1) * cols / a.ks;
-    float b0 = 0.f, b1 = 0.f;
-    if (warp >= kEpiWarp0 && in) {
-      b0 = a.b_scale0[n];
-      if (GATED) b1 = a.b_scale1[n];
+    float b0[kMine], b1[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const bool in = warp >= kEpiWarp0 && n + i < a.N;
+      b0[i] = in ? a.b_scale0[n + i] : 0.f;
+      b1[i] = GATED && in ? a.b_scale1[n + i] : 0.f;
     }
     cluster_sync();
-    if (warp >= kEpiWarp0) {
-      constexpr int kAtOnce = 4;
-      // the two warps of a lane quarter take every second group of columns
-      for (int c = c0 + (mine >> 2) * kAtOnce; c < c1; c += 2 * kAtOnce) {
-        int sum[kAtOnce] = {};
-        float sa[kAtOnce];
+    for (int c = c0 + warp - kEpiWarp0; warp >= kEpiWarp0 && c < c1; c += kEpiWarps) {
+      const float sa = a.a_scale[m0 + c];
+      const uint32_t at = smem_u32(smem) + (uint32_t)(c * kRows + r) * 4;
+      int4 v[kMaxCluster];
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) sa[j] = a.a_scale[m0 + min(c + j, c1 - 1)];
-        const uint32_t at = smem_u32(smem) + (uint32_t)(c * kRows + r) * 4;
-        // four CTAs' sums of four columns in flight
-        for (int z0 = 0; z0 < a.ks; z0 += 4) {
-          int v[4][kAtOnce];
+      for (int z = 0; z < kMaxCluster; ++z)
+        v[z] = z < a.ks ? ld_cluster4(at, z) : make_int4(0, 0, 0, 0);
+      int sum[4] = {0, 0, 0, 0};
 #pragma unroll
-          for (int z = 0; z < 4; ++z)
+      for (int z = 0; z < kMaxCluster; ++z) {
+        sum[0] += v[z].x;
+        sum[1] += v[z].y;
+        sum[2] += v[z].z;
+        sum[3] += v[z].w;
+      }
+      const size_t at_out = (size_t)(m0 + c) * a.ldo + n;
 #pragma unroll
-            for (int j = 0; j < kAtOnce; ++j)
-              v[z][j] = z0 + z < a.ks && c + j < c1 ? ld_cluster(at + j * kRows * 4, z0 + z) : 0;
-#pragma unroll
-          for (int z = 0; z < 4; ++z)
-#pragma unroll
-            for (int j = 0; j < kAtOnce; ++j) sum[j] += v[z][j];
-        }
-        if (!GATED) {
-#pragma unroll
-          for (int j = 0; j < kAtOnce; ++j)
-            if (in && c + j < c1) i8_store(a.out, (size_t)(m0 + c + j) * a.ldo + n, a.out_bf16, i8_value(sum[j], sa[j], b0));
+      for (int i = 0; i < kMine; ++i) {
+        float y;
+        if (GATED) {
+          const int other = __shfl_xor_sync(0xffffffffu, up ? sum[i] : sum[i + 2], 4), own = up ? sum[i + 2] : sum[i];
+          y = siluf_(i8_value(up ? other : own, sa, b0[i])) * i8_value(up ? own : other, sa, b1[i]);
         } else {
-          // as above: the gate lane two columns, the up lane two
-#pragma unroll
-          for (int j = 0; j < kAtOnce / 2; ++j) {
-            const int own = up ? sum[j + 2] : sum[j];
-            const int other = __shfl_xor_sync(0xffffffffu, up ? sum[j] : sum[j + 2], 16);
-            const int k = c + j + (up ? 2 : 0);
-            const float f = up ? sa[j + 2] : sa[j];
-            const float y = siluf_(i8_value(up ? other : own, f, b0)) * i8_value(up ? own : other, f, b1);
-            if (in && k < c1) i8_store(a.out, (size_t)(m0 + k) * a.ldo + n, a.out_bf16, y);
-          }
+          y = i8_value(sum[i], sa, b0[i]);
         }
+        if (n + i < a.N) i8_store(a.out, at_out + i, a.out_bf16, y);
       }
     }
     cluster_sync();
@@ -737,7 +733,6 @@ __global__ void __launch_bounds__(256) i8_widen_kernel(I8WidenArgs a) {
   st_global_v4(dst + 8, v[4], v[5], v[6], v[7]);
 }
 
-constexpr int kMaxCluster = 8;
 constexpr int kCutCost = 5;  // of a cut tile's end, in steps
 
 // Clusters of ks CTAs that fit the device at a time.

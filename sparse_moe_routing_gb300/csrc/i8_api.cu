@@ -38,7 +38,7 @@ moe_status_t validate_mm(const moe_i8_matmul_t* m) {
   if (m->lda >= (1ll << 40) || m->ldb >= (1ll << 40) || m->ldo >= (1ll << 40)) return MOE_ERR_UNSUPPORTED;
   // the kernels count tiles in 32 bits
   if (m->N > (1 << 30) || m->M > (1 << 30) ||
-      ((long long)m->M / 16 + 1) * ((long long)m->N / 64 + 1) > (1ll << 24))
+      ((long long)m->M / 16 + 1) * ((long long)m->N / 64 + 1) > (1ll << 24) || (long long)m->M * m->K > (1ll << 40))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

@@ -238,7 +238,7 @@ __device__ __forceinline__ void load_codes(uint4 (&c)[N], const uint8_t* row, lo
   }
 }
 
-template <int KIND, int HALF, bool GATED>
+template <int KIND, int HALF, bool GATED, bool SHORT>
 __global__ void __launch_bounds__(kThreads, 1)
     i8_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
                  const __grid_constant__ CUtensorMap tmB1, const I8TcArgs a) {
@@ -513,6 +513,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tq = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + part * kCols;
     float* scale = reinterpret_cast<float*>(smem + P::kScale) + mine * 128;
     const bool up = GATED && (lane & 16) != 0;  // this lane's row is up's
+    // What becomes of an accumulator's sums, whole numbers up to 2^24: SHORT (K up to
+    // 1024) they are final, for kI8One after the other accumulator's are added, and
+    // stay fp32 (bits in `sum`); else they are added as integers.
+    const auto value = [](int sum, float sa, float sb) {
+      return SHORT ? __int_as_float(sum) * sa * sb : i8_value(sum, sa, sb);
+    };
     int use = 0;
     bool alive = true;
     Item it;
@@ -551,9 +557,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             // moves no use above the wait
 #pragma unroll
             for (int j = 0; j < kPiece; ++j) asm volatile("" : "+r"(v[j]));
+            if (SHORT) {
 #pragma unroll
-            for (int j = 0; j < kPiece; ++j)
-              sum[s][c * kPiece + j] += __float2int_rn(__uint_as_float(v[j]));
+              for (int j = 0; j < kPiece; ++j) {
+                int& to = sum[s][c * kPiece + j];
+                to = __float_as_int(__int_as_float(to) + __uint_as_float(v[j]));
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < kPiece; ++j)
+                sum[s][c * kPiece + j] += __float2int_rn(__uint_as_float(v[j]));
+            }
           }
           tc_fence_before();
           __syncwarp();
@@ -569,7 +583,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int s = 0; s < kBlocks; ++s)
 #pragma unroll
-          for (int j = 0; j < kCols; ++j) dst[(s * HALF + j) * kRows] = sum[s][j];
+          for (int j = 0; j < kCols; ++j)
+            dst[(s * HALF + j) * kRows] = SHORT ? __float2int_rn(__int_as_float(sum[s][j])) : sum[s][j];
         break;
       }
       copies_wait();
@@ -589,10 +604,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 8; i += 4) {
                   const float4 sa = *reinterpret_cast<const float4*>(scale + s * kCols + j + i);
-                  y[i] = i8_value(sum[s][j + i], sa.x, b0);
-                  y[i + 1] = i8_value(sum[s][j + i + 1], sa.y, b0);
-                  y[i + 2] = i8_value(sum[s][j + i + 2], sa.z, b0);
-                  y[i + 3] = i8_value(sum[s][j + i + 3], sa.w, b0);
+                  y[i] = value(sum[s][j + i], sa.x, b0);
+                  y[i + 1] = value(sum[s][j + i + 1], sa.y, b0);
+                  y[i + 2] = value(sum[s][j + i + 2], sa.z, b0);
+                  y[i + 3] = value(sum[s][j + i + 3], sa.w, b0);
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -615,8 +630,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int lo = sum[s][p + j], hi = sum[s][kCols / 2 + p + j];
                 const int own = up ? hi : lo, other = __shfl_xor_sync(0xffffffffu, up ? lo : hi, 16);
                 const float sa = scale[s * kCols + c0 + p + j];
-                const float g = i8_value(up ? other : own, sa, b0);
-                y[j] = siluf_(g) * i8_value(up ? own : other, sa, b1);
+                const float g = value(up ? other : own, sa, b0);
+                y[j] = siluf_(g) * value(up ? own : other, sa, b1);
               }
 #pragma unroll
               for (int j = 0; j < kGroup; ++j) {
@@ -736,7 +751,7 @@ __global__ void __launch_bounds__(256) i8_widen_kernel(I8WidenArgs a) {
 constexpr int kCutCost = 5;  // of a cut tile's end, in steps
 
 // Clusters of ks CTAs that fit the device at a time.
-template <int KIND, int HALF, bool GATED>
+template <int KIND, int HALF, bool GATED, bool SHORT>
 int clusters_of(int ks) {
   static int known[64][kMaxCluster + 1] = {};
   int dev = 0;
@@ -753,7 +768,7 @@ int clusters_of(int ks) {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, i8_tc_kernel<KIND, HALF, GATED>, &cfg) != cudaSuccess || n < 1) {
+    if (cudaOccupancyMaxActiveClusters(&n, i8_tc_kernel<KIND, HALF, GATED, SHORT>, &cfg) != cudaSuccess || n < 1) {
       cudaGetLastError();
       n = -1;  // none
     }
@@ -762,10 +777,10 @@ int clusters_of(int ks) {
   return known[dev][ks];
 }
 
-template <int KIND, int HALF, bool GATED>
+template <int KIND, int HALF, bool GATED, bool SHORT>
 cudaError_t launch_t(const I8TcMaps& m, I8TcArgs a, cudaStream_t st) {
   static int attr[64] = {};
-  const auto kernel = i8_tc_kernel<KIND, HALF, GATED>;
+  const auto kernel = i8_tc_kernel<KIND, HALF, GATED, SHORT>;
   cudaError_t e = ensure_smem_limit(kernel, (int)Plan<HALF>::kBytes, attr);
   if (e != cudaSuccess) return e;
   // Whole tiles in waves over the SMs; or clusters of ks CTAs, and what is left after
@@ -777,7 +792,7 @@ cudaError_t launch_t(const I8TcMaps& m, I8TcArgs a, cudaStream_t st) {
   int grid = tiles < sms ? tiles : sms;
   long long best = (long long)a.waves * a.steps;
   for (int ks = 2; ks <= kMaxCluster && 2 * ks <= a.steps && a.waves <= 3; ++ks) {
-    const int fit = clusters_of<KIND, HALF, GATED>(ks);
+    const int fit = clusters_of<KIND, HALF, GATED, SHORT>(ks);
     if (fit < 1) continue;
     const int waves = tiles / (fit * ks), rest = tiles - waves * fit * ks;
     if (rest == 0 || rest > fit) continue;
@@ -805,13 +820,20 @@ cudaError_t launch_t(const I8TcMaps& m, I8TcArgs a, cudaStream_t st) {
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, m.A, m.B0, m.B1, a);
 }
+// A kernel of its own for K of up to 1024, where blocks are large and the
+// epilogue is what takes the time (8192 x 14336 x 128 112 -> 92 us, 2048 x 14336 x
+// 512 gated 83 -> 75; asked at run time, it slowed long sums by 2.6 %).
+template <int KIND, bool GATED>
+cudaError_t launch_128(const I8TcMaps& m, const I8TcArgs& a, cudaStream_t st) {
+  return a.steps <= kChunk ? launch_t<KIND, 128, GATED, true>(m, a, st) : launch_t<KIND, 128, GATED, false>(m, a, st);
+}
 template <bool GATED>
 cudaError_t launch_half(I8Kind kind, int half, const I8TcMaps& m, const I8TcArgs& a, cudaStream_t st) {
-  if (kind == kI8Two) return half == 128 ? launch_t<kI8Two, 128, GATED>(m, a, st) : cudaErrorInvalidValue;
-  if (half == 16) return launch_t<kI8One, 16, GATED>(m, a, st);
-  if (half == 32) return launch_t<kI8One, 32, GATED>(m, a, st);
-  if (half == 64) return launch_t<kI8One, 64, GATED>(m, a, st);
-  return half == 128 ? launch_t<kI8One, 128, GATED>(m, a, st) : cudaErrorInvalidValue;
+  if (kind == kI8Two) return half == 128 ? launch_128<kI8Two, GATED>(m, a, st) : cudaErrorInvalidValue;
+  if (half == 16) return launch_t<kI8One, 16, GATED, false>(m, a, st);
+  if (half == 32) return launch_t<kI8One, 32, GATED, false>(m, a, st);
+  if (half == 64) return launch_t<kI8One, 64, GATED, false>(m, a, st);
+  return half == 128 ? launch_128<kI8One, GATED>(m, a, st) : cudaErrorInvalidValue;
 }
 
 }  // namespace

@@ -351,7 +351,7 @@ cudaError_t launch_quant(RowsArgs a, cudaStream_t st) {
   const int units = (a.cols + 255) / 256;
   const bool few = a.rows <= 2 * tc_sm_count();
   a.warp_rows = units <= 4;
-  const dim3 grid((unsigned)(a.warp_rows ? (a.rows + kWarpRows - 1) / kWarpRows : a.rows));
+  const dim3 grid((unsigned)(a.warp_rows ? ((long long)a.rows + kWarpRows - 1) / kWarpRows : a.rows));
   const int ch = a.warp_rows ? units : few && units <= 16 ? 1 : units <= 8 ? 4 : 8;
   const int threads = a.warp_rows ? 32 * kWarpRows : 32 * ((units + ch - 1) / ch);
   if (ch == 1) return launch_pdl(quant_kernel<TX, 1>, grid, threads, 0, st, a);
@@ -365,7 +365,7 @@ cudaError_t launch_ch(RowsArgs a, cudaStream_t st) {
   const int units = (a.cols + 255) / 256;
   if (units <= 4) {
     a.warp_rows = 1;
-    const dim3 grid((unsigned)((a.rows + kWarpRows - 1) / kWarpRows));
+    const dim3 grid((unsigned)(((long long)a.rows + kWarpRows - 1) / kWarpRows));
     if (units == 1) return launch_pdl(rows_kernel<TX, RES, NORM, VEC, 1>, grid, 32 * kWarpRows, 0, st, a);
     if (units == 2) return launch_pdl(rows_kernel<TX, RES, NORM, VEC, 2>, grid, 32 * kWarpRows, 0, st, a);
     return launch_pdl(rows_kernel<TX, RES, NORM, VEC, 4>, grid, 32 * kWarpRows, 0, st, a);

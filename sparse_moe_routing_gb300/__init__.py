@@ -735,10 +735,13 @@ _int8 = _device = _raw = None
 
 
 def _here(stream):
-    """(current device, handle of the stream: the given one or the current one)."""
+    """(current device, handle of the stream: the given one or the current one). Without a GPU the device is -1, a host
+    tensor's, so that arguments are looked over before the call is refused."""
     global _device, _raw
     if _device is None:
         import torch
+        if not torch.cuda.is_available():
+            return -1, None
         torch.cuda.init()
         _device = torch.cuda.current_device
         _raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -747,38 +750,58 @@ def _here(stream):
     return device, stream.cuda_stream if stream is not None else _raw(device)
 
 
-def _away(tensors, device):
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise ValueError("tensors must be on the current CUDA device (%d), got one on %s" % (device, t.device))
+def _on(t, device, name):
+    if t.get_device() != device:
+        raise ValueError("%s must be on the current CUDA device (%d), it is on %s" % (name, device, t.device))
 
 
-def _rows_of(t, shape, name):
-    """Values between the rows of a matrix of this shape with contiguous rows; the row length where there is one row."""
+def _matrix(t, shape, name, device):
+    """Values between the rows of a matrix of this shape on the current device with contiguous rows; a multiple of 16
+    where there is one row, which nothing follows."""
     if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    s0, s1 = t.stride()
-    if s1 != 1 and shape[1] > 1:
-        raise ValueError("%s must have contiguous rows" % name)
-    return s0 if shape[0] > 1 else max(s0, shape[1])
+    rows, ld = shape
+    if rows <= 1:
+        if ld > 1 and t.stride(1) != 1:
+            raise ValueError("%s must have contiguous rows" % name)
+        ld = (ld + 15) & ~15
+    elif not t.is_contiguous():
+        pitch, step = t.stride()
+        if step != 1 and ld > 1:
+            raise ValueError("%s must have contiguous rows" % name)
+        ld = pitch
+    if t.get_device() != device:
+        _on(t, device, name)
+    return ld
 
 
-def _vector(t, n, name):
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous vector of %d values, got shape %s" % (name, n, tuple(t.shape)))
+def _values(t, shape, name, device, types):
+    """(type, row pitch, address) of a float32 or bfloat16 matrix."""
+    ld = _matrix(t, shape, name, device)
+    kind = types.get(t.dtype)
+    if kind is None:
+        raise ValueError("%s: expected a float32 or bfloat16 tensor, got %s" % (name, t.dtype))
+    return kind, ld, t.data_ptr()
 
 
-def _i8_type(t):
+def _scales(t, shape, name, device, types):
+    """The address of contiguous float32 scales."""
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if types.get(t.dtype) != F32:
+        raise ValueError("%s must be float32" % name)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if t.get_device() != device:
+        _on(t, device, name)
+    return t.data_ptr()
+
+
+def _int8_type():
     global _int8
-    if _int8 is None:
-        import torch
-        _int8 = torch.int8
-    return t.dtype == _int8
-
-
-def _i8_codes(t, name):
-    if t.dim() != 2 or not _i8_type(t):
-        raise ValueError("%s must be an int8 matrix" % name)
+    import torch
+    _int8 = torch.int8
+    return _int8
 
 
 def add_rmsnorm(x, residual=None, gain=None, eps=1e-6, out=None, sum_out=None, codes=None, scales=None, stream=None):
@@ -791,36 +814,39 @@ def add_rmsnorm(x, residual=None, gain=None, eps=1e-6, out=None, sum_out=None, c
         raise ValueError("x must have two dimensions")
     shape = x.shape
     T, d = shape
-    xt, ldx = _dtype_of(x), _rows_of(x, shape, "x")
+    types = _dt or _dtypes()
+    device, handle = _here(stream)
+    xt, ldx, px = _values(x, shape, "x", device, types)
     rt = gt = st = ot = qt = ldr = lds = ldo = ldq = 0
     pr = pg = ps = po = pq = pc = None
     if residual is not None:
-        ldr, rt, pr = _rows_of(residual, shape, "residual"), _dtype_of(residual), residual.data_ptr()
+        rt, ldr, pr = _values(residual, shape, "residual", device, types)
     if gain is not None:
-        _vector(gain, d, "gain")
-        gt, pg = _dtype_of(gain), gain.data_ptr()
+        if gain.shape != (d,) or not gain.is_contiguous():
+            raise ValueError("gain must be a contiguous vector of %d values, got shape %s" % (d, tuple(gain.shape)))
+        gt = _dtype_of(gain)
+        _on(gain, device, "gain")
+        pg = gain.data_ptr()
     if sum_out is not None:
-        lds, st, ps = _rows_of(sum_out, shape, "sum_out"), _dtype_of(sum_out), sum_out.data_ptr()
+        st, lds, ps = _values(sum_out, shape, "sum_out", device, types)
     if out is not None:
-        ldo, ot, po = _rows_of(out, shape, "out"), _dtype_of(out), out.data_ptr()
+        ot, ldo, po = _values(out, shape, "out", device, types)
     if codes is not None or scales is not None:
         if codes is None or scales is None:
             raise ValueError("codes and scales belong together")
-        ldq = _rows_of(codes, shape, "codes")
-        if _i8_type(codes):
+        ldq = _matrix(codes, shape, "codes", device)
+        if codes.dtype == (_int8 or _int8_type()):
             qt = I8_ROW
-            _scales_ok(scales, (T,), "scales")
+            pc = _scales(scales, (T,), "scales", device, types)
         else:
             _codes_dtype(codes, "codes")
             qt = F8_E4M3_B128
-            _scales_ok(scales, (T, -(-d // 128)), "scales")
-        if not scales.is_contiguous():
-            raise ValueError("scales must be contiguous")
-        pq, pc = codes.data_ptr(), scales.data_ptr()
-    device, handle = _here(stream)
-    _away((x, residual, gain, sum_out, out, codes, scales), device)
-    status = lib().moe_add_rmsnorm(_RmsNorm(T, d, xt, rt, gt, st, ot, qt, ldx, ldr, lds, ldo, ldq, eps), x.data_ptr(),
-                                   pr, pg, ps, po, pq, pc, handle)
+            pc = _scales(scales, (T, -(-d // 128)), "scales", device, types)
+        pq = codes.data_ptr()
+    if device < 0:
+        raise RuntimeError("moe_add_rmsnorm needs a CUDA device")
+    status = (_lib or lib()).moe_add_rmsnorm(
+        _RmsNorm(T, d, xt, rt, gt, st, ot, qt, ldx, ldr, lds, ldo, ldq, eps), px, pr, pg, ps, po, pq, pc, handle)
     if status:
         raise MoEError(status, "moe_add_rmsnorm")
 
@@ -833,22 +859,26 @@ def int8_empty(rows, cols, device=None):
     return codes[:, :cols], torch.empty(rows, dtype=torch.float32, device=device or "cuda")
 
 
+def _i8_codes(t, name):
+    if t.dim() != 2 or t.dtype != (_int8 or _int8_type()):
+        raise ValueError("%s must be an int8 matrix" % name)
+
+
 def int8_quantize(x, codes, scales, stream=None):
     """moe_i8_quantize: rows of x [rows, cols] (float32 or bfloat16) into int8 codes and scales [rows]."""
     if x.dim() != 2:
         raise ValueError("x must have two dimensions")
     shape = x.shape
     rows, cols = shape
+    types = _dt or _dtypes()
     _i8_codes(codes, "codes")
-    ldq = _rows_of(codes, shape, "codes")
-    _scales_ok(scales, (rows,), "scales")
-    if not scales.is_contiguous():
-        raise ValueError("scales must be contiguous")
-    ldx = _rows_of(x, shape, "x")
-    dtype = _dtype_of(x)
     device, handle = _here(stream)
-    _away((x, codes, scales), device)
-    status = lib().moe_i8_quantize(x.data_ptr(), dtype, ldx, rows, cols, codes.data_ptr(), ldq, scales.data_ptr(), handle)
+    ldq = _matrix(codes, shape, "codes", device)
+    ps = _scales(scales, (rows,), "scales", device, types)
+    xt, ldx, px = _values(x, shape, "x", device, types)
+    if device < 0:
+        raise RuntimeError("moe_i8_quantize needs a CUDA device")
+    status = (_lib or lib()).moe_i8_quantize(px, xt, ldx, rows, cols, codes.data_ptr(), ldq, ps, handle)
     if status:
         raise MoEError(status, "moe_i8_quantize")
 
@@ -879,44 +909,41 @@ def int8_matmul_workspace(M, N, K, gated=False, device=None, stream=None):
     return ws
 
 
-def _i8_weight(b, b_scale, shape, name):
-    """The row pitch of a product's weight; what does not fit raises."""
-    _i8_codes(b, name)
-    ld = _rows_of(b, shape, name)
-    _scales_ok(b_scale, shape[:1], name + "_scale")
-    if not b_scale.is_contiguous():
-        raise ValueError("%s_scale must be contiguous" % name)
-    return ld
-
-
-def _i8_product(a, a_scale, b, b_scale, up, up_scale, out, workspace, stream):
-    """(structure, stream's handle) of a product with one weight or two; what does not fit raises."""
+def _i8_product(a, a_scale, out, workspace, weights, stream):
+    """(addresses of the operands, structure, address of the result, stream's handle) of a product with one weight or
+    two, (name, codes, scales) each; what does not fit raises."""
     _i8_codes(a, "a")
     shape = a.shape
     M, K = shape
-    first = "b" if up is None else "gate"
-    _i8_codes(b, first)
-    N = b.shape[0]
-    ldb = _i8_weight(b, b_scale, (N, K), first)
-    if up is not None and _i8_weight(up, up_scale, (N, K), "up") != ldb:
-        raise ValueError("gate and up must have the same row pitch")
-    _scales_ok(a_scale, shape[:1], "a_scale")
-    lda, ldo = _rows_of(a, shape, "a"), _rows_of(out, (M, N), "out")
-    if not (a_scale.is_contiguous() and workspace.is_contiguous()):
-        raise ValueError("a_scale and workspace must be contiguous")
-    m = _I8Matmul(M, N, K, _dtype_of(out), 0 if up is None else 1, lda, ldb, ldo, workspace.data_ptr(),
-                  workspace.numel() * workspace.element_size())
+    types = _dt or _dtypes()
     device, handle = _here(stream)
-    _away((a, a_scale, b, b_scale, up, up_scale, out, workspace), device)
-    return m, handle
+    lda = _matrix(a, shape, "a", device)
+    at = [a.data_ptr(), _scales(a_scale, (M,), "a_scale", device, types)]
+    ldb = N = None
+    for name, b, b_scale in weights:
+        _i8_codes(b, name)
+        if N is None:
+            N = b.shape[0]
+        ld = _matrix(b, (N, K), name, device)
+        if ldb is not None and ld != ldb:
+            raise ValueError("gate and up must have the same row pitch")
+        ldb = ld
+        at.append(b.data_ptr())
+        at.append(_scales(b_scale, (N,), name + "_scale", device, types))
+    ot, ldo, po = _values(out, (M, N), "out", device, types)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _on(workspace, device, "workspace")
+    if device < 0:
+        raise RuntimeError("an int8 product needs a CUDA device")
+    return at, _I8Matmul(M, N, K, ot, len(weights) - 1, lda, ldb, ldo, workspace.data_ptr(), workspace.nbytes), po, handle
 
 
 def int8_matmul(a, a_scale, b, b_scale, out, workspace, stream=None):
     """moe_i8_matmul: out [M, N] = (a [M, K] b [N, K]^T) a_scale [M] b_scale [N], int8 codes, the sum exact; out float32
     or bfloat16. K at most 131071."""
-    m, handle = _i8_product(a, a_scale, b, b_scale, None, None, out, workspace, stream)
-    status = lib().moe_i8_matmul(a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), m, out.data_ptr(),
-                                 handle)
+    at, m, po, handle = _i8_product(a, a_scale, out, workspace, (("b", b, b_scale),), stream)
+    status = (_lib or lib()).moe_i8_matmul(*at, m, po, handle)
     if status:
         raise MoEError(status, "moe_i8_matmul")
 
@@ -924,9 +951,9 @@ def int8_matmul(a, a_scale, b, b_scale, out, workspace, stream=None):
 def int8_gated_matmul(a, a_scale, gate, gate_scale, up, up_scale, out, workspace, stream=None):
     """moe_i8_gated_matmul: out [M, N] = SiLU(g) * u, g and u the products of a with gate and up [N, K] as by
     int8_matmul, in fp32. gate and up have the same row pitch."""
-    m, handle = _i8_product(a, a_scale, gate, gate_scale, up, up_scale, out, workspace, stream)
-    status = lib().moe_i8_gated_matmul(a.data_ptr(), a_scale.data_ptr(), gate.data_ptr(), gate_scale.data_ptr(),
-                                       up.data_ptr(), up_scale.data_ptr(), m, out.data_ptr(), handle)
+    at, m, po, handle = _i8_product(a, a_scale, out, workspace, (("gate", gate, gate_scale), ("up", up, up_scale)),
+                                    stream)
+    status = (_lib or lib()).moe_i8_gated_matmul(*at, m, po, handle)
     if status:
         raise MoEError(status, "moe_i8_gated_matmul")
 

@@ -135,6 +135,20 @@ def test_scales_of_zero_nan_and_infinity_stay_in_their_rows_and_columns():
         assert bool(got[keep][:, cols].isfinite().all()) and bool((~got[keep][:, 7].isfinite()).all())
 
 
+def test_one_row_needs_no_pitch():
+    """A single row of any length, whatever its tensor's strides say."""
+    g = gen(14)
+    K = 1001
+    a, w = (random_codes(g, 1, K)[0].clone().view(1, K) for _ in range(2))
+    assert a.stride(0) == K
+    one = torch.ones(1, device="cuda")
+    got = product(a, one, [(w, one)], torch.float32)
+    assert torch.equal(got, sums64(a, w).to(torch.float32))
+    b = random_codes(g, 40, K)
+    got = product(a, one, [(b, torch.ones(40, device="cuda"))], torch.float32)
+    assert torch.equal(got, sums64(a, b).to(torch.float32))
+
+
 def test_nothing_to_do():
     one = torch.ones(4, device="cuda")
     ws = smr.int8_matmul_workspace(64, 64, 64)

@@ -1,4 +1,8 @@
 """8-bit integer products and quantiser on the GPU against exact integer sums in fp64."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -54,7 +58,7 @@ SHAPES = [(1, 1, 1), (1, 16, 16), (3, 17, 63), (8, 128, 64), (8, 130, 1000), (7,
           (9, 1, 1), (9, 128, 128), (16, 129, 127), (17, 1000, 1024), (33, 255, 1025), (64, 4096, 2048),
           (65, 300, 300), (128, 128, 4096), (129, 640, 129), (333, 1001, 1400), (257, 19400, 513),
           (1024, 2561, 1111), (700, 9800, 1100), (100, 30000, 333), (16, 41000, 600), (50, 25000, 4096),
-          (20, 12300, 4200), (200, 2000, 10000), (128, 5632, 2048)]
+          (20, 12300, 4200), (200, 2000, 10000), (128, 5632, 2048), (600, 9740, 1300), (600, 5000, 700)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
@@ -205,8 +209,90 @@ def test_graph_and_side_stream(M, N, K):
         assert torch.equal(out, again)
 
 
+def test_two_streams_with_a_workspace_each():
+    """Products that overlap on the GPU, each with a workspace of its own."""
+    g = gen(15)
+    cases = []
+    for M, N, K in ((40, 3000, 4096), (300, 5000, 900), (5, 4000, 4096), (130, 700, 6000)):
+        a, sa = random_codes(g, M, K), random_scales(g, M, 0.02)
+        w = [(random_codes(g, N, K), random_scales(g, N, 0.001))]
+        cases.append((a, sa, w, smr.int8_matmul_workspace(M, N, K), torch.empty(M, N, device="cuda")))
+    want = [product(a, sa, w, torch.float32, ws) for a, sa, w, ws, _ in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for st, (a, sa, w, ws, out) in zip(streams, cases):
+            product(a, sa, w, torch.float32, ws, out, stream=st)
+    torch.cuda.synchronize()
+    for y, (*_, ws, out) in zip(want, cases):
+        assert torch.equal(out, y) and status(ws) == (0, 0)
+
+
+def test_captured_first():
+    """A graph whose capture is the first call of its kernels in the process (a child)."""
+    code = """
+import torch, sparse_moe_routing_gb300 as smr
+torch.manual_seed(1)
+graphs = []
+for M, N, K, gated in ((4, 64, 512, False), (12, 300, 4096, True), (200, 900, 4096, False), (300, 20000, 256, True)):
+    a = torch.randint(-127, 128, (M, K), dtype=torch.int8, device="cuda")
+    w = [torch.randint(-127, 128, (N, K), dtype=torch.int8, device="cuda") for _ in range(1 + gated)]
+    sa, sb = torch.full((M,), 1e-3, device="cuda"), torch.full((N,), 1e-3, device="cuda")
+    out = torch.zeros(M, N, device="cuda")
+    x = torch.randn(M, K, device="cuda")
+    q, qs = smr.int8_empty(M, K)
+    ws = smr.int8_matmul_workspace(M, N, K, gated=gated)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    def calls():
+        smr.add_rmsnorm(x, codes=q, scales=qs)
+        if gated:
+            smr.int8_gated_matmul(a, sa, w[0], sb, w[1], sb, out, ws)
+        else:
+            smr.int8_matmul(a, sa, w[0], sb, out, ws)
+    with torch.cuda.graph(graph):
+        calls()
+    graph.replay()
+    torch.cuda.synchronize()
+    first, fq = out.clone(), q.clone()
+    out.zero_(); q.zero_()
+    calls()
+    torch.cuda.synchronize()
+    assert torch.equal(out, first) and torch.equal(q, fq) and bool(first.any()) and bool(fq.any())
+print("same")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=240, cwd=root)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
+
+
+def test_tensors_elsewhere_are_refused():
+    one = torch.ones(4, device="cuda")
+    codes = torch.zeros(4, 64, dtype=torch.int8, device="cuda")
+    ws = smr.int8_matmul_workspace(4, 4, 64)
+    out = torch.empty(4, 4, device="cuda")
+    for bad in (dict(a=codes.cpu()), dict(a_scale=one.cpu()), dict(b=codes.cpu()), dict(b_scale=one.cpu()),
+                dict(out=out.cpu()), dict(workspace=ws.cpu())):
+        args = dict(a=codes, a_scale=one, b=codes, b_scale=one, out=out, workspace=ws)
+        args.update(bad)
+        with pytest.raises(ValueError, match="current CUDA device"):
+            smr.int8_matmul(**args)
+    with pytest.raises(ValueError, match="gain must be on"):
+        smr.add_rmsnorm(torch.zeros(4, 64, device="cuda"), gain=torch.ones(64), out=torch.zeros(4, 64, device="cuda"))
+    with pytest.raises(smr.MoEError):  # codes off 16 bytes
+        smr.int8_matmul(torch.zeros(4, 72, dtype=torch.int8, device="cuda")[:, 8:], one, codes, one, out, ws)
+
+
+def test_small_workspaces_are_refused():
+    a = torch.zeros(100, 256, dtype=torch.int8, device="cuda")
+    one, out = torch.ones(100, device="cuda"), torch.empty(100, 100, device="cuda")
+    ws = smr.int8_matmul_workspace(16, 100, 256)
+    with pytest.raises(smr.MoEError, match="WORKSPACE"):
+        smr.int8_matmul(a, one, a, one, out, ws)
+
+
 @pytest.mark.parametrize("gated", [False, True])
-@pytest.mark.parametrize("M,N,K", [(40, 500, 4096), (300, 20000, 300)])
+@pytest.mark.parametrize("M,N,K", [(40, 500, 4096), (300, 20000, 300), (12, 700, 4096)])
 def test_a_wait_that_runs_out(M, N, K, gated):
     """A stalled launch reports a timeout and returns; the next call on the same workspace is right."""
     g = gen(10)
@@ -306,6 +392,10 @@ def test_linear(rows):
     smr.int8_quantize(x, *q)
     assert torch.equal(lin(q, torch.empty(rows, 301, device="cuda")), y)
     assert lin.device_status() == (0, 0)
+    small = smr.Int8Linear(w, 4)  # (whose workspace holds the control block alone)
+    if rows <= 4:
+        assert torch.equal(small(x, torch.empty(rows, 301, device="cuda")), y)
+    assert small.device_status() == (0, 0)
     with pytest.raises(ValueError, match="made for"):
         lin(torch.zeros(101, 500, device="cuda"), torch.empty(101, 301, device="cuda"))
 

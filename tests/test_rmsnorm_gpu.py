@@ -175,3 +175,29 @@ def test_graph_and_side_stream():
         x.copy_(rows(g, 40, 2048, BF))
         graph.replay()
         check(x, r, None, 1e-6, out, total, codes, scales)
+
+
+def test_large_and_small_numbers():
+    """Rows of very large and very small values keep their scale; above 1e19 the sum of squares is infinite and f 0."""
+    d = 520
+    x = torch.randn(4, d, device="cuda")
+    x[0] *= 1e15
+    x[1] *= 1e-15
+    x[2] *= 1e-30
+    out = torch.empty_like(x)
+    codes, scales = smr.int8_empty(4, d)
+    smr.add_rmsnorm(x, eps=1e-6, out=out, codes=codes, scales=scales)
+    check(x, None, None, 1e-6, out, None, codes, scales)
+    x[3] = 1e20
+    smr.add_rmsnorm(x, eps=1e-6, out=out, codes=codes, scales=scales)
+    assert not bool(out[3].any()) and float(scales[3]) == 0.0 and bool((codes[3] == 127).all())
+
+
+def test_many_rows():
+    """More rows than the grid's other dimensions would hold, one warp each."""
+    g = gen(16)
+    x = rows(g, 300000, 24, BF)
+    codes, scales = smr.int8_empty(300000, 24)
+    out = torch.empty_like(x)
+    smr.add_rmsnorm(x, out=out, codes=codes, scales=scales)
+    check(x, None, None, 1e-6, out, None, codes, scales)

@@ -1003,8 +1003,8 @@ class Int8FeedForward:
     h = SiLU(W_gate x) * (W_up x), for up to max_rows rows. W_gate, W_up [I, d] and W_down [d, I] float32 or bfloat16.
 
     x is quantised on the way, or given as (codes, scales), as add_rmsnorm writes them; h is rounded to bfloat16 and
-    then to 8 bits with a scale per row (the bfloat16 rounding is 1/2^9 of a value, a step of the codes 1/127 of the
-    row's largest). The workspace and what lies between the products belong to the object: calls on several streams
+    then to 8 bits with a scale per row (the bfloat16 rounding is at most 2^-8 of a value, half a step of the codes
+    1/254 of the row's largest; fp32 rows would be twice the traffic). The workspace and what lies between the products belong to the object: calls on several streams
     are ordered by the caller."""
 
     def __init__(self, W_gate, W_up, W_down, max_rows, device=None):

@@ -18,6 +18,9 @@
 // mma.sync: 1 x 5632 x 2048 4.5 / 5.4, 2 x 4096 x 14336 12.4 / 13.5, but four rows of
 // it 19.4 / 13.5: dp4a loads every row of A for every lane).
 //
+// Measured, weights rotated beyond L2: 1 x 5632 x 2048 4.5 us, 8 x 4096 x 14336 13.3
+// (4.4 TB/s), gated 8 x 14336 x 4096 21.0 us (5.6 TB/s), 8 x 57344 x 8192 79 us (6.0).
+//
 // The warps of a CTA are tiles x slices of k (ks of them), whose sums are added
 // in int32 through shared memory: any order gives the same bits.
 #include "i8_common.cuh"

@@ -24,12 +24,18 @@
 // (kI8One) they take the steps in turn, with two (kI8Two) a block each, and each
 // sums on its own. Their sums rotate through three accumulators, so that one is
 // read back while two fill (two accumulators left the tensor core idle for the
-// read-back, 1400 cycles every 1024 k: the conversion to integers runs at 16 a
-// cycle).
+// read-back, some 1400 cycles of the 8200 that 1024 k take).
 //
 // Warps: 0 brings weights, 3 tokens, 1 and 2 issue, 4-11 widen, 12-19 read back,
 // scale and store. Gated, the two lanes of a warp that hold a column's gate and
 // its up sums give each other half of them.
+//
+// Bound for few tokens by the weights' stream (5.6 TB/s once it runs; start and end
+// of the kernel are 7 us: 64 x 4096 x 14336 19.5 us, gated 64 x 14336 x 4096 28.9),
+// for many by the hand-overs between widening, issue and read-back: a step's MMAs
+// are 1024 cycles, an issuer's waits, issues and commits some 1100 (8192 x 14336 x
+// 4096 553 us with 18 of widening, 1.74 PFLOP/s; gated 2048 x 14336 x 4096 286 us,
+// 1.68; the tensor pipe busy for 75 % of the cycles).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

@@ -9,10 +9,11 @@
 // codes and whatever the order.
 //
 // The weights are the m side of the products (128 rows a tile; gated: 64 rows of
-// gate and the same 64 of up, 16 and 16 in turn), the tokens the n side. Weights come by TMA as
-// 8-bit codes, 128 x 128 a step; eight warps widen them, a thread half a row,
-// and write them to TMEM, from where tcgen05.mma takes its first operand: the
-// widened weights cost no shared memory traffic. Up to 16 tokens are few bytes
+// gate and the same 64 of up, 16 and 16 in turn in TMEM), the tokens the n side.
+// Weights come by TMA as 8-bit codes, 128 x 128 a step; eight warps widen them,
+// a thread half a row or a row of every second step, and write them to TMEM, from
+// where tcgen05.mma takes its first operand: the widened weights cost no shared
+// memory traffic. Up to 16 tokens are few bytes
 // beside the weights, and the same warps widen them into shared memory on the
 // way; more are widened once, by a launch before this one, into the workspace,
 // and come by TMA as fp16 (us, on the way / before: 16 x 4096 x 4096 9.7 / 10.6,

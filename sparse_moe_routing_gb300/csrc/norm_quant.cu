@@ -13,10 +13,11 @@
 // reduction serves both. The integer quantiser of plain rows is the same kernel
 // without norm (f = 1, t = x).
 //
-// A row belongs to a group of threads (a warp where it has at most 1024
-// columns, a CTA else) and stays in its registers: x and the residual are read
-// once, everything is written once. Bound by HBM for many rows, by latency for
-// few (a load, one reduction, a store).
+// A row belongs to a group of threads (a warp where it is short and there are
+// many, a CTA else) and stays in its registers: x and the residual are read
+// once, everything is written once. Bound by HBM for many rows (8192 x 4096 bf16 +
+// fp32 residual -> int8 60 us, 6.1 TB/s; 14336 x 4096 bf16 quantised 27.5 us, 6.4
+// TB/s), by latency for few (a load, one reduction, a store: 1 x 2048 2.3 us).
 //
 // Rows that are not finite: the norm of a row with an infinity or a NaN is NaN
 // there and 0 or NaN elsewhere; an integer row gets the scale NaN and codes 0, an
@@ -168,6 +169,7 @@ __device__ __forceinline__ uint32_t int8x4(const float* v, float inv) {
   return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
 }
 
+constexpr int kFewRows = 8;  // an SM: up to here a row has a CTA, whatever its length
 constexpr float kLeastMax = 127.f * 1.17549435e-38f;  // 127 * 2^-126, an fp32 number
 
 // TX: x's type. RES: 0 no residual, 1 fp32, 2 bf16. NORM: with the factor f (and
@@ -342,15 +344,16 @@ __global__ void __launch_bounds__(512) quant_kernel(RowsArgs a) {
   if (unit0 == 0 && lane == 0) a.scales[row] = finite ? m / 127.f : __uint_as_float(kF8NanScale);
 }
 
-// Rows of up to 1024 values are a warp's, longer ones a CTA's. Eight pieces a thread
+// Many rows of up to 1024 values are a warp's each (16384 x 1024 bf16 9.8 us, a CTA
+// 17.2), others a CTA's. Eight pieces a thread
 // past 2048 values, one where rows are few: 14336 x 4096 bf16 27.5 us (four: 28.8,
 // two in the general kernel above: 36.7), 4096 x 14336 28.6 (four: 35.8 there); a warp
 // for 2048 fp32 values lost (15.3 against 13.7).
 template <typename TX>
 cudaError_t launch_quant(RowsArgs a, cudaStream_t st) {
   const int units = (a.cols + 255) / 256;
-  const bool few = a.rows <= 2 * tc_sm_count();
-  a.warp_rows = units <= 4;
+  const bool few = a.rows <= kFewRows * tc_sm_count();
+  a.warp_rows = units <= 4 && !few;
   const dim3 grid((unsigned)(a.warp_rows ? ((long long)a.rows + kWarpRows - 1) / kWarpRows : a.rows));
   const int ch = a.warp_rows ? units : few && units <= 16 ? 1 : units <= 8 ? 4 : 8;
   const int threads = a.warp_rows ? 32 * kWarpRows : 32 * ((units + ch - 1) / ch);
@@ -363,20 +366,14 @@ cudaError_t launch_quant(RowsArgs a, cudaStream_t st) {
 template <typename TX, int RES, bool NORM, bool VEC>
 cudaError_t launch_ch(RowsArgs a, cudaStream_t st) {
   const int units = (a.cols + 255) / 256;
-  if (units <= 4) {
-    a.warp_rows = 1;
-    const dim3 grid((unsigned)(((long long)a.rows + kWarpRows - 1) / kWarpRows));
-    if (units == 1) return launch_pdl(rows_kernel<TX, RES, NORM, VEC, 1>, grid, 32 * kWarpRows, 0, st, a);
-    if (units == 2) return launch_pdl(rows_kernel<TX, RES, NORM, VEC, 2>, grid, 32 * kWarpRows, 0, st, a);
-    return launch_pdl(rows_kernel<TX, RES, NORM, VEC, 4>, grid, 32 * kWarpRows, 0, st, a);
-  }
-  a.warp_rows = 0;
-  const dim3 grid((unsigned)a.rows);
-  const bool few = a.rows <= 2 * tc_sm_count();
-  // pieces a thread: one where rows are few (latency), else two while a row
-  // fits a CTA that way
-  const int ch = few && units <= 32 ? 1 : units <= 64 ? 2 : 8;
-  const int threads = 32 * ((units + ch - 1) / ch);
+  const bool few = a.rows <= kFewRows * tc_sm_count();
+  // A warp a row up to 512 columns (to 1024: 8192 x 1024 22.1 against 19.5 us) where
+  // rows are many (333 x 1001 5.8 against 2.2 us); else a CTA a row, with one piece a
+  // thread where rows are few, two while a row fits a CTA that way.
+  a.warp_rows = units <= 2 && !few;
+  const int ch = a.warp_rows ? units : few && units <= 32 ? 1 : units <= 64 ? 2 : 8;
+  const dim3 grid((unsigned)(a.warp_rows ? ((long long)a.rows + kWarpRows - 1) / kWarpRows : a.rows));
+  const int threads = a.warp_rows ? 32 * kWarpRows : 32 * ((units + ch - 1) / ch);
   if (ch == 1) return launch_pdl(rows_kernel<TX, RES, NORM, VEC, 1>, grid, threads, 0, st, a);
   if (ch == 2) return launch_pdl(rows_kernel<TX, RES, NORM, VEC, 2>, grid, threads, 0, st, a);
   return launch_pdl(rows_kernel<TX, RES, NORM, VEC, 8>, grid, threads, 0, st, a);

@@ -59,7 +59,33 @@ MmPlan mm_plan(const moe_i8_matmul_t& m) {
   p.n_tiles = (m.N + cols - 1) / cols;
   const auto tiles_of = [&](int rows) { return (long long)((m.M + rows - 1) / rows) * p.n_tiles; };
   // two blocks a tile where that leaves a tile for every second SM
-  if (m.M > 128 && 2 * tiles_of(256) >= kSms) p.kind = kI8Two;
+  if (m.M > 128 && 2 * tiles_of(256) >= kSms) {
+    p.kind = kI8Two;
+  } else if (m.M > 32) {
+    // Else the block of tokens that ends soonest by this estimate, in steps, among
+    // those of one wave of tiles: the steps of a CTA, after cutting over a
+    // cluster, and the read-back and sums behind them. us with blocks of 128 / 64 / 32:
+    // 256 x 240 x 4608 12.3 / 10.3 / 9.8, 333 x 1001 x 1400 11.2 / 9.3 / 8.7, 128 x 4911 x
+    // 1858 13.3 / 11.1 / 14.6, 4571 x 64 x 1328 15.0 / 12.8 / 14.6, 1536 x 1044 x 465 8.0 /
+    // 10.2 / 11.1, 64 x 4096 x 4096 - / 12.1 / 13.2. It takes the slower of two at 333 x
+    // 1001 x 1400.
+    const int steps = (m.K + kStepK - 1) / kStepK;
+    double best = 1e30;
+    for (int half = p.half, h = half; h >= 32; h /= 2) {
+      const long long tiles = tiles_of(h);
+      if (tiles > kSms && h < half) break;
+      int ks = tiles > 0 && tiles <= kSms ? (int)(kSms / tiles) : 1;
+      if (ks > 8) ks = 8;
+      if (ks > steps / 2) ks = steps / 2;
+      const int end = h == 32 ? 3 : h == 64 ? 5 : steps <= 8 ? 6 : 15;  // (128: sums of up to 1024 stay fp32)
+      double cost = steps + end;
+      if (ks > 1 && (double)steps / ks + end + 3 < cost) cost = (double)steps / ks + end + 3;
+      if (cost < best) {
+        best = cost;
+        p.half = h;
+      }
+    }
+  }
   const int rows = p.half * (p.kind == kI8Two ? 2 : 1);
   p.m_tiles = (m.M + rows - 1) / rows;
   p.pitch = (m.K + 15) / 16 * 16;

@@ -125,8 +125,9 @@ moe_status_t product(const void* a, const float* a_scale, const void* b0, const 
   I8TcMaps m{};
   if ((!fused && !i8_make_map(&m.A, ws + p.wide, mm->M, mm->K, p.pitch, p.half)) ||
       !f8_make_map(&m.B0, b0, mm->N, mm->K, mm->ldb, gated ? kTileRows / 2 : kTileRows) ||
-      !f8_make_map(&m.B1, gated ? b1 : b0, mm->N, mm->K, mm->ldb, kTileRows / 2))
+      (gated && !f8_make_map(&m.B1, b1, mm->N, mm->K, mm->ldb, kTileRows / 2)))
     return MOE_ERR_CUDA;
+  if (!gated) m.B1 = m.B0;  // (not read)
   if (fused) {
     m.A = m.B0;  // (not read)
   } else {

@@ -35,8 +35,9 @@
 // of the kernel are 7 us: 64 x 4096 x 14336 19.5 us, gated 64 x 14336 x 4096 28.9),
 // for many by the hand-overs between widening, issue and read-back: a step's MMAs
 // are 1024 cycles, an issuer's waits, issues and commits some 1100 (8192 x 14336 x
-// 4096 553 us with 18 of widening, 1.74 PFLOP/s; gated 2048 x 14336 x 4096 286 us,
-// 1.68; the tensor pipe busy for 75 % of the cycles).
+// 4096 553 us with 18 of widening, 1.74 PFLOP/s; gated 2048 x 14336 x 4096 285-300
+// us, 1.6-1.7; the tensor pipe busy for 75 % of the cycles), and where sums are short
+// by the epilogue's stores (5632 x 8432 x 384 in fp32 50 us, 31 without them).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -759,10 +760,8 @@ constexpr int kCutCost = 5;  // of a cut tile's end, in steps
 
 // Clusters of ks CTAs that fit the device at a time.
 template <int KIND, int HALF, bool GATED, bool SHORT>
-int clusters_of(int ks) {
+int clusters_of(int dev, int ks) {
   static int known[64][kMaxCluster + 1] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   if (known[dev][ks] == 0) {
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -793,13 +792,15 @@ cudaError_t launch_t(const I8TcMaps& m, I8TcArgs a, cudaStream_t st) {
   // Whole tiles in waves over the SMs; or clusters of ks CTAs, and what is left after
   // the full waves cut over a cluster each, where that ends sooner.
   const int tiles = a.m_tiles * a.n_tiles, sms = tc_sm_count();
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;  // (below 64: ensure_smem_limit)
   a.ks = 1;
   a.cut = 0;
   a.waves = (tiles + sms - 1) / sms;
   int grid = tiles < sms ? tiles : sms;
   long long best = (long long)a.waves * a.steps;
   for (int ks = 2; ks <= kMaxCluster && 2 * ks <= a.steps && a.waves <= 3; ++ks) {
-    const int fit = clusters_of<KIND, HALF, GATED, SHORT>(ks);
+    const int fit = clusters_of<KIND, HALF, GATED, SHORT>(dev, ks);
     if (fit < 1) continue;
     const int waves = tiles / (fit * ks), rest = tiles - waves * fit * ks;
     if (rest == 0 || rest > fit) continue;

@@ -443,8 +443,9 @@ typedef struct {
  *   MOE_I8_ROW        as moe_i8_quantize's of t; scales [T], each times f;
  *   MOE_F8_E4M3_B128  as moe_fp8_quantize's of t with block_rows 1; scales
  *                     [T][ceil(d/128)], each times f.
- * s, t and the sum of squares are f32 (rows with |s| above 1e19 overflow it: f
- * is 0). A row that holds an infinity or a NaN is NaN or 0 throughout; its int8
+ * s, t and the sum of squares are f32. Rows of values up to 6e18 in magnitude,
+ * whatever d, have a finite sum; larger squares may overflow, and f is then 0.
+ * A row that holds an infinity or a NaN is NaN or 0 throughout; its int8
  * scale is NaN and its codes 0. sum_out and out may each be x or residual with
  * the same type and row pitch; nothing else may overlap. Tensors need the
  * alignment of their element; 16-byte aligned rows are read and written in wide

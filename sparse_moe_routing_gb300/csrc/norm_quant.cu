@@ -19,6 +19,10 @@
 // fp32 residual -> int8 60 us, 6.1 TB/s; 14336 x 4096 bf16 quantised 27.5 us, 6.4
 // TB/s), by latency for few (a load, one reduction, a store: 1 x 2048 2.3 us).
 //
+// The squares are summed as they are and, eight at a time, in units of 2^13; a row whose
+// sum overflows takes its mean from the second (a row of 32768 values of 6e18 sums to
+// 2^140). Rows that do not overflow have the first sum's bits.
+//
 // Rows that are not finite: the norm of a row with an infinity or a NaN is NaN
 // there and 0 or NaN elsewhere; an integer row gets the scale NaN and codes 0, an
 // e4m3 block the scale NaN and NaN codes.
@@ -170,6 +174,8 @@ __device__ __forceinline__ uint32_t int8x4(const float* v, float inv) {
 }
 
 constexpr int kFewRows = 8;  // an SM: up to here a row has a CTA, whatever its length
+// 32768 values are 4096 pieces, so that pieces of up to 2^128 sum to 2^127 at most
+constexpr float kSquareUnit = 1.f / 8192.f;
 constexpr float kLeastMax = 127.f * 1.17549435e-38f;  // 127 * 2^-126, an fp32 number
 
 // TX: x's type. RES: 0 no residual, 1 fp32, 2 bf16. NORM: with the factor f (and
@@ -201,7 +207,7 @@ __global__ void __launch_bounds__(max_threads(CH)) rows_kernel(RowsArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) t[c][j] += r[c][j];
   }
-  float sum = 0.f;
+  float sum = 0.f, scaled = 0.f;
   if (NORM) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -210,6 +216,7 @@ __global__ void __launch_bounds__(max_threads(CH)) rows_kernel(RowsArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) q = fmaf(t[c][j], t[c][j], q);
       sum += q;
+      scaled = fmaf(q, kSquareUnit, scaled);
     }
     if (a.gain) {
       float g[CH][8];
@@ -245,7 +252,20 @@ __global__ void __launch_bounds__(max_threads(CH)) rows_kernel(RowsArgs a) {
     mx = __reduce_max_sync(0xffffffffu, wm);
   }
   float f = 1.f;
-  if (NORM) f = 1.f / sqrtf(sum / (float)a.cols + a.eps);
+  if (NORM) {
+    float mean = sum / (float)a.cols;
+    if (__float_as_uint(sum) == 0x7F800000u) {  // (the same in all of the row's threads)
+      scaled = warp_sum(scaled);
+      if (!a.warp_rows) {
+        __syncthreads();  // every warp has read s_sum
+        if (lane == 0) s_sum[warp] = scaled;
+        __syncthreads();
+        scaled = warp_sum(lane < units ? s_sum[lane] : 0.f);
+      }
+      mean = scaled / ((float)a.cols * kSquareUnit);
+    }
+    f = 1.f / sqrtf(mean + a.eps);
+  }
 
   if (NORM && a.out) {
 #pragma unroll

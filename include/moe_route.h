@@ -445,11 +445,13 @@ typedef struct {
  *                     [T][ceil(d/128)], each times f.
  * s, t and the sum of squares are f32. Rows of values up to 6e18 in magnitude,
  * whatever d, have a finite sum; larger squares may overflow, and f is then 0.
- * A row that holds an infinity or a NaN is NaN or 0 throughout; its int8
- * scale is NaN and its codes 0. sum_out and out may each be x or residual with
- * the same type and row pitch; nothing else may overlap. Tensors need the
- * alignment of their element; 16-byte aligned rows are read and written in wide
- * pieces. Deterministic. */
+ * With eps 0, a row whose squares sum to 0 in f32 (zeros, values below 2e-23)
+ * has an infinite f: out is NaN where t is 0 and infinite elsewhere, scales are
+ * infinite, codes those of t. A row that holds an infinity or a NaN is NaN or 0
+ * throughout; its int8 scale is NaN and its codes 0. sum_out and out may each be
+ * x or residual with the same type and row pitch; nothing else may overlap.
+ * Tensors need the alignment of their element; 16-byte aligned rows are read and
+ * written in wide pieces. Deterministic. */
 MOE_API moe_status_t moe_add_rmsnorm(const moe_rmsnorm_t* n, const void* x, const void* residual,
                                      const void* gain, void* sum_out, void* out, void* codes,
                                      float* scales, void* stream);

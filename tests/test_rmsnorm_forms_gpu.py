@@ -38,3 +38,20 @@ def test_every_value_at_the_bound():
         smr.add_rmsnorm(x, out=out, codes=codes, scales=scales)
         check(x[:1], None, None, 1e-6, out[:1], None, codes[:1], scales[:1])
         assert not bool(out[1].any()) and float(scales[1]) == 0.0
+
+
+@pytest.mark.parametrize("T,d", [(4, 96), (3, 4100), (2000, 200)])
+def test_eps_zero_where_nothing_is_left_of_the_squares(T, d):
+    """0 / 0 is NaN: a row of zeros, and one whose squares are below every fp32 number; their neighbours are as ever."""
+    x = torch.randn(T, d, generator=gen(T), device="cuda")
+    x[0] = 0.0
+    x[1] = 2e-23
+    x[1, 3] = 0.0
+    out = torch.empty_like(x)
+    for make in (smr.int8_empty, smr.fp8_empty):
+        codes, scales = make(T, d)
+        smr.add_rmsnorm(x, eps=0.0, out=out, codes=codes, scales=scales)
+        check(x[2:], None, None, 0.0, out[2:], None, codes[2:], scales[2:])
+        assert bool(out[0].isnan().all()) and bool(out[1, 3].isnan()) and int(out[1].isinf().sum()) == d - 1
+        assert bool(scales[:2].isinf().all()) and not bool(codes[0].float().any())
+        assert bool((codes[1].float() > 0).sum() == d - 1)

@@ -467,12 +467,14 @@ MOE_API moe_status_t moe_i8_quantize(const void* x, int32_t x_dtype, int64_t ldx
                                      void* stream);
 
 typedef struct {
-  int32_t M, N, K;       /* M, N >= 0; K 1..131071 */
+  int32_t M, N, K;       /* 0 <= M, N < 2^30; K 1..131071; M K up to 2^40, M N
+                            up to 2^44 (gated 2^43): MOE_ERR_UNSUPPORTED above */
   int32_t out_dtype;     /* MOE_BF16 or MOE_F32 */
   int32_t gated;         /* 0: moe_i8_matmul, 1: moe_i8_gated_matmul */
   int64_t lda, ldb;      /* codes between rows of a and of b (or gate and up):
                             >= K, multiples of 16 */
-  int64_t ldo;           /* values between rows of out: >= N */
+  int64_t ldo;           /* values between rows of out: >= N. Pitches are below
+                            2^40 */
   void* workspace;       /* device scratch, >= moe_i8_matmul_workspace_bytes */
   size_t workspace_bytes;
 } moe_i8_matmul_t;

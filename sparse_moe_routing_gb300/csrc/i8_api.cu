@@ -36,9 +36,10 @@ moe_status_t validate_mm(const moe_i8_matmul_t* m) {
   if (m->K > kI8MaxK) return MOE_ERR_UNSUPPORTED;
   // a tensor map's row pitch is below 2^40 bytes
   if (m->lda >= (1ll << 40) || m->ldb >= (1ll << 40) || m->ldo >= (1ll << 40)) return MOE_ERR_UNSUPPORTED;
-  // the kernels count tiles in 32 bits
-  if (m->N > (1 << 30) || m->M > (1 << 30) ||
-      ((long long)m->M / 16 + 1) * ((long long)m->N / 64 + 1) > (1ll << 24) || (long long)m->M * m->K > (1ll << 40))
+  // the kernels count rows, columns and tiles (of 256 rows where there are more than a
+  // wave: below 2^30) in 32 bits, and the widening launch its pieces
+  if (m->N >= (1 << 30) || m->M >= (1 << 30) || (long long)m->M * m->N > (1ll << (m->gated ? 43 : 44)) ||
+      (long long)m->M * m->K > (1ll << 40))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

@@ -126,6 +126,21 @@ def test_the_structure_names_its_call(L):
     assert L.moe_i8_matmul(*p[:4], ctypes.byref(mm(gated=2)), 0x7000, None) == INVALID
 
 
+@pytest.mark.parametrize("gated", [0, 1])
+def test_sizes_on_each_side_of_the_limits(L, gated):
+    """As the header has them: 2^30 rows or columns, 2^44 values (gated 2^43), 2^40 codes of a."""
+    side = 1 << 22 if not gated else 1 << 21
+    for M, N, K, good in [
+            (131072, 131072, 4096, True), (1048576, 16384, 128, True), (16, (1 << 30) - 1, 64, True),
+            ((1 << 30) - 1, 64, 16, True), ((1 << 30) - 1, 64, 1024, True), ((1 << 30) - 1, 64, 1040, False),
+            (1 << 30, 1, 1, False), (1, 1 << 30, 1, False), (side, 1 << 22, 128, True), (side + 1, 1 << 22, 128, False),
+            (1 << 23, 1, 131071, True), ((1 << 23) + 256, 1, 131071, False)]:
+        p = -(-K // 16) * 16
+        m = mm(M=M, N=N, K=K, gated=gated, lda=p, ldb=p, ldo=N, workspace_bytes=1 << 50)
+        assert (L.moe_i8_matmul_workspace_bytes(ctypes.byref(m)) > 0) == good, (M, N, K)
+        assert call(L, m, (None,) * 7) == (INVALID if good else UNSUPPORTED), (M, N, K)  # (tensors are looked at last)
+
+
 def test_workspace_that_serves_every_number_of_rows(L):
     """What Int8Linear and Int8FeedForward allocate is enough for each product that they run: it grows with the rows
     and with the sums' length and asks for nothing else."""

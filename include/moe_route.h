@@ -459,9 +459,10 @@ MOE_API moe_status_t moe_add_rmsnorm(const moe_rmsnorm_t* n, const void* x, cons
 /* Quantises rows of x (F32 or BF16, the first `cols` of every ldx values) into
  * int8 codes in [-127, 127] and a scale per row: with m = max(max |x|,
  * 127 * 2^-126), code = rint(x * (127 / m)) to nearest even and scale = m / 127,
- * each step in f32 (code * scale is within 0.5000001 scales of x). A row with
- * a value that is not finite gets the scale NaN and codes 0. Codes past a row's
- * last column are not written. cols 1..32768. */
+ * each step in f32 (code * scale is within 0.50003 scales of x: half a step, and
+ * three roundings of a value of up to 127 of them). A row with a value that is
+ * not finite gets the scale NaN and codes 0. Codes past a row's last column are
+ * not written. cols 1..32768. */
 MOE_API moe_status_t moe_i8_quantize(const void* x, int32_t x_dtype, int64_t ldx, int32_t rows,
                                      int32_t cols, void* codes, int64_t ldq, float* scales,
                                      void* stream);

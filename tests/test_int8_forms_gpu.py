@@ -1,4 +1,5 @@
-"""The 8-bit integer products on the GPU where their form matters: very large results."""
+"""The 8-bit integer products on the GPU where their form matters: very large results,
+values next to the quantiser's borders."""
 import pytest
 import torch
 
@@ -27,3 +28,17 @@ def test_results_of_more_than_2_to_the_34_values(M, N):
         for j in range(0, N, cols):
             want = (a[i:i + rows].float() * sa[i:i + rows, None]) @ (b[j:j + cols].float() * sb[j:j + cols, None]).T
             assert torch.equal(out[i:i + rows, j:j + cols], want.to(torch.bfloat16)), (i, j)
+
+
+def test_codes_are_within_the_documented_distance():
+    """Values next to the borders between two codes, where the distance is largest: half a step of the scale and three
+    roundings (127 / m, its product with the value, m / 127) of 2^-24, relative, of up to 127 steps: 0.5 + 2.3e-5."""
+    g = gen(21)
+    m = torch.exp(20 * (torch.rand(400, 1, generator=g, device="cuda") - 0.5))
+    k = torch.randint(100, 127, (400, 2000), generator=g, device="cuda")
+    x = (m.double() * (k + 0.5) / 127).float()
+    x = torch.cat([m, x, torch.nextafter(x, 0 * x), torch.nextafter(x, 2 * m.expand_as(x))], 1)
+    codes, scales = smr.int8_empty(*x.shape)
+    smr.int8_quantize(x, codes, scales)
+    off = ((codes.double() * scales.double()[:, None] - x.double()).abs() / scales.double()[:, None]).max()
+    assert 0.5000001 < float(off) <= 0.50003, float(off)

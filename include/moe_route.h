@@ -507,6 +507,11 @@ MOE_API moe_status_t moe_i8_gated_matmul(const void* a, const float* a_scale, co
 MOE_API size_t moe_i8_matmul_workspace_bytes(const moe_i8_matmul_t* mm);
 MOE_API moe_status_t moe_i8_matmul_init(const moe_i8_matmul_t* mm, void* stream);
 
+/* Measurement aid: the rows of a that a tile of the product takes, which names
+ * the kernel that runs: 16, 32, 64 or 128 in one block, 256 in two blocks of
+ * 128, 0 where up to 8 rows stream b, -1 if mm is invalid. */
+MOE_API int32_t moe_i8_matmul_form(const moe_i8_matmul_t* mm);
+
 #ifdef __cplusplus
 }
 #endif

@@ -21,7 +21,7 @@ __all__ = [
     "inject_stall", "F8_E4M3_B128", "fp8_empty", "fp8_quantize", "fp8_matmul",
     "fp8_matmul_workspace", "fp8_workspace_bytes", "fp8_alloc_workspace", "fp8_experts_forward",
     "fp8_layer_forward", "Fp8Experts", "Fp8Linear", "I8_ROW", "add_rmsnorm", "int8_empty",
-    "int8_quantize", "int8_matmul_workspace", "int8_matmul", "int8_gated_matmul", "Int8Linear",
+    "int8_quantize", "int8_matmul_workspace", "int8_matmul_form", "int8_matmul", "int8_gated_matmul", "Int8Linear",
     "Int8FeedForward",
 ]
 
@@ -116,6 +116,7 @@ _SIGS = {
     "moe_i8_quantize": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _P,
                                        ctypes.c_int64, _P, _P]),
     "moe_i8_matmul_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(_I8Matmul)]),
+    "moe_i8_matmul_form": (ctypes.c_int32, [ctypes.POINTER(_I8Matmul)]),
     "moe_i8_matmul_init": (ctypes.c_int, [ctypes.POINTER(_I8Matmul), _P]),
     "moe_i8_matmul": (ctypes.c_int, [_P] * 4 + [ctypes.POINTER(_I8Matmul), _P, _P]),
     "moe_i8_gated_matmul": (ctypes.c_int, [_P] * 6 + [ctypes.POINTER(_I8Matmul), _P, _P]),
@@ -907,6 +908,14 @@ def int8_matmul_workspace(M, N, K, gated=False, device=None, stream=None):
     _check(lib().moe_i8_matmul_init(ctypes.byref(_i8_args(M, N, K, gated, workspace=ws)), _stream(stream)),
            "moe_i8_matmul_init")
     return ws
+
+
+def int8_matmul_form(M, N, K, gated=False):
+    """moe_i8_matmul_form: the rows of a that a tile of an M x N x K product takes (0: up to 8 rows, without tiles)."""
+    n = lib().moe_i8_matmul_form(ctypes.byref(_i8_args(M, N, K, gated)))
+    if n < 0:
+        raise MoEError(1, "moe_i8_matmul_form")
+    return n
 
 
 def _i8_product(a, a_scale, out, workspace, weights, stream):

@@ -248,6 +248,12 @@ size_t moe_i8_matmul_workspace_bytes(const moe_i8_matmul_t* mm) {
   return validate_mm(mm) == MOE_OK ? mm_plan(*mm).total : 0;
 }
 
+int32_t moe_i8_matmul_form(const moe_i8_matmul_t* mm) {
+  if (validate_mm(mm) != MOE_OK) return -1;
+  const MmPlan p = mm_plan(*mm);
+  return p.kind == kI8Two ? 2 * p.half : p.half;
+}
+
 moe_status_t moe_i8_matmul_init(const moe_i8_matmul_t* mm, void* stream) {
   moe_status_t s = validate_mm(mm);
   if (s != MOE_OK) return s;

@@ -76,3 +76,15 @@ def gated_floor(g64, u64):
     """What a gated result may be off whatever its size: __fdividef(g, y) is 0 for a y = 1 + exp(-g) above 2^126, where the
     quotient is below |g| 2^-126; u multiplies that."""
     return g64.abs() * u64.abs() * 2.0 ** -126
+
+
+# Rows and columns of products, plain and gated, by the rows of a tile that they take for every K of FORM_KS: each kernel
+# that a product can run on, with a few tiles and with several waves of them. K on both sides of 1024, up to which blocks
+# of 128 keep their sums in fp32.
+FORM_KS = [1023, 1024, 1040, 3000]
+FORMS = [(3, 200, 0), (12, 200, 16), (16, 41000, 16), (40, 300, 32), (50, 25000, 64), (100, 30000, 128), (70, 20000, 128),
+         (300, 5120, 256), (300, 20000, 256)]
+# the same where the few tiles are cut along k over clusters: (M, N, K, gated, rows of a tile)
+CUT_FORMS = [(200, 2000, 1024, False, 128), (200, 2000, 10000, True, 128), (200, 2000, 10000, False, 128),
+             (257, 2432, 3000, True, 256), (257, 2432, 4096, True, 256), (300, 5120, 1024, True, 256),
+             (300, 5120, 4096, True, 256), (600, 9740, 1300, False, 256)]

@@ -8,6 +8,7 @@ import torch
 
 import sparse_moe_routing_gb300 as smr
 from sparse_moe_routing_gb300 import build as smr_build
+from int8_util import CUT_FORMS, FORM_KS, FORMS
 
 INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 3
 
@@ -230,3 +231,21 @@ def test_feed_forward_shapes():
         smr.Int8FeedForward(w(64, 32), w(63, 32), w(32, 64), 4)
     with pytest.raises(ValueError, match="W_down has shape"):
         smr.Int8FeedForward(w(64, 32), w(64, 32), w(64, 32), 4)
+
+
+def test_every_kernel_is_among_the_tested_shapes(L):
+    """The shapes that stand for a kernel in the GPU tests run on it: a change of the choice has to bring others."""
+    for M, N, form in FORMS:
+        for K in FORM_KS:
+            for gated in (False, True):
+                assert smr.int8_matmul_form(M, N, K, gated) == form, (M, N, K, gated)
+    for M, N, K, gated, form in CUT_FORMS:
+        assert smr.int8_matmul_form(M, N, K, gated) == form, (M, N, K, gated)
+    assert {f for _, _, f in FORMS} == {0, 16, 32, 64, 128, 256}
+
+
+def test_form_of_nothing(L):
+    assert L.moe_i8_matmul_form(None) == -1 and L.moe_i8_matmul_form(ctypes.byref(mm(K=0))) == -1
+    assert smr.int8_matmul_form(0, 5, 5) == smr.int8_matmul_form(8, 5, 5) == smr.int8_matmul_form(9, 0, 5) == 0
+    with pytest.raises(smr.MoEError):
+        smr.int8_matmul_form(9, 9, 131072)

@@ -1,12 +1,79 @@
-"""The 8-bit integer products on the GPU where their form matters: very large results,
-values next to the quantiser's borders."""
+"""The 8-bit integer products on the GPU where their form matters: sums at the ends of
+what it holds and rows' equality on every kernel, very large results, values next to the quantiser's borders."""
 import pytest
 import torch
 
 import sparse_moe_routing_gb300 as smr
-from test_int8_gpu import gen, random_codes
+from int8_util import (CUT_FORMS, FORM_KS, FORMS, assert_near, gated_floor, gated_room, pitched, random_codes,
+                       random_scales, scaled64, silu64, sums64)
+from test_int8_gpu import gen, product, status
 
 pytestmark = pytest.mark.gpu
+
+
+SHAPES = [(M, N, K) for M, N, _ in FORMS for K in FORM_KS]
+CUT = [c[:4] for c in CUT_FORMS]
+
+
+def codes_at_the_ends(g, M, N, K):
+    """Codes of one sign and nearly all at their ends: sums of up to 2^14 K, odd and even, of either sign."""
+    a = pitched(torch.full((M, K), -128, dtype=torch.int8, device="cuda"))
+    b = pitched(torch.full((N, K), -128, dtype=torch.int8, device="cuda"))
+    a += (torch.rand(M, K, generator=g, device="cuda") < 0.01).to(torch.int8)
+    b += (torch.rand(N, K, generator=g, device="cuda") < 0.003).to(torch.int8)
+    a[0] = b[0] = -128  # and the largest sum itself
+    b[N // 2:] = torch.where(b[N // 2:] == -128, 127, -127).to(torch.int8)
+    return a, b
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES + [c[:3] for c in CUT if not c[3]])
+def test_sums_at_the_ends(M, N, K):
+    """Scales of one: the result is the sum rounded to fp32, and any lost unit of it shows."""
+    g = gen(K + M)
+    a, b = codes_at_the_ends(g, M, N, K)
+    one = torch.ones(max(M, N), device="cuda")
+    got = product(a, one[:M], [(b, one[:N])], torch.float32)
+    want = sums64(a, b)
+    assert float(want[0, 0]) == K * 2.0 ** 14
+    assert torch.equal(got, want.to(torch.float32))
+
+
+@pytest.mark.parametrize("block", [64, 128, 256, 512, 1024])
+@pytest.mark.parametrize("M,N", [(M, N) for M, N, _ in FORMS if N < 10000 or M == 100])
+def test_sums_that_cancel(M, N, block):
+    """Stretches of one sign and of the other in turn, which leave a few units: within a step of 128, between the steps of
+    two issuers, within one accumulator and between its reads."""
+    g = gen(block + M)
+    for K in (1024, 4096):
+        sign = 1 - 2 * ((torch.arange(K, device="cuda") // block) % 2)
+        a = (127 * sign).to(torch.int8).repeat(M, 1).contiguous()
+        b = torch.full((N, K), 127, dtype=torch.int8, device="cuda")
+        b -= (torch.rand(N, K, generator=g, device="cuda") < 0.002).to(torch.int8)
+        one = torch.ones(max(M, N), device="cuda")
+        got = product(a, one[:M], [(b, one[:N])], torch.float32)
+        want = sums64(a, b)
+        if block < K:
+            assert want.abs().max() < 10000
+        assert torch.equal(got, want.to(torch.float32)), K
+
+
+@pytest.mark.parametrize("M,N,K,gated", [(M, N, K, gated) for M, N, K in SHAPES if M > 16 and K != 1023
+                                         for gated in (False, True)] + CUT)
+def test_a_row_is_the_same_on_every_kernel(M, N, K, gated):
+    """Rows of a product against the same rows by themselves, on the kernels for up to 8 and up to 16 rows, bit for bit; a
+    gated result also against its definition."""
+    g = gen(M + N + K)
+    a, sa = random_codes(g, M, K, -128), random_scales(g, M, 0.02)
+    w = [(random_codes(g, N, K, -128), random_scales(g, N, 0.01 / K ** 0.5)) for _ in range(1 + gated)]
+    ws = smr.int8_matmul_workspace(M, N, K, gated=gated)
+    whole = product(a, sa, w, torch.float32, ws)
+    for r0, r1 in ((0, 1), (M // 2, M // 2 + 8), (M - 13, M), (128 % M, min(128 % M + 16, M))):
+        assert torch.equal(product(a[r0:r1], sa[r0:r1], w, torch.float32, ws), whole[r0:r1]), (r0, r1)
+    assert torch.equal(product(a, sa, w, torch.bfloat16, ws), whole.to(torch.bfloat16))
+    if gated:
+        first, second = scaled64(a, sa, *w[0]), scaled64(a, sa, *w[1])
+        assert_near(whole, silu64(first) * second, gated_room(first, torch.float32), gated_floor(first, second))
+    assert status(ws) == (0, 0)
 
 
 @pytest.mark.parametrize("M,N", [(131077, 131073), (16, 2 ** 29 + 77)])

@@ -111,10 +111,12 @@ __device__ __forceinline__ float siluf_(float v) { return __fdividef(v, 1.0f + _
 // must come before the kernel's first global memory access; pdl_trigger()
 // then lets the successor grid be scheduled. Both are no-ops for a plain
 // launch. Every kernel triggers after its own wait only: when a kernel starts,
-// all but its direct predecessor have completed. One kernel relies on that:
-// f8_few_down reads, before it waits, what is older than its direct predecessor,
-// f8_few_gateup, which the same call launches (the ids, the weights and their
-// scales; nothing that gate/up writes).
+// all but its direct predecessor have completed. Two kernels rely on that and
+// read, before they wait, what is older than their direct predecessor, which the
+// same call launches and which writes none of it:
+//  * f8_few_down after f8_few_gateup: the ids, the weights and their scales;
+//  * i8_tc after i8_widen (more than 16 tokens; only its warp of tokens waits):
+//    the weights, their scales and the tokens' scales.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

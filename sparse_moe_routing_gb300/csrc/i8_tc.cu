@@ -317,8 +317,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 0) {
       // --------------------------------------------------------------- weights
-      // (Without kFused before the wait for the kernel before this one: that is the
-      // same call's widening of the tokens, and what is older has completed.)
+      // (Without kFused the weights here and the scales in the epilogue are read before
+      // the wait for the kernel before this one: that is the same call's widening of the
+      // tokens, which writes neither, and what is older has completed.)
       if (lane == 0) {
         Place<P::kW> p;
         bool alive = true;
@@ -736,7 +737,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Rows of codes as fp16, 16 a thread.
+// Rows of codes as fp16, 16 a thread. i8_tc reads weights and scales before it waits for
+// this kernel: its trigger stays behind its own wait, and it writes the widened rows only.
 __global__ void __launch_bounds__(256) i8_widen_kernel(I8WidenArgs a) {
   const int pieces = a.pitch / 16;
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;

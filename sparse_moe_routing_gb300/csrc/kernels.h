@@ -396,7 +396,8 @@ inline cudaError_t ensure_smem_limit(K kernel, int bytes, int* limits) {
 // scheduled (and run their set-up) while the previous kernel on the stream
 // is still finishing. Every kernel of this library calls pdl_wait() before
 // its first global memory access, so only launch latency and set-up overlap
-// (but f8_few_down, which reads before it what its predecessor does not write).
+// (but f8_few_down and i8_tc, which read before it what their predecessors do not
+// write: common.cuh).
 template <typename... P, typename... A>
 inline cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
                               cudaStream_t st, A&&... args) {

@@ -493,7 +493,10 @@ MOE_API moe_status_t moe_i8_matmul(const void* a, const float* a_scale, const vo
                                    void* stream);
 
 /* out [M][N] = SiLU(g) * u, g and u the products of a with gate and with up
- * [N][K] as above, both in f32; ldb is both matrices' pitch. */
+ * [N][K] as above, both in f32; ldb is both matrices' pitch. SiLU takes the fast
+ * exponential and division: an F32 result is within (8 + 2.7 |g|) 2^-23 of its
+ * value, relative, and one whose gate is below -87 may be 0 (BF16 results carry
+ * their own rounding of 2^-8 beside it). */
 MOE_API moe_status_t moe_i8_gated_matmul(const void* a, const float* a_scale, const void* gate,
                                          const float* gate_scale, const void* up,
                                          const float* up_scale, const moe_i8_matmul_t* mm, void* out,

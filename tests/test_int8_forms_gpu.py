@@ -1,5 +1,5 @@
-"""The 8-bit integer products on the GPU where their form matters: sums at the ends of
-what it holds and rows' equality on every kernel, very large results, values next to the quantiser's borders."""
+"""The 8-bit integer products on the GPU where their form matters: sums at the ends of what it holds and rows' equality
+on every kernel, gates far from zero, very large results, values next to the quantiser's borders."""
 import pytest
 import torch
 
@@ -74,6 +74,23 @@ def test_a_row_is_the_same_on_every_kernel(M, N, K, gated):
         first, second = scaled64(a, sa, *w[0]), scaled64(a, sa, *w[1])
         assert_near(whole, silu64(first) * second, gated_room(first, torch.float32), gated_floor(first, second))
     assert status(ws) == (0, 0)
+
+
+@pytest.mark.parametrize("M", [1, 5, 12, 40, 300])
+def test_gates_of_every_size(M):
+    """Gates from -130 to 130 in the documented distance, fp32 results: the fast exponential's error grows with the gate,
+    and below -87 its quotient may be 0."""
+    N, K = 1000, 1
+    steps = torch.arange(N, device="cuda")
+    a = pitched(torch.full((M, K), 127, dtype=torch.int8, device="cuda"))
+    gate = pitched((steps % 255 - 127).to(torch.int8)[:, None])
+    up = pitched(torch.full((N, K), 101, dtype=torch.int8, device="cuda"))
+    sa = torch.linspace(1e-3, 130 / 127, M, device="cuda") if M > 1 else torch.ones(1, device="cuda")
+    sg, su = 1 / 127 * (0.9 + 0.1 * torch.rand(N, generator=gen(M), device="cuda")), torch.ones(N, device="cuda") / 101
+    got = product(a, sa, [(gate, sg), (up, su)], torch.float32)
+    first, second = scaled64(a, sa, gate, sg), scaled64(a, sa, up, su)
+    assert_near(got, silu64(first) * second, (8 + 2.7 * first.abs()) * 2.0 ** -23, gated_floor(first, second))
+    assert float(first.min()) < -100
 
 
 @pytest.mark.parametrize("M,N", [(131077, 131073), (16, 2 ** 29 + 77)])

@@ -451,7 +451,9 @@ typedef struct {
  * throughout; its int8 scale is NaN and its codes 0. sum_out and out may each be
  * x or residual with the same type and row pitch; nothing else may overlap.
  * Tensors need the alignment of their element; 16-byte aligned rows are read and
- * written in wide pieces. Deterministic. */
+ * written in wide pieces. Deterministic; a row's codes and sum_out are the same
+ * whatever T is, out and scales but for their last bits (the order in which the
+ * squares are summed goes by T). */
 MOE_API moe_status_t moe_add_rmsnorm(const moe_rmsnorm_t* n, const void* x, const void* residual,
                                      const void* gain, void* sum_out, void* out, void* codes,
                                      float* scales, void* stream);

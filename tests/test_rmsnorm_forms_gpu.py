@@ -3,8 +3,8 @@ import pytest
 import torch
 
 import sparse_moe_routing_gb300 as smr
-from int8_util import codes32
-from test_rmsnorm_gpu import BF, F, check, gen, rows
+from int8_util import assert_near, codes32
+from test_rmsnorm_gpu import BF, F, ROOM, check, gen, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +128,21 @@ def test_quantize_many_rows(cols, dtype):
         assert torch.equal(codes.cpu(), want)
         good, got = ~s.isnan(), scales.cpu()
         assert int(good.sum()) == T - 2 and torch.equal(got[good], s[good]) and bool(got[~good].isnan().all())
+
+
+@pytest.mark.parametrize("d", [300, 512, 4096, 9000])
+def test_a_rows_codes_and_sum_do_not_depend_on_the_others(d):
+    """Alone or among many, a row's codes and sum are the same bits; its values and scales are near."""
+    T = many()
+    g = gen(d)
+    x, r = rows(g, T, d, BF), rows(g, T, d, F)
+    for make in (smr.int8_empty, smr.fp8_empty):
+        whole, wscales = make(T, d)
+        wsum = torch.empty_like(r)
+        smr.add_rmsnorm(x, r, sum_out=wsum, codes=whole, scales=wscales)
+        for r0, r1 in ((0, 1), (T - 7, T)):
+            codes, scales = make(r1 - r0, d)
+            total = torch.empty_like(r[r0:r1])
+            smr.add_rmsnorm(x[r0:r1], r[r0:r1], sum_out=total, codes=codes, scales=scales)
+            assert torch.equal(codes.float(), whole[r0:r1].float()) and torch.equal(total, wsum[r0:r1])
+            assert_near(scales, wscales[r0:r1].double(), 2 * ROOM)

@@ -126,15 +126,17 @@ moe_status_t product(const void* a, const float* a_scale, const void* b0, const 
   I8TcMaps m{};
   if ((!fused && !i8_make_map(&m.A, ws + p.wide, mm->M, mm->K, p.pitch, p.half)) ||
       !f8_make_map(&m.B0, b0, mm->N, mm->K, mm->ldb, gated ? kTileRows / 2 : kTileRows) ||
-      (gated && !f8_make_map(&m.B1, b1, mm->N, mm->K, mm->ldb, kTileRows / 2)))
-    return MOE_ERR_CUDA;
+      (gated && !f8_make_map(&m.B1, b1, mm->N, mm->K, mm->ldb, kTileRows / 2))) {
+    const cudaError_t e = cudaGetLastError();  // (set where the driver has no encoder)
+    return cuda_status(e != cudaSuccess ? e : cudaErrorInvalidValue);
+  }
   if (!gated) m.B1 = m.B0;  // (not read)
   if (fused) {
     m.A = m.B0;  // (not read)
   } else {
     const I8WidenArgs w{static_cast<const uint8_t*>(a), ws + p.wide, mm->M, mm->K, p.pitch, mm->lda};
     const cudaError_t e = run_kernel(MOE_KERNEL_I8_MATMUL, st, [&] { return launch_i8_widen(w, st); });
-    if (e != cudaSuccess) return MOE_ERR_CUDA;
+    if (e != cudaSuccess) return cuda_status(e);
   }
   I8TcArgs g{};
   g.a = static_cast<const uint8_t*>(a);

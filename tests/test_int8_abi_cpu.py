@@ -1,7 +1,10 @@
 """Refusals of the norm's and of the 8-bit integer calls, on the host, in the C ABI and in the binding: every bad
 argument is answered before anything touches a device. Nothing here launches a kernel."""
 import ctypes
+import os
 import random
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -249,3 +252,21 @@ def test_form_of_nothing(L):
     assert smr.int8_matmul_form(0, 5, 5) == smr.int8_matmul_form(8, 5, 5) == smr.int8_matmul_form(9, 0, 5) == 0
     with pytest.raises(smr.MoEError):
         smr.int8_matmul_form(9, 9, 131072)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="what a machine without a GPU answers")
+@pytest.mark.parametrize("M", [4, 12, 40])
+def test_a_failure_of_cuda_has_a_text(M):
+    """Every kernel's way to MOE_ERR_CUDA leaves the reason behind. (No call before leaves one: this is a child.)"""
+    code = """
+import ctypes, sys
+sys.path[:0] = ["tests"]
+import sparse_moe_routing_gb300 as smr
+from test_int8_abi_cpu import call, mm
+L = smr.lib()
+assert L.moe_last_cuda_error() == b"no error"
+assert call(L, mm(M=%d)) == 4 and L.moe_last_cuda_error() != b"no error", L.moe_last_cuda_error()
+""" % M
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=240, cwd=root)
+    assert r.returncode == 0, r.stderr[-2000:]

@@ -977,8 +977,8 @@ class _Int8Weight:
 
 
 class Int8Linear:
-    """y = x W^T with W [N, K] held in 8-bit integers, for up to max_rows rows: x quantised on the way, or given as
-    (codes, scales), as add_rmsnorm and int8_quantize write them. The quantised x and the workspace belong to the
+    """y = x W^T with W [N, K] held in 8-bit integers (K at most 32768, as the quantiser takes rows), for up to max_rows
+    rows: x quantised on the way, or given as (codes, scales), as add_rmsnorm and int8_quantize write them. The quantised x and the workspace belong to the
     object: calls on several streams are ordered by the caller."""
 
     def __init__(self, weight, max_rows, device=None):
@@ -1009,12 +1009,13 @@ class Int8Linear:
 
 class Int8FeedForward:
     """The dense feed-forward block of a layer without experts, in 8-bit integers: y = W_down h,
-    h = SiLU(W_gate x) * (W_up x), for up to max_rows rows. W_gate, W_up [I, d] and W_down [d, I] float32 or bfloat16.
+    h = SiLU(W_gate x) * (W_up x), for up to max_rows rows. W_gate, W_up [I, d] and W_down [d, I] float32 or bfloat16, d and
+    I at most 32768.
 
     x is quantised on the way, or given as (codes, scales), as add_rmsnorm writes them; h is rounded to bfloat16 and
     then to 8 bits with a scale per row (the bfloat16 rounding is at most 2^-8 of a value, half a step of the codes
-    1/254 of the row's largest; fp32 rows would be twice the traffic). The workspace and what lies between the products belong to the object: calls on several streams
-    are ordered by the caller."""
+    1/254 of the row's largest; fp32 rows would be twice the traffic). The workspace and what lies between the products
+    belong to the object: calls on several streams are ordered by the caller."""
 
     def __init__(self, W_gate, W_up, W_down, max_rows, device=None):
         import torch

@@ -31,13 +31,18 @@
 // scale and store. Gated, the two lanes of a warp that hold a column's gate and
 // its up sums give each other half of them.
 //
-// Bound for few tokens by the weights' stream (5.6 TB/s once it runs; start and end
-// of the kernel are 7 us: 64 x 4096 x 14336 19.5 us, gated 64 x 14336 x 4096 28.9),
+// Bound for few tokens by the weights' stream (5.6 TB/s once it runs, 128 of 152 SMs
+// having a share of 4096 weight rows; start and end of the kernel are 7 us: 64 x 4096 x
+// 14336 19.5 us, gated 64 x 14336 x 4096 28.9-29.4),
 // for many by the hand-overs between widening, issue and read-back: a step's MMAs
 // are 1024 cycles, an issuer's waits, issues and commits some 1100 (8192 x 14336 x
-// 4096 553 us with 18 of widening, 1.74 PFLOP/s; gated 2048 x 14336 x 4096 285-300
-// us, 1.6-1.7; the tensor pipe busy for 75 % of the cycles), and where sums are short
-// by the epilogue's stores (5632 x 8432 x 384 in fp32 50 us, 31 without them).
+// 4096 553-574 us with 18 of widening, 1.68-1.74 PFLOP/s; gated 2048 x 14336 x 4096
+// 285-300 us, 1.6-1.7; the tensor pipe busy for 75 % of the cycles), and where sums are
+// short by the epilogue's stores, 32 columns of a token an instruction (5632 x 8432 x 384
+// in fp32 50 us, 31 without them; 8192 x 14336 x 128 91, floor 35). Between these, 65 to
+// about 1000 tokens, by what a tile is: with one block of tokens a slot of widened weights
+// serves half the MMAs, and a tile is cut over a whole cluster or not at all (512 x 4096
+// x 4096 24.1 us, floor 9.1; 256 x 14336 x 4096 29.6, floor 15.9).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

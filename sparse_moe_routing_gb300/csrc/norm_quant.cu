@@ -16,8 +16,11 @@
 // A row belongs to a group of threads (a warp where it is short and there are
 // many, a CTA else) and stays in its registers: x and the residual are read
 // once, everything is written once. Bound by HBM for many rows (8192 x 4096 bf16 +
-// fp32 residual -> int8 60 us, 6.1 TB/s; 14336 x 4096 bf16 quantised 27.5 us, 6.4
-// TB/s), by latency for few (a load, one reduction, a store: 1 x 2048 2.3 us).
+// fp32 residual -> int8 61 us, 6.0 TB/s, -> e4m3 63; 14336 x 4096 bf16 quantised 27.5
+// us, 6.4 TB/s), by latency for few (a load, one reduction, a store: 1 x 2048 2.2 us).
+// Rows of more than 8192 columns with norm have one CTA an SM, whose barrier nothing
+// covers (4096 x 14336 -> int8 131 us, 0.73 of HBM), and past 16384 spill registers as
+// well (2048 x 28672 136 us; without a residual 68, 0.38).
 //
 // The squares are summed as they are and, eight at a time, in units of 2^13; a row whose
 // sum overflows takes its mean from the second (a row of 32768 values of 6e18 sums to

@@ -93,12 +93,12 @@ def test_gates_of_every_size(M):
     assert float(first.min()) < -100
 
 
-@pytest.mark.parametrize("M,N", [(131077, 131073), (16, 2 ** 29 + 77)])
-def test_results_of_more_than_2_to_the_34_values(M, N):
-    """Tiles and places past what 32 bits of values or bytes hold: every value is the sum, which fp32 holds, times two
-    powers of two."""
+@pytest.mark.parametrize("M,N", [(131077, 131073), (16, 2 ** 29 + 77), (2 ** 30 - 1, 3)])
+def test_the_largest_results(M, N):
+    """More than 2^34 values, and as many rows as there may be: tiles and places past what 32 bits of values or bytes
+    hold. Every value is the sum, which fp32 holds, times two powers of two."""
     K = 16
-    need = M * N * 2 + (M + N) * (K + 8)
+    need = M * N * 2 + (M + N) * (K + 8) + M * K * 2
     if torch.cuda.mem_get_info()[0] < need + (30 << 30):
         pytest.skip("needs %d GB" % ((need >> 30) + 30))
     g = gen(M)
@@ -107,7 +107,7 @@ def test_results_of_more_than_2_to_the_34_values(M, N):
     sb = torch.exp2(torch.randint(-3, 4, (N,), generator=g, device="cuda").float())
     out = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
     smr.int8_matmul(a, sa, b, sb, out, smr.int8_matmul_workspace(M, N, K))
-    rows, cols = (2048, N) if M > 16 else (M, 1 << 24)
+    rows, cols = (max(16, (1 << 28) // N), min(N, 1 << 24))
     for i in range(0, M, rows):
         for j in range(0, N, cols):
             want = (a[i:i + rows].float() * sa[i:i + rows, None]) @ (b[j:j + cols].float() * sb[j:j + cols, None]).T

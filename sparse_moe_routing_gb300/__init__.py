@@ -978,8 +978,8 @@ class _Int8Weight:
 
 class Int8Linear:
     """y = x W^T with W [N, K] held in 8-bit integers (K at most 32768, as the quantiser takes rows), for up to max_rows
-    rows: x quantised on the way, or given as (codes, scales), as add_rmsnorm and int8_quantize write them. The quantised x and the workspace belong to the
-    object: calls on several streams are ordered by the caller."""
+    rows: x quantised on the way, or given as (codes, scales), as add_rmsnorm and int8_quantize write them. The
+    quantised x and the workspace belong to the object: calls on several streams are ordered by the caller."""
 
     def __init__(self, weight, max_rows, device=None):
         if device is not None:
